@@ -314,6 +314,60 @@ PA_API pa_status pa_reshape_and_cache_int8(const void* k_new, const void* v_new,
                                            int32_t num_blocks, int32_t block_size, int32_t Hkv,
                                            int32_t d, pa_dtype dtype, void* stream);
 
+/* 4-bit KV append (the next step of [P4] section 4.3's cache quantisation; the
+ * pages fix no format).  For t in [0, T) with slot = slot_mapping[t] >= 0, every
+ * KV head h and every group of 64 consecutive values x of k_new[t][h][:]
+ * (widened to fp32; every operation rounded to fp32, IEEE division):
+ *   m = f16(min x),  s = f16((max x - min x) / 15)   (RNE, saturating at +-65504)
+ *   c_i = clamp(rint((x_i - m) / s), 0, 15)          (ties to even; 0 where s == 0)
+ * so that a code stands for s c + m.  Two codes share a byte: byte i of a row
+ * holds value 2i in its low and value 2i + 1 in its high four bits.  KV heads lie
+ * outside the rows of a block, so a (block, KV head) tile is one contiguous run;
+ * blocks stay contiguous, so pa_copy_blocks and pa_swap_blocks move them (codes
+ * and scales as pools of their own block sizes).  The same for V.  A negative
+ * slot is padding and is skipped; a slot >= num_blocks * block_size is skipped
+ * and sets PA_DEVERR_SLOT.  Slots must be distinct.  Rows holding NaN or infinity
+ * are outside this contract (their codes and scales are unspecified).
+ *   k_new, v_new     (device) [T][Hkv][d] fp16/bf16 (dtype), d = 64 or 128
+ *   slot_mapping     (device) [T] int64
+ *   k_cache, v_cache (device) [num_blocks][Hkv][block_size][d / 2] uint8 codes,
+ *                    16-byte aligned
+ *   k_scale, v_scale (device) [num_blocks][Hkv][block_size][d / 64][2] f16 {s, m},
+ *                    16-byte aligned for pa_decode_int4 */
+PA_API pa_status pa_reshape_and_cache_int4(const void* k_new, const void* v_new,
+                                           const int64_t* slot_mapping, int32_t T, void* k_cache,
+                                           void* v_cache, void* k_scale, void* v_scale,
+                                           int32_t num_blocks, int32_t block_size, int32_t Hkv,
+                                           int32_t d, pa_dtype dtype, void* stream);
+
+/* Reads tokens of a quantised cache back into 16 bits, the appends' inverse:
+ * for t in [0, T) with slot = slot_mapping[t] >= 0 and every KV head h,
+ * k_out[t][h][:] becomes the values that the row at that slot stands for --
+ *   int4: fl32(s c + m)   int8, fp8: fl32(code scale)
+ * -- rounded once to dtype, and the same for V.  A negative slot leaves its
+ * output row as it is; a slot >= num_blocks * block_size does too and sets
+ * PA_DEVERR_SLOT.  A slot may be read any number of times.  Writing whole
+ * sequences block by block (out row = slot of a scratch pool, -1 behind the last
+ * token) makes a 16-bit paged cache that pa_multi_query / pa_multi_query_tc read,
+ * which is how prompts in chunks and draft tokens run over a quantised cache.
+ *   k_out, v_out     (device) [T][Hkv][d] fp16/bf16 (dtype), 16-byte aligned
+ *   caches, scales   as in the appends (_int8, _fp8: d = 128 only) */
+PA_API pa_status pa_gather_cache_int4(const void* k_cache, const void* v_cache,
+                                      const void* k_scale, const void* v_scale,
+                                      const int64_t* slot_mapping, int32_t T, void* k_out,
+                                      void* v_out, int32_t num_blocks, int32_t block_size,
+                                      int32_t Hkv, int32_t d, pa_dtype dtype, void* stream);
+PA_API pa_status pa_gather_cache_int8(const void* k_cache, const void* v_cache,
+                                      const float* k_scale, const float* v_scale,
+                                      const int64_t* slot_mapping, int32_t T, void* k_out,
+                                      void* v_out, int32_t num_blocks, int32_t block_size,
+                                      int32_t Hkv, int32_t d, pa_dtype dtype, void* stream);
+PA_API pa_status pa_gather_cache_fp8(const void* k_cache, const void* v_cache,
+                                     const float* k_scale, const float* v_scale,
+                                     const int64_t* slot_mapping, int32_t T, void* k_out,
+                                     void* v_out, int32_t num_blocks, int32_t block_size,
+                                     int32_t Hkv, int32_t d, pa_dtype dtype, void* stream);
+
 /* Copy-on-write block copies ([P3] section 3.3): for every layer l and pair p,
  * block pairs[p][1] of k_caches[l] and v_caches[l] becomes a bit copy of
  * block pairs[p][0].  block_bytes = block_size * Hkv * d * element size and
@@ -480,6 +534,99 @@ PA_API pa_status pa_decode_int8(const void* q, const void* k_cache, const void* 
                                 int32_t H, int32_t Hkv, int32_t d, int32_t block_size,
                                 int32_t num_blocks, float scale, pa_dtype dtype, void* out,
                                 void* workspace, size_t ws_bytes, void* stream);
+
+/* pa_decode over a 4-bit cache written by pa_reshape_and_cache_int4: computes
+ * what pa_decode computes with the rows K_j, V_j that the codes stand for (s c + m
+ * per group of 64 values), for d = 64 or 128.  Both products take fp32 sums; a
+ * bf16 q is scaled by a power of two into f16 range first (exact for its elements
+ * down to 2^-25 of its largest).  A table entry outside the pool reads rows of
+ * zeros and sets PA_DEVERR_BLOCK_ID.  Other arguments, the workspace
+ * (pa_decode_workspace_size) and the errors are those of pa_decode.
+ *   q, out           (device) 16-byte aligned
+ *   k_cache, v_cache (device) [num_blocks][Hkv][block_size][d / 2] uint8, 16-byte aligned
+ *   k_scale, v_scale (device) [num_blocks][Hkv][block_size][d / 64][2] f16,
+ *                    16-byte aligned */
+PA_API pa_status pa_decode_int4(const void* q, const void* k_cache, const void* v_cache,
+                                const void* k_scale, const void* v_scale,
+                                const int32_t* block_tables, int32_t max_blocks,
+                                const int32_t* context_lens, int32_t max_context_len, int32_t B,
+                                int32_t H, int32_t Hkv, int32_t d, int32_t block_size,
+                                int32_t num_blocks, float scale, pa_dtype dtype, void* out,
+                                void* workspace, size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Block-sparse decode: a long context's query reads only the blocks whose keys
+ * can score high.  The pages have no counterpart; it is the paged cache's own
+ * unit, the block, that is chosen.  pa_summarize_blocks keeps one box per (block,
+ * KV head), pa_select_blocks ranks a context's blocks by what their boxes promise
+ * and lists the best, pa_decode_selected attends over the lists.
+ * ---------------------------------------------------------------------- */
+
+/* Summarises blocks of a 16-bit cache: for e in [0, n) with b = block_ids[e] and
+ * every KV head h, over the rows r < fill of k_cache[b][r][h][:] (fill =
+ * fills[e], or block_size where fills is NULL),
+ *   lo_c = min_r x_rc,  hi_c = max_r x_rc,  S = fl32(max_c max(|lo_c|, |hi_c|) / 127)
+ *   boxes[b][h][0][c] = clamp(rint(fl32(lo_c / S)), -127, 127)   (ties to even)
+ *   boxes[b][h][1][c] = the same of hi_c;  box_scale[b][h] = S
+ * (IEEE fp32 division); codes are 0 where S == 0, as for fill 0.  A block is
+ * summarised when it has been filled (and again after it was written anew); the
+ * blocks that pa_select_blocks always keeps need no box.  The same id may be
+ * listed more than once if its fill is the same.  An id outside the pool is
+ * skipped and sets PA_DEVERR_BLOCK_ID; a fill outside [0, block_size] is cut to it
+ * and sets PA_DEVERR_CONTEXT.  Rows holding NaN or infinity are outside this
+ * contract.
+ *   k_cache    (device) [num_blocks][block_size][Hkv][d] fp16/bf16 (dtype)
+ *   block_ids  (device) [n] int32;  fills (device, nullable) [n] int32
+ *   boxes      (device) [num_blocks][Hkv][2][d] int8, 16-byte aligned
+ *   box_scale  (device) [num_blocks][Hkv] fp32 */
+PA_API pa_status pa_summarize_blocks(const void* k_cache, const int32_t* block_ids,
+                                     const int32_t* fills, int32_t n, void* boxes,
+                                     float* box_scale, int32_t num_blocks, int32_t block_size,
+                                     int32_t Hkv, int32_t d, pa_dtype dtype, void* stream);
+
+/* Chooses, for each sequence i and KV head g, at most `keep` of the nb =
+ * ceil(context_lens[i] / block_size) blocks of the context: the first `first`,
+ * the last `last`, and of those between the ones with the largest score, ties to
+ * the lower position.  With sq_h = fl32(max |q[i][h]| / 127) and the query codes
+ * c = clamp(rint(fl32(q[i][h] / sq_h)), -127, 127) (0 where sq_h == 0),
+ *   dot_h = sum_c c (c > 0 ? boxes[b][g][1] : boxes[b][g][0])   (an integer)
+ *   score(b) = max over the query heads h of g of fl32(fl32(dot_h sq_h) box_scale[b][g])
+ * sel_blocks[i][g] receives the chosen blocks' physical ids in context order, then
+ * -1; sel_lens[i][g] the tokens they hold (the context's last block is always
+ * chosen and always last, so the lists read like block tables).  nb <= keep
+ * chooses every block and reads no box.  A negative context counts as 0 and sets
+ * PA_DEVERR_CONTEXT, one longer than its table row is cut to it and sets
+ * PA_DEVERR_TABLE_WIDTH; an id outside the pool scores lowest, sets
+ * PA_DEVERR_BLOCK_ID and is passed on if chosen all the same.
+ *   q            (device) [B][H][d] fp16/bf16 (dtype), 16-byte aligned
+ *   keep         >= first + last, first >= 0, last >= 1;  H / Hkv <= 128
+ *   sel_blocks   (device) [B][Hkv][keep] int32;  sel_lens (device) [B][Hkv] int32
+ *   workspace    (device, 4-byte aligned) >= pa_select_blocks_workspace_size(B,
+ *                Hkv, max_blocks) bytes, zeroed once (pa_decode_workspace_init);
+ *                every call leaves its counters at zero.  Calls that overlap on
+ *                the GPU must not share one. */
+PA_API size_t pa_select_blocks_workspace_size(int32_t B, int32_t Hkv, int32_t max_blocks);
+PA_API pa_status pa_select_blocks(const void* q, const void* boxes, const float* box_scale,
+                                  const int32_t* block_tables, int32_t max_blocks,
+                                  const int32_t* context_lens, int32_t B, int32_t H, int32_t Hkv,
+                                  int32_t d, int32_t block_size, int32_t num_blocks, int32_t keep,
+                                  int32_t first, int32_t last, pa_dtype dtype,
+                                  int32_t* sel_blocks, int32_t* sel_lens, void* workspace,
+                                  size_t ws_bytes, void* stream);
+
+/* pa_decode with a block list and a length per (sequence, KV head) instead of per
+ * sequence: query head h of sequence i attends to the first sel_lens[i][h / G]
+ * tokens of the blocks sel_blocks[i][h / G][:].  sel_blocks [B][Hkv][keep] and
+ * sel_lens [B][Hkv] are those of pa_select_blocks (any lists will do); max_sel_len
+ * is an upper bound of sel_lens.  B * Hkv is at most 4096.  Other arguments, the
+ * workspace (pa_decode_workspace_size(B, H, d)) and the errors are those of
+ * pa_decode; a pair of length 0 gives zero rows. */
+PA_API pa_status pa_decode_selected(const void* q, const void* k_cache, const void* v_cache,
+                                    const int32_t* sel_blocks, int32_t keep,
+                                    const int32_t* sel_lens, int32_t max_sel_len, int32_t B,
+                                    int32_t H, int32_t Hkv, int32_t d, int32_t block_size,
+                                    int32_t num_blocks, float scale, pa_dtype dtype, void* out,
+                                    void* workspace, size_t ws_bytes, void* stream);
 
 /* pa_decode without a caller-supplied workspace, for callers that cannot
  * allocate device memory: code running inside an allocator's own hooks, or in

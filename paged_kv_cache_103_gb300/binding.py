@@ -105,6 +105,22 @@ SIGNATURES = {
                                         _ST, _P]),
     "pa_decode_int8": (_ST, [_P, _P, _P, _P, _P, _P, _I32, _P, _I32, _I32, _I32, _I32, _I32, _I32,
                              _I32, ctypes.c_float, _ST, _P, _P, _SZ, _P]),
+    "pa_reshape_and_cache_int4": (_ST, [_P, _P, _P, _I32, _P, _P, _P, _P, _I32, _I32, _I32, _I32,
+                                        _ST, _P]),
+    "pa_gather_cache_int4": (_ST, [_P, _P, _P, _P, _P, _I32, _P, _P, _I32, _I32, _I32, _I32, _ST,
+                                   _P]),
+    "pa_gather_cache_int8": (_ST, [_P, _P, _P, _P, _P, _I32, _P, _P, _I32, _I32, _I32, _I32, _ST,
+                                   _P]),
+    "pa_gather_cache_fp8": (_ST, [_P, _P, _P, _P, _P, _I32, _P, _P, _I32, _I32, _I32, _I32, _ST,
+                                  _P]),
+    "pa_decode_int4": (_ST, [_P, _P, _P, _P, _P, _P, _I32, _P, _I32, _I32, _I32, _I32, _I32, _I32,
+                             _I32, _F32, _ST, _P, _P, _SZ, _P]),
+    "pa_summarize_blocks": (_ST, [_P, _P, _P, _I32, _P, _P, _I32, _I32, _I32, _I32, _ST, _P]),
+    "pa_select_blocks_workspace_size": (_SZ, [_I32, _I32, _I32]),
+    "pa_select_blocks": (_ST, [_P, _P, _P, _P, _I32, _P, _I32, _I32, _I32, _I32, _I32, _I32, _I32,
+                               _I32, _I32, _ST, _P, _P, _P, _SZ, _P]),
+    "pa_decode_selected": (_ST, [_P, _P, _P, _P, _I32, _P, _I32, _I32, _I32, _I32, _I32, _I32,
+                                 _I32, _F32, _ST, _P, _P, _SZ, _P]),
     "pa_decode_noalloc": (_ST, [_P, _P, _P, _P, _I32, _P, _I32, _I32, _I32, _I32, _I32, _I32,
                                 _I32, _F32, _ST, _P, _P]),
     "pa_step_layout_get": (_ST, [ctypes.POINTER(StepDesc), ctypes.POINTER(StepLayout)]),
@@ -376,6 +392,203 @@ def pa_decode_noalloc(q, k_cache, v_cache, block_tables, context_lens, max_conte
                                     Hkv, d, bs, N, float(scale), _dtype_code(q), _dev(out),
                                     _stream_ptr(stream)),
            "pa_decode_noalloc")
+
+
+def _same_device(*tensors):
+    """The library launches on the current device: refuses tensors of another one."""
+    import torch
+    cur = torch.cuda.current_device()
+    for t in tensors:
+        if t.is_cuda and t.device.index != cur:
+            raise ValueError("tensor on %s, but the current device is cuda:%d" % (t.device, cur))
+
+
+def _shape(name, t, shape):
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError("%s must be %s, got %s" % (name, tuple(shape), tuple(t.shape)))
+
+
+def _check_int4_cache(k_cache, v_cache, k_scale, v_scale, Hkv: int, d: int):
+    """(num_blocks, block_size) of a 4-bit cache whose four tensors fit each other."""
+    if k_cache.dim() != 4 or d % 64:
+        raise ValueError("4-bit caches are [num_blocks, Hkv, block_size, d / 2], d a multiple of 64")
+    N, bs = int(k_cache.shape[0]), int(k_cache.shape[2])
+    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
+        _shape(name, t, (N, Hkv, bs, d // 2))
+    for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+        _shape(name, t, (N, Hkv, bs, d // 64, 2))
+    return N, bs
+
+
+def _check_q8_cache(k_cache, v_cache, k_scale, v_scale, Hkv: int, d: int):
+    if k_cache.dim() != 4:
+        raise ValueError("8-bit caches are [num_blocks, block_size, Hkv, d]")
+    N, bs = int(k_cache.shape[0]), int(k_cache.shape[1])
+    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
+        _shape(name, t, (N, bs, Hkv, d))
+    for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+        _shape(name, t, (N, Hkv, bs))
+    return N, bs
+
+
+def pa_reshape_and_cache_int4(k_new, v_new, slot_mapping, k_cache, v_cache, k_scale, v_scale,
+                              stream=None) -> None:
+    """Quantising append into a 4-bit cache: ``k_new/v_new [T, Hkv, d]`` fp16/bf16,
+    ``slot_mapping [T]`` int64 (distinct slots, negative = padding), caches
+    ``[N, Hkv, bs, d / 2]`` uint8 (two codes a byte), scales
+    ``[N, Hkv, bs, d / 64, 2]`` float16 (step and minimum of each group of 64)."""
+    import torch
+    T, Hkv, d = k_new.shape
+    N, bs = _check_int4_cache(k_cache, v_cache, k_scale, v_scale, Hkv, d)
+    _shape("v_new", v_new, k_new.shape)
+    _shape("slot_mapping", slot_mapping, (T,))
+    _same_device(k_new, v_new, slot_mapping, k_cache, v_cache, k_scale, v_scale)
+    _check(load().pa_reshape_and_cache_int4(
+        _dev(k_new), _dev(v_new, k_new.dtype), _dev(slot_mapping, torch.int64), T,
+        _dev(k_cache, torch.uint8), _dev(v_cache, torch.uint8), _dev(k_scale, torch.float16),
+        _dev(v_scale, torch.float16), N, bs, Hkv, d, _dtype_code(k_new), _stream_ptr(stream)),
+        "pa_reshape_and_cache_int4")
+
+
+def pa_gather_cache_int4(k_cache, v_cache, k_scale, v_scale, slot_mapping, k_out, v_out,
+                         stream=None) -> None:
+    """Reads a 4-bit cache back: row ``t`` of ``k_out/v_out [T, Hkv, d]`` (fp16/bf16)
+    becomes the values at ``slot_mapping[t]``; a negative slot leaves its row as it is."""
+    import torch
+    T, Hkv, d = k_out.shape
+    N, bs = _check_int4_cache(k_cache, v_cache, k_scale, v_scale, Hkv, d)
+    _gather("pa_gather_cache_int4", torch.float16, k_cache, v_cache, k_scale, v_scale,
+            slot_mapping, k_out, v_out, N, bs, stream)
+
+
+def pa_gather_cache_int8(k_cache, v_cache, k_scale, v_scale, slot_mapping, k_out, v_out,
+                         stream=None) -> None:
+    """``pa_gather_cache_int4`` for an INT8 cache (``[N, bs, Hkv, 128]`` uint8 codes,
+    ``[N, Hkv, bs]`` float32 scales)."""
+    import torch
+    T, Hkv, d = k_out.shape
+    N, bs = _check_q8_cache(k_cache, v_cache, k_scale, v_scale, Hkv, d)
+    _gather("pa_gather_cache_int8", torch.float32, k_cache, v_cache, k_scale, v_scale,
+            slot_mapping, k_out, v_out, N, bs, stream)
+
+
+def pa_gather_cache_fp8(k_cache, v_cache, k_scale, v_scale, slot_mapping, k_out, v_out,
+                        stream=None) -> None:
+    """``pa_gather_cache_int8`` for a cache of E4M3 codes."""
+    import torch
+    T, Hkv, d = k_out.shape
+    N, bs = _check_q8_cache(k_cache, v_cache, k_scale, v_scale, Hkv, d)
+    _gather("pa_gather_cache_fp8", torch.float32, k_cache, v_cache, k_scale, v_scale,
+            slot_mapping, k_out, v_out, N, bs, stream)
+
+
+def _gather(name, scale_dtype, k_cache, v_cache, k_scale, v_scale, slot_mapping, k_out, v_out, N,
+            bs, stream):
+    import torch
+    T, Hkv, d = k_out.shape
+    _shape("v_out", v_out, k_out.shape)
+    _shape("slot_mapping", slot_mapping, (T,))
+    _same_device(k_cache, v_cache, k_scale, v_scale, slot_mapping, k_out, v_out)
+    _check(getattr(load(), name)(
+        _dev(k_cache, torch.uint8), _dev(v_cache, torch.uint8), _dev(k_scale, scale_dtype),
+        _dev(v_scale, scale_dtype), _dev(slot_mapping, torch.int64), T, _dev(k_out),
+        _dev(v_out, k_out.dtype), N, bs, Hkv, d, _dtype_code(k_out), _stream_ptr(stream)), name)
+
+
+def pa_decode_int4(q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens,
+                   max_context_len: int, scale: float, out, workspace, stream=None) -> None:
+    """``pa_decode`` over a 4-bit cache (from ``pa_reshape_and_cache_int4``):
+    ``q/out [B, H, d]``, caches ``[N, Hkv, bs, d / 2]`` uint8, scales
+    ``[N, Hkv, bs, d / 64, 2]`` float16."""
+    import torch
+    B, H, d = q.shape
+    Hkv = int(k_cache.shape[1])
+    N, bs = _check_int4_cache(k_cache, v_cache, k_scale, v_scale, Hkv, d)
+    _shape("block_tables", block_tables, (B, block_tables.shape[-1]))
+    _shape("context_lens", context_lens, (B,))
+    _shape("out", out, q.shape)
+    _same_device(q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, out, workspace)
+    _check(load().pa_decode_int4(_dev(q), _dev(k_cache, torch.uint8), _dev(v_cache, torch.uint8),
+                                 _dev(k_scale, torch.float16), _dev(v_scale, torch.float16),
+                                 _dev(block_tables, torch.int32), int(block_tables.shape[1]),
+                                 _dev(context_lens, torch.int32), int(max_context_len), B, H, Hkv,
+                                 d, bs, N, float(scale), _dtype_code(q), _dev(out, q.dtype),
+                                 _dev(workspace), workspace.numel() * workspace.element_size(),
+                                 _stream_ptr(stream)),
+           "pa_decode_int4")
+
+
+def pa_summarize_blocks(k_cache, block_ids, boxes, box_scale, fills=None, stream=None) -> None:
+    """Summarises blocks ``block_ids [n]`` (int32) of a 16-bit ``k_cache [N, bs, Hkv, d]``
+    into ``boxes [N, Hkv, 2, d]`` int8 and ``box_scale [N, Hkv]`` float32; ``fills [n]``
+    (int32) gives the rows in use of each (all of them by default)."""
+    import torch
+    N, bs, Hkv, d = k_cache.shape
+    n = int(block_ids.shape[0])
+    _shape("block_ids", block_ids, (n,))
+    _shape("boxes", boxes, (N, Hkv, 2, d))
+    _shape("box_scale", box_scale, (N, Hkv))
+    _same_device(k_cache, block_ids, boxes, box_scale)
+    if fills is not None:
+        _shape("fills", fills, (n,))
+        _same_device(fills)
+    _check(load().pa_summarize_blocks(
+        _dev(k_cache), _dev(block_ids, torch.int32),
+        None if fills is None else _dev(fills, torch.int32), n, _dev(boxes, torch.int8),
+        _dev(box_scale, torch.float32), N, bs, Hkv, d, _dtype_code(k_cache), _stream_ptr(stream)),
+        "pa_summarize_blocks")
+
+
+def pa_select_blocks_workspace_size(B: int, Hkv: int, max_blocks: int) -> int:
+    return int(load().pa_select_blocks_workspace_size(B, Hkv, max_blocks))
+
+
+def pa_select_blocks(q, boxes, box_scale, block_tables, context_lens, block_size: int, first: int,
+                     last: int, sel_blocks, sel_lens, workspace, stream=None) -> None:
+    """Chooses at most ``keep`` blocks per (sequence, KV head) by the scores that ``boxes``
+    promise for ``q [B, H, d]``: ``sel_blocks [B, Hkv, keep]`` and ``sel_lens [B, Hkv]``
+    (int32) receive the lists; the ``first`` and ``last`` blocks of a context are always
+    kept.  ``workspace``: ``pa_select_blocks_workspace_size`` zeroed bytes."""
+    import torch
+    B, H, d = q.shape
+    N, Hkv = int(boxes.shape[0]), int(boxes.shape[1])
+    keep = int(sel_blocks.shape[-1])
+    _shape("boxes", boxes, (N, Hkv, 2, d))
+    _shape("box_scale", box_scale, (N, Hkv))
+    _shape("block_tables", block_tables, (B, block_tables.shape[-1]))
+    _shape("context_lens", context_lens, (B,))
+    _shape("sel_blocks", sel_blocks, (B, Hkv, keep))
+    _shape("sel_lens", sel_lens, (B, Hkv))
+    _same_device(q, boxes, box_scale, block_tables, context_lens, sel_blocks, sel_lens, workspace)
+    _check(load().pa_select_blocks(
+        _dev(q), _dev(boxes, torch.int8), _dev(box_scale, torch.float32),
+        _dev(block_tables, torch.int32), int(block_tables.shape[1]),
+        _dev(context_lens, torch.int32), B, H, Hkv, d, int(block_size), N, keep, int(first),
+        int(last), _dtype_code(q), _dev(sel_blocks, torch.int32), _dev(sel_lens, torch.int32),
+        _dev(workspace), workspace.numel() * workspace.element_size(), _stream_ptr(stream)),
+        "pa_select_blocks")
+
+
+def pa_decode_selected(q, k_cache, v_cache, sel_blocks, sel_lens, max_sel_len: int, scale: float,
+                       out, workspace, stream=None) -> None:
+    """``pa_decode`` over a block list per (sequence, KV head): ``q/out [B, H, d]``, caches
+    ``[N, bs, Hkv, d]``, ``sel_blocks [B, Hkv, keep]`` and ``sel_lens [B, Hkv]`` int32
+    (from ``pa_select_blocks``), ``workspace`` as ``pa_decode``'s."""
+    import torch
+    B, H, d = q.shape
+    N, bs, Hkv, _ = k_cache.shape
+    keep = int(sel_blocks.shape[-1])
+    _shape("k_cache", k_cache, (N, bs, Hkv, d))
+    _shape("v_cache", v_cache, k_cache.shape)
+    _shape("sel_blocks", sel_blocks, (B, Hkv, keep))
+    _shape("sel_lens", sel_lens, (B, Hkv))
+    _shape("out", out, q.shape)
+    _same_device(q, k_cache, v_cache, sel_blocks, sel_lens, out, workspace)
+    _check(load().pa_decode_selected(
+        _dev(q), _dev(k_cache, q.dtype), _dev(v_cache, q.dtype), _dev(sel_blocks, torch.int32),
+        keep, _dev(sel_lens, torch.int32), int(max_sel_len), B, H, Hkv, d, bs, N, float(scale),
+        _dtype_code(q), _dev(out, q.dtype), _dev(workspace),
+        workspace.numel() * workspace.element_size(), _stream_ptr(stream)), "pa_decode_selected")
 
 
 def pa_check_device_errors(stream=None) -> int:

@@ -105,6 +105,7 @@ struct DecodeParams {
     // head g / subs (query heads g * G .. g * G + G - 1 either way).
     int32_t max_blocks, B, H, Hkv, G, bs, num_blocks, stages, subs;
     int32_t len_hint;   // the caller's max_context_len: a guess of every context's length
+    int32_t pair_heads; // kPair: the cache's KV heads (pair i reads KV head i mod pair_heads)
     float scale_log2;
 };
 
@@ -218,7 +219,11 @@ __device__ __forceinline__ void q8x4_to_f16(uint32_t x, uint32_t& lo, uint32_t& 
         pa::e4m3x4_to_f16(x, lo, hi);
 }
 
-template <int D, bool kBF16, int NT, bool kAsync, bool kFp8, bool kInt8>
+// kPair (pa_decode_selected): every (sequence, KV head) pair has a table row and
+// a length of its own.  The kernel sees the pairs as sequences of one KV head
+// each (B Hkv of them, H / Hkv query heads); only the cache's KV head, i mod
+// the real Hkv, differs.
+template <int D, bool kBF16, int NT, bool kAsync, bool kFp8, bool kInt8, bool kPair>
 __global__ void __launch_bounds__(cta_threads(kFp8), kCtasPerSm)
 paged_decode_kernel(const __grid_constant__ CUtensorMap kmap,
                     const __grid_constant__ CUtensorMap vmap,
@@ -284,7 +289,8 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap kmap,
             if (cg < nc && Wg >= 4 * Cg) {
                 const int bpc_g = kChunk >> rows_shift;
                 const int32_t j0 = (cg * kChunk) >> (31 - __clz(bs));
-                const int32_t kvh_g = ((lo_g - g_i * Hkv * nc) / nc) / p.subs;
+                const int32_t kvh_g = kPair ? g_i % p.pair_heads
+                                            : ((lo_g - g_i * Hkv * nc) / nc) / p.subs;
                 for (int b = 0; b < bpc_g; ++b) {
                     const int32_t e = __shfl_sync(0xffffffffu, g_went, (j0 - g_wbase + b) & 31);
                     if (lane == 0 && e >= 0 && e < p.num_blocks) {
@@ -391,7 +397,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap kmap,
         auto open = [&](int32_t at) {
             Walk w;
             w.s = find_segment(prefix, B, Hkv, at, hi);
-            w.kvh = w.s.g / p.subs;
+            w.kvh = kPair ? w.s.i % p.pair_heads : w.s.g / p.subs;
             w.n_raw = __ldg(p.context_lens + w.s.i);
             w.trow = p.block_tables + (int64_t)w.s.i * p.max_blocks;
             w.wbase = (w.s.c0 * kChunk) >> bs_shift;
@@ -1222,11 +1228,11 @@ int choose_stages(int D, int G, int B, bool fp8, int bs) {
     return s;
 }
 
-template <int D, bool kBF16, int NT, bool kAsync, bool kFp8, bool kInt8>
+template <int D, bool kBF16, int NT, bool kAsync, bool kFp8, bool kInt8, bool kPair>
 pa_status launch(const CUtensorMap& km, const CUtensorMap& vm, const CUtensorMap& ksm,
                  const CUtensorMap& vsm, const DecodeParams& prm, size_t smem,
                  cudaStream_t stream) {
-    auto kern = paged_decode_kernel<D, kBF16, NT, kAsync, kFp8, kInt8>;
+    auto kern = paged_decode_kernel<D, kBF16, NT, kAsync, kFp8, kInt8, kPair>;
     static std::once_flag once;
     static cudaError_t attr_err = cudaSuccess;
     static int regs = 0;
@@ -1245,15 +1251,15 @@ pa_status launch(const CUtensorMap& km, const CUtensorMap& vm, const CUtensorMap
     return pa::cuda_status(cudaGetLastError());
 }
 
-template <int D, bool kBF16, bool kFp8, bool kInt8 = false>
+template <int D, bool kBF16, bool kFp8, bool kInt8 = false, bool kPair = false>
 pa_status launch_g(const CUtensorMap& km, const CUtensorMap& vm, const CUtensorMap& ksm,
                    const CUtensorMap& vsm, const DecodeParams& prm, size_t smem,
                    cudaStream_t stream) {
     if (async_merge(prm.G))
-        return launch<D, kBF16, 1, true, kFp8, kInt8>(km, vm, ksm, vsm, prm, smem, stream);
+        return launch<D, kBF16, 1, true, kFp8, kInt8, kPair>(km, vm, ksm, vsm, prm, smem, stream);
     return prm.G <= 8
-               ? launch<D, kBF16, 1, false, kFp8, kInt8>(km, vm, ksm, vsm, prm, smem, stream)
-               : launch<D, kBF16, 2, false, kFp8, kInt8>(km, vm, ksm, vsm, prm, smem, stream);
+               ? launch<D, kBF16, 1, false, kFp8, kInt8, kPair>(km, vm, ksm, vsm, prm, smem, stream)
+               : launch<D, kBF16, 2, false, kFp8, kInt8, kPair>(km, vm, ksm, vsm, prm, smem, stream);
 }
 
 // Checks shared by pa_decode and pa_decode_fp8; fills everything of prm but the
@@ -1294,6 +1300,7 @@ pa_status prepare(int32_t max_blocks, int32_t max_context_len, int32_t B, int32_
     prm->num_blocks = num_blocks;
     prm->stages = stages;
     prm->len_hint = max_context_len;
+    prm->pair_heads = 0;
     prm->scale_log2 = scale * kLog2e;
     *smem = make_layout(d, G, B, stages, async_merge(G) ? 2 : 1, fp8, block_size).total;
     return PA_OK;
@@ -1436,6 +1443,61 @@ PA_API pa_status pa_decode_int8(const void* q, const void* k_cache, const void* 
     return decode_q8<true>(q, k_cache, v_cache, k_scale, v_scale, block_tables, max_blocks,
                            context_lens, max_context_len, B, H, Hkv, d, block_size, num_blocks,
                            scale, dtype, out, workspace, ws_bytes, stream);
+}
+
+}  // extern "C"
+
+extern "C" {
+
+PA_API pa_status pa_decode_selected(const void* q, const void* k_cache, const void* v_cache,
+                                    const int32_t* sel_blocks, int32_t keep,
+                                    const int32_t* sel_lens, int32_t max_sel_len, int32_t B,
+                                    int32_t H, int32_t Hkv, int32_t d, int32_t block_size,
+                                    int32_t num_blocks, float scale, pa_dtype dtype, void* out,
+                                    void* workspace, size_t ws_bytes, void* stream) {
+    if (B < 0 || H <= 0 || Hkv <= 0) return PA_ERR_INVALID;
+    if (H % Hkv != 0 || (int64_t)B * Hkv > kMaxBatch) return PA_ERR_UNSUPPORTED;
+    DecodeParams prm;
+    size_t smem = 0;
+    // The pairs as B * Hkv sequences of one KV head; the workspace is the same
+    // size either way (a counter per (sequence, query head)).
+    const pa_status st0 = prepare(keep, max_sel_len, B * Hkv, H / Hkv, 1, d, block_size,
+                                  num_blocks, scale, dtype, ws_bytes, false, &prm, &smem);
+    if (st0 != PA_OK || B == 0) return st0;
+    if (!q || !k_cache || !v_cache || !sel_blocks || !sel_lens || !out || !workspace)
+        return PA_ERR_INVALID;
+    if ((reinterpret_cast<uintptr_t>(k_cache) | reinterpret_cast<uintptr_t>(v_cache)) & 15u)
+        return PA_ERR_INVALID;
+    if ((reinterpret_cast<uintptr_t>(q) & 3u) || (reinterpret_cast<uintptr_t>(out) & 15u))
+        return PA_ERR_INVALID;
+
+    unsigned int* err = pa::device_error_word();
+    if (!err || pa_decode_grid_size() <= 0) return PA_ERR_CUDA;
+
+    CUtensorMap km, vm;
+    const int32_t rows = num_blocks * block_size;
+    if (!encode_cache_map(&km, k_cache, rows, Hkv, d, block_size, dtype) ||
+        !encode_cache_map(&vm, v_cache, rows, Hkv, d, block_size, dtype))
+        return PA_ERR_CUDA;
+
+    prm.pair_heads = Hkv;
+    prm.q = static_cast<const uint16_t*>(q);
+    prm.out = static_cast<uint16_t*>(out);
+    prm.block_tables = sel_blocks;
+    prm.context_lens = sel_lens;
+    prm.counters = static_cast<int32_t*>(workspace);
+    prm.partials = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) +
+                                            counters_bytes(B, H));
+    prm.err = err;
+
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (d == 128)
+        return dtype == PA_BF16
+                   ? launch_g<128, true, false, false, true>(km, vm, km, vm, prm, smem, st)
+                   : launch_g<128, false, false, false, true>(km, vm, km, vm, prm, smem, st);
+    return dtype == PA_BF16
+               ? launch_g<64, true, false, false, true>(km, vm, km, vm, prm, smem, st)
+               : launch_g<64, false, false, false, true>(km, vm, km, vm, prm, smem, st);
 }
 
 }  // extern "C"
