@@ -114,6 +114,17 @@ __device__ __forceinline__ void tma_prefetch_3d(const CUtensorMap* map, int32_t 
                  : "memory");
 }
 
+// Copies `bytes` contiguous bytes global -> shared (addresses and size multiples
+// of 16), counted on `bar`.
+__device__ __forceinline__ void bulk_load(uint32_t smem_dst, const void* src, uint32_t bytes,
+                                          uint32_t bar, uint64_t l2_policy) {
+    asm volatile(
+        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint "
+        "[%0], [%1], %2, [%3], %4;" ::"r"(smem_dst),
+        "l"(src), "r"(bytes), "r"(bar), "l"(l2_policy)
+        : "memory");
+}
+
 // Transposes an 8x8 matrix of 16-bit values held across the warp in the
 // ldmatrix fragment layout (lane l: row l/4, columns 2(l%4), 2(l%4)+1).
 __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t x) {
