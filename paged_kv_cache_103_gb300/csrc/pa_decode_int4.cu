@@ -42,18 +42,13 @@
 
 namespace {
 
-constexpr int kWarps = 8;
-constexpr int kThreads = kWarps * 32;
+constexpr int kMaxWarps = 8;            // per CTA
 constexpr int kChunk = 32;              // tokens per stage
 constexpr int kTiles = kChunk / 16;     // 16-key MMA tiles per chunk
 constexpr int kMaxG = 16;
 constexpr int kMaxBatch = 4096;
 constexpr int kMaxCtas = 512;
-constexpr int kMaxStages = 8;
-// A CTA in use has at least one chunk per warp: smaller batches take fewer CTAs
-// rather than more partial results.
-constexpr int kMinChunksPerCta = kWarps;
-constexpr uint64_t kWaitLimitNs = 1ull << 30;   // about one second
+constexpr int kMaxStages = 5;
 constexpr float kLog2e = 1.4426950408889634f;
 
 struct Int4Params {
@@ -66,7 +61,7 @@ struct Int4Params {
     float* partials;     // [2 * CTAs][2 * kMaxG + kMaxG * D]
     unsigned int* err;
     // A KV head with more than kMaxG query heads is `subs` pairs of kMaxG heads.
-    int32_t max_blocks, B, H, Hkv, G, bs_shift, num_blocks, stages, subs;
+    int32_t max_blocks, B, H, Hkv, G, bs_shift, num_blocks, stages, subs, warps;
     float scale_log2;
 };
 
@@ -86,18 +81,19 @@ struct Run {
 };
 
 struct Layout {
-    uint32_t stage, slots, runs, bars, open, scan, prefix, total;
+    uint32_t stage, rows, slots, runs, open, scan, prefix, total;
 };
 
-__host__ __device__ inline Layout make_layout(int D, int G, int B, int stages) {
+__host__ __device__ inline Layout make_layout(int D, int G, int B, int warps,
+                                              int stages) {
     Layout L;
     L.stage = 2u * kChunk * (D / 2 + D / 64 * 4);            // K, V codes, K, V scales
-    L.slots = kWarps * stages * L.stage;                     // a slot per warp
-    L.runs = L.slots + kWarps * slot_floats(G, D) * 4;       // [2 * kWarps]
-    L.bars = L.runs + 2 * kWarps * (uint32_t)sizeof(Run);    // [kWarps][stages]
-    L.open = L.bars + kWarps * kMaxStages * 8;               // runs left to other CTAs
+    L.rows = warps * stages * L.stage;                      // per warp: K and V of 32 rows
+    L.slots = L.rows + warps * 2 * kChunk * (D / 64) * 8;   // a slot per warp
+    L.runs = L.slots + warps * slot_floats(G, D) * 4;       // [2 * warps]
+    L.open = L.runs + 2 * warps * (uint32_t)sizeof(Run);     // runs left to other CTAs
     L.scan = L.open + 16;
-    L.prefix = L.scan + kWarps * 4;                          // [B + 1]
+    L.prefix = L.scan + warps * 4;                          // [B + 1]
     L.total = L.prefix + (uint32_t)(B + 1) * 4;
     return L;
 }
@@ -106,10 +102,17 @@ __device__ __forceinline__ int32_t clamp_len(int32_t n, int32_t cap) {
     return n < 0 ? 0 : (n > cap ? cap : n);
 }
 
-// First chunk of part x when W chunks are cut into n parts.
-__device__ __forceinline__ int32_t share(int64_t x, int64_t W, int64_t n) {
-    return (int32_t)(x * W / n);
-}
+// W chunks cut into n parts, the first W % n of them one chunk longer.
+struct Cut {
+    int32_t q, r;
+    __device__ Cut(int32_t W, int32_t n) : q(W / n), r(W - W / n * n) {}
+    __device__ int32_t begin(int32_t x) const { return x * q + min(x, r); }
+    // the part that holds chunk c
+    __device__ int32_t part(int32_t c) const {
+        const int32_t big = r * (q + 1);
+        return c < big ? c / (q + 1) : r + (c - big) / q;
+    }
+};
 
 // A position in the flattened list: chunk c of pair (i, g), whose nc chunks start at a.
 struct Cursor {
@@ -144,6 +147,22 @@ __device__ __forceinline__ Cursor next_pair(const int32_t* prefix, int32_t Hkv, 
     return s;
 }
 
+// 16 bytes global -> shared, asynchronously; zeros and no read unless ok.
+__device__ __forceinline__ void copy16(uint32_t to, const void* from, bool ok, uint64_t policy) {
+    asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2, %3;" ::"r"(to), "l"(from),
+                 "r"(ok ? 16 : 0), "l"(policy) : "memory");
+}
+__device__ __forceinline__ void commit_group() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// Waits until at most S - 1 of this thread's groups are in flight.
+__device__ __forceinline__ void wait_group(int S) {
+    switch (S) {
+        case 2: asm volatile("cp.async.wait_group 1;" ::: "memory"); break;
+        case 3: asm volatile("cp.async.wait_group 2;" ::: "memory"); break;
+        case 4: asm volatile("cp.async.wait_group 3;" ::: "memory"); break;
+        default: asm volatile("cp.async.wait_group 4;" ::: "memory"); break;
+    }
+}
+
 __device__ __forceinline__ uint32_t lds32(uint32_t addr) {
     uint32_t v;
     asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr));
@@ -164,35 +183,67 @@ __device__ __forceinline__ float2 widen2(uint32_t v) {
         return half2_floats(v);
 }
 
-// (step, minimum) of the NG groups of one row.
+// (step, minimum) of the NG groups of one row, as they lie in the cache (f16) and as
+// the rows' scratch holds them (fp32).
 template <int NG>
-__device__ __forceinline__ void load_scales(uint32_t addr, float (&s)[NG], float (&m)[NG]) {
+__device__ __forceinline__ void load_f16_scales(uint32_t addr, float (&v)[2 * NG]) {
     uint32_t w[NG];
     if constexpr (NG == 2) {
-        const uint2 v = pa::lds64(addr);
-        w[0] = v.x;
-        w[1] = v.y;
+        const uint2 x = pa::lds64(addr);
+        w[0] = x.x;
+        w[1] = x.y;
     } else {
         w[0] = lds32(addr);
     }
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
         const float2 f = half2_floats(w[g]);
-        s[g] = f.x;
-        m[g] = f.y;
+        v[2 * g] = f.x;
+        v[2 * g + 1] = f.y;
     }
+}
+template <int NG>
+__device__ __forceinline__ void load_row(uint32_t addr, float (&v)[2 * NG]) {
+    if constexpr (NG == 2) {
+        const uint4 x = pa::lds128(addr);
+        v[0] = __uint_as_float(x.x);
+        v[1] = __uint_as_float(x.y);
+        v[2] = __uint_as_float(x.z);
+        v[3] = __uint_as_float(x.w);
+    } else {
+        const uint2 x = pa::lds64(addr);
+        v[0] = __uint_as_float(x.x);
+        v[1] = __uint_as_float(x.y);
+    }
+}
+template <int NG>
+__device__ __forceinline__ void store_row(uint32_t addr, const float (&v)[2 * NG]) {
+    if constexpr (NG == 2)
+        asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(v[0]), "f"(v[1]),
+                     "f"(v[2]), "f"(v[3]) : "memory");
+    else
+        asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(addr), "f"(v[0]), "f"(v[1]) : "memory");
 }
 
 constexpr uint32_t kLowNibbles = 0x000F000Fu;    // c 2^-24 each
 constexpr uint32_t kHighNibbles = 0x00F000F0u;   // c 2^-20 each
 
-template <int D, bool kBF16, int NT>
-__global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) decode_int4_kernel(const Int4Params p) {
-    constexpr int NG = D / 64;
+// A head's running maximum is raised only when a logit exceeds it by more than this
+// (base 2): probabilities reach 2^8, which fp32 sums and the f16 range of P bear, and
+// most chunks need neither the maximum across lanes nor a rescale.
+constexpr float kLazy = 8.f;
+
+// kOne: one query head per KV head; a lane then tracks one column instead of two.
+template <int D, bool kBF16, int NT, bool kOne, int kShift>
+__global__ void __launch_bounds__(kMaxWarps * 32, ctas_per_sm(NT)) decode_int4_kernel(const Int4Params p) {
+    constexpr int NG = D / 64, NJ = kOne ? 1 : 2;
     constexpr uint32_t kRow = D / 2, kSRow = NG * 4;         // bytes of a row's codes and scales
     constexpr uint32_t kCodes = kChunk * kRow, kScales = kChunk * kSRow;
-    const int32_t B = p.B, Hkv = p.Hkv, G = p.G, S = p.stages, bs_shift = p.bs_shift;
-    const Layout L = make_layout(D, G, B, S);
+    constexpr uint32_t kStage = 2 * (kCodes + kScales);   // K, V codes, K, V scales
+    const int32_t B = p.B, Hkv = p.Hkv, G = p.G, S = p.stages;
+    constexpr int bs_shift = kShift, bmask = (1 << kShift) - 1;
+    const int nw = p.warps, threads = nw * 32;
+    const Layout L = make_layout(D, G, B, nw, S);
     extern __shared__ __align__(128) unsigned char smem[];
     const uint32_t sbase = pa::smem_addr(smem);
     Run* runs = reinterpret_cast<Run*>(smem + L.runs);
@@ -204,7 +255,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) decode_int4_kernel(
 
     // ---- prefix[i] = Hkv * chunks of the sequences before i
     {
-        const int per = (B + kThreads - 1) / kThreads;
+        const int per = (B + threads - 1) / threads;
         const int beg = min(tid * per, B), end = min(beg + per, B);
         int32_t local = 0;
         for (int i = beg; i < end; ++i) {
@@ -222,13 +273,8 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) decode_int4_kernel(
             if (lane >= o) x += y;
         }
         if (lane == 31) scan[warp] = x;
-        if (tid < 2 * kWarps) runs[tid].a = -1;
+        if (tid < 2 * nw) runs[tid].a = -1;
         if (tid < 2) open_run[tid] = -1;
-        if (lane == 0) {
-            for (int s = 0; s < S; ++s)
-                pa::mbar_init(reinterpret_cast<uint64_t*>(smem + L.bars) + warp * S + s, 1);
-            pa::fence_barrier_init();
-        }
         __syncthreads();
         int32_t run = x - local;
         for (int w = 0; w < warp; ++w) run += scan[w];
@@ -238,7 +284,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) decode_int4_kernel(
         }
         if (tid == 0) {
             int32_t total = 0;
-            for (int w = 0; w < kWarps; ++w) total += scan[w];
+            for (int w = 0; w < nw; ++w) total += scan[w];
             prefix[B] = total * Hkv;
         }
         __syncthreads();
@@ -248,95 +294,123 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) decode_int4_kernel(
     for (int32_t i = blockIdx.x; i < B; i += gridDim.x) {
         if (prefix[i + 1] != prefix[i]) continue;
         uint4* row = reinterpret_cast<uint4*>(p.out + (int64_t)i * p.H * D);
-        for (int v = tid; v < p.H * D / 8; v += kThreads) row[v] = make_uint4(0, 0, 0, 0);
+        for (int v = tid; v < p.H * D / 8; v += threads) row[v] = make_uint4(0, 0, 0, 0);
     }
 
-    const int64_t W = prefix[B];
-    int64_t C = (W + kMinChunksPerCta - 1) / kMinChunksPerCta;
-    if (C > (int64_t)gridDim.x) C = gridDim.x;
-    if ((int64_t)blockIdx.x >= C) return;
-    const int32_t cta_lo = share(blockIdx.x, W, C), cta_hi = share(blockIdx.x + 1, W, C);
-    const int32_t lo = cta_lo + share(warp, cta_hi - cta_lo, kWarps);
-    const int32_t hi = cta_lo + share(warp + 1, cta_hi - cta_lo, kWarps);
+    const int32_t W = prefix[B];
+    // CTAs in use have a chunk per warp at least: smaller batches take fewer CTAs
+    // rather than more partial results.
+    const int32_t C = min((W + nw - 1) / nw, (int32_t)gridDim.x);
+    if ((int32_t)blockIdx.x >= C) return;
+    const Cut cut(W, C);
+    const int32_t cta_lo = cut.begin(blockIdx.x), cta_hi = cut.begin(blockIdx.x + 1);
+    const Cut mine(cta_hi - cta_lo, nw);
+    const int32_t lo = cta_lo + mine.begin(warp), hi = cta_lo + mine.begin(warp + 1);
 
-    const uint32_t ring = sbase + (uint32_t)warp * S * L.stage;
-    const uint32_t bars = sbase + L.bars + (uint32_t)(warp * S) * 8;
-    uint64_t* bars_p = reinterpret_cast<uint64_t*>(smem + L.bars) + warp * S;
-    bool dead = false;
+    const uint32_t ring = sbase + (uint32_t)warp * S * kStage;
+    const uint32_t krows = sbase + L.rows + (uint32_t)warp * (2 * kChunk * NG * 8);
+    const uint32_t vrows = krows + kChunk * NG * 8;
 
     if (lo < hi) {
         // ================= loading: this warp's chunks, in order =================
-        // Lane 4 b + w issues copy w (K codes, V codes, K scales, V scales) of the
-        // chunk's block b.
-        const int which = lane & 3;
-        const int bpc = kChunk >> bs_shift;     // blocks per chunk: 4, 2 or 1
-        const uint8_t* src = which == 0 ? p.k_cache : which == 1 ? p.v_cache
-                                        : which == 2 ? p.k_scale : p.v_scale;
-        const uint32_t unit = (which < 2 ? kRow : kSRow) << bs_shift;   // bytes of a tile
-        const uint32_t dst = (which == 0 ? 0 : which == 1 ? kCodes
-                              : which == 2 ? 2 * kCodes : 2 * kCodes + kScales) +
-                             (uint32_t)(lane >> 2) * unit;
-        const uint32_t block_bytes = (2 * (kRow + kSRow)) << bs_shift;
+        // A copy instruction moves 512 bytes: kPass rows of codes.  The lane's row and
+        // 16-byte column in a pass, and in the chunk's scales (K's by the lower lanes,
+        // V's by the upper ones).
+        constexpr int kPass = 512 / kRow, kScaleLanes = kScales / 16;
+        const int lrow = lane / (kRow / 16), srow = lane % kScaleLanes * (16 / kSRow);
+        const uint32_t lcol = lane % (kRow / 16) * 16;
+        constexpr uint32_t kTile = kRow << bs_shift, kSTile = kSRow << bs_shift;
+        const uint32_t heads = (uint32_t)(Hkv / p.subs);
         const uint64_t policy = pa::l2_policy_evict_first();
-        const int32_t real_heads = Hkv / p.subs;
-        // A pair's table entries, 32 at a time (lane l holds entry wbase + l), with
+        const int64_t k_to_v = p.v_cache - p.k_cache;
+        const uint8_t* scales = lane < kScaleLanes ? p.k_scale : p.v_scale;
+        constexpr int bpc = kChunk >> bs_shift;     // blocks per chunk: 4, 2 or 1
+        // A pair's table entries, 32 at a time (lane l holds the window's entry l), with
         // the window after it and the next pair's first one loaded a step ahead.
         struct Walk {
             Cursor s;
-            int32_t n, wbase, went, wnext;
-            const int32_t* row;
+            uint32_t head;           // the cache's KV head
+            int32_t at, left;        // first block of the chunk: in the window, and how many follow
+            int32_t went, wnext;
+            const int32_t* next;     // this lane's entry of the window after wnext
         };
         auto open = [&](const Cursor& s) {
             Walk w;
             w.s = s;
-            w.n = __ldg(p.context_lens + s.i);
-            w.row = p.block_tables + (int64_t)s.i * p.max_blocks;
-            w.wbase = (s.c * kChunk) >> bs_shift;
-            const int32_t j = w.wbase + lane;
-            w.went = j < p.max_blocks ? __ldg(w.row + j) : -1;
-            w.wnext = j + 32 < p.max_blocks ? __ldg(w.row + j + 32) : -1;
+            const int32_t j0 = (s.c * kChunk) >> bs_shift, j = j0 + lane;
+            const int32_t* row = p.block_tables + (int64_t)s.i * p.max_blocks + j;
+            const int32_t n = clamp_len(__ldg(p.context_lens + s.i), max_len);
+            w.head = (uint32_t)(s.g / p.subs);
+            w.at = 0;
+            w.left = ((n + bmask) >> bs_shift) - j0;
+            w.went = j < p.max_blocks ? __ldg(row) : -1;
+            w.wnext = j + 32 < p.max_blocks ? __ldg(row + 32) : -1;
+            w.next = row + 64;
             return w;
         };
         int32_t ipos = lo;              // next chunk to issue
-        int istage = 0;
+        uint32_t ito = ring;            // its stage
         Walk cur = open(find(prefix, B, Hkv, lo)), nxt = cur;
         const Cursor start = cur.s;
         if (start.a + start.nc < hi) nxt = open(next_pair(prefix, Hkv, start));
+        // One chunk's copies, as one group.  Blocks past the context and ids outside the
+        // pool are not read: zeros take their place (a step and a minimum of zero: rows of
+        // zeros).
         auto issue = [&]() {
-            const int32_t j0 = (cur.s.c * kChunk) >> bs_shift;
-            if (j0 + bpc > cur.wbase + 32) {
-                cur.wbase += 32;
-                cur.went = cur.wnext;
-                const int32_t j = cur.wbase + 32 + lane;
-                cur.wnext = j < p.max_blocks ? __ldg(cur.row + j) : -1;
-            }
-            const int32_t b = lane >> 2;
-            const int32_t blk = __shfl_sync(0xffffffffu, cur.went, (j0 - cur.wbase + b) & 31);
-            const int32_t nb = (clamp_len(cur.n, max_len) + (1 << bs_shift) - 1) >> bs_shift;
-            const bool want = b < bpc && j0 + b < nb;
-            const bool ok = want && blk >= 0 && blk < p.num_blocks;
-            const uint32_t good = __ballot_sync(0xffffffffu, ok && which == 0);
-            const uint32_t to = ring + (uint32_t)istage * L.stage + dst;
-            if (__any_sync(0xffffffffu, want && !ok)) {
-                // A block outside the pool stands for rows of zeros: steps and
-                // minima of zero (its stale codes are finite).
-                if (want && !ok && which >= 2) {
-                    if (which == 2) pa::raise_error(p.err, PA_DEVERR_BLOCK_ID);
-                    for (uint32_t x = 0; x < unit; x += 16)
-                        asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(to + x), "r"(0)
-                                     : "memory");
+            bool bad = false;
+            // tile index of the lane's row of pass or scales; b: the row's block in the chunk
+            auto tile_of = [&](int b, bool& ok) {
+                const int32_t blk = __shfl_sync(0xffffffffu, cur.went, cur.at + b);
+                ok = b < cur.left && (uint32_t)blk < (uint32_t)p.num_blocks;
+                bad |= b < cur.left && !ok;
+                return (uint64_t)((ok ? (uint32_t)blk : 0u) * heads + cur.head);
+            };
+            if constexpr (kPass <= bmask + 1) {   // a pass lies in one block
+                constexpr int kPasses = (bmask + 1) / kPass < kChunk / kPass ? (bmask + 1) / kPass : kChunk / kPass;
+#pragma unroll
+                for (int b = 0; b < bpc; ++b) {
+                    bool ok;
+                    const uint8_t* from = p.k_cache + tile_of(b, ok) * kTile + lane * 16;
+                    const uint8_t* vfrom = from + k_to_v;
+                    const uint32_t to = ito + b * kTile + lane * 16;
+#pragma unroll
+                    for (int t = 0; t < kPasses; ++t) {
+                        copy16(to + t * 512, from + t * 512, ok, policy);
+                        copy16(to + t * 512 + kCodes, vfrom + t * 512, ok, policy);
+                    }
                 }
-                pa::fence_proxy_async_smem();
+            } else {
+#pragma unroll
+                for (int t = 0; t < kChunk / kPass; ++t) {
+                    const int row = t * kPass + lrow;
+                    bool ok;
+                    const uint8_t* from = p.k_cache + tile_of(row >> bs_shift, ok) * kTile +
+                                          ((row & bmask) * kRow + lcol);
+                    const uint32_t to = ito + t * 512 + lane * 16;
+                    copy16(to, from, ok, policy);
+                    copy16(to + kCodes, from + k_to_v, ok, policy);
+                }
             }
-            if (lane == 0)
-                pa::mbar_arrive_expect_tx(bars_p + istage, (uint32_t)__popc(good) * block_bytes);
-            __syncwarp();
-            if (ok)
-                pa::bulk_load(to, src + ((int64_t)blk * real_heads + cur.s.g / p.subs) * unit, unit,
-                              bars + 8 * istage, policy);
-            if (++istage == S) istage = 0;
+            {
+                bool ok;
+                const uint8_t* from = scales + tile_of(srow >> bs_shift, ok) * kSTile +
+                                      (srow & bmask) * kSRow;
+                if (lane < 2 * kScaleLanes) copy16(ito + 2 * kCodes + lane * 16, from, ok, policy);
+            }
+            if (bad) pa::raise_error(p.err, PA_DEVERR_BLOCK_ID);
+            ito = ito + kStage == ring + S * kStage ? ring : ito + kStage;
             ++ipos;
-            if (++cur.s.c == cur.s.nc && ipos < hi) {
+            if (++cur.s.c < cur.s.nc) {
+                cur.left -= bpc;
+                cur.at += bpc;
+                if (cur.at == 32) {     // a window is a whole number of chunks
+                    cur.at = 0;
+                    cur.went = cur.wnext;
+                    const int32_t j = (int32_t)(cur.next - (p.block_tables + (int64_t)cur.s.i * p.max_blocks));
+                    cur.wnext = j < p.max_blocks ? __ldg(cur.next) : -1;
+                    cur.next += 32;
+                }
+            } else if (ipos < hi) {
                 cur = nxt;
                 if (cur.s.a + cur.s.nc < hi) nxt = open(next_pair(prefix, Hkv, cur.s));
             }
@@ -404,43 +478,80 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) decode_int4_kernel(
 
         Cursor s = start;
         load_q(s);
-        while (ipos < hi && ipos - lo < S) issue();
-        int stage = 0;
-        uint32_t phase = 0;
+        for (int k = 0; k < S; ++k) {   // a group per stage, empty or not
+            if (ipos < hi) issue();
+            commit_group();
+        }
+        uint32_t stage = ring;   // the chunk to compute
+        // Offsets of this lane in a stage: K rows cr, V rows 2 c4 + {0, 1} in its order.
+        const uint32_t odd = c4 & 1;
+        const uint32_t koff = cr * kRow + 8 * c4;
+        const uint32_t voff0 = kCodes + (2 * c4 + odd) * kRow + 4 * cr;
+        const uint32_t voff1 = kCodes + (2 * c4 + (odd ^ 1)) * kRow + 4 * cr;
+        const uint32_t perm0 = odd ? 0x1054 : 0x5410, perm1 = odd ? 0x3276 : 0x7632;
+        const uint32_t krow = krows + cr * NG * 8, vrow = vrows + cr * NG * 8;
         int segn = 0;
         for (int32_t pos = lo; pos < hi;) {
             const int32_t c0 = s.c, c_end = min(s.nc, s.c + hi - pos);
             const int32_t n = clamp_len(__ldg(p.context_lens + s.i), max_len);
             // Running state for heads 8 nt + 2 c4 + {0, 1}: maximum, sum, sums of P times
             // V's minima; o: rows are values 64 g + 8 cr + u (e < 2) and + 4 + u.
-            float m_run[NT][2], l_run[NT][2], lowv[NT][NG][2], o[NG][4][NT][4];
+            float m_run[NT][NJ], l_run[NT][NJ], lowv[NT][NG][NJ], o[NG][4][NT][4];
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+            for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
+                for (int j = 0; j < NJ; ++j) {
                     m_run[nt][j] = -INFINITY;
                     l_run[nt][j] = 0.f;
 #pragma unroll
-                    for (int g = 0; g < NG; ++g) {
-                        lowv[nt][g][j] = 0.f;
-#pragma unroll
-                        for (int u = 0; u < 4; ++u) o[g][u][nt][j] = o[g][u][nt][2 + j] = 0.f;
-                    }
+                    for (int g = 0; g < NG; ++g) lowv[nt][g][j] = 0.f;
                 }
+#pragma unroll
+                for (int g = 0; g < NG; ++g)
+#pragma unroll
+                    for (int u = 0; u < 4; ++u)
+                        o[g][u][nt][0] = o[g][u][nt][1] = o[g][u][nt][2] = o[g][u][nt][3] = 0.f;
+            }
             // P times V's step is kept in f16 range by 2^vexp, which o carries.
             int vexp = 126;
-            for (int32_t c = c0; c < c_end; ++c) {
-                const bool ready = dead || pa::mbar_wait(bars_p + stage, phase, kWaitLimitNs);
-                if (!__all_sync(0xffffffffu, ready)) {
-                    dead = true;
-                    if (lane == 0) pa::raise_error(p.err, PA_DEVERR_TIMEOUT);
-                }
-                if (!dead) {
-                    const int32_t valid = n - c * kChunk;   // tokens of the chunk in the context
-                    const uint32_t kt = ring + (uint32_t)stage * L.stage;
-                    const uint32_t vt = kt + kCodes, kst = vt + kCodes, vst = kst + kScales;
+            int32_t valid = n - c0 * kChunk;   // tokens of the context from the chunk on
+            for (int32_t c = c0; c < c_end; ++c, valid -= kChunk) {
+                wait_group(S);
+                __syncwarp();   // every lane's copies have landed
+                {
+                    const uint32_t kt = stage + koff, vt0 = stage + voff0, vt1 = stage + voff1;
+                    const uint32_t st_at = stage + 2 * kCodes + lane * kSRow;
+                    // ---- steps and minima: lane r takes row r of the chunk to fp32, K's
+                    // steps with the score's factor, V's with 2^vexp, for all lanes to read
+                    float rs = 1.f;   // what o is to be multiplied by
+                    {
+                        float kv[2 * NG], vv[2 * NG], vmax = 0.f;
+                        load_f16_scales<NG>(st_at, kv);
+                        load_f16_scales<NG>(st_at + kScales, vv);
+#pragma unroll
+                        for (int g = 0; g < NG; ++g) {
+                            // rows past the context may hold anything: weightless
+                            vv[2 * g] = lane < valid ? vv[2 * g] : 0.f;
+                            vv[2 * g + 1] = lane < valid ? vv[2 * g + 1] : 0.f;
+                            vmax = fmaxf(vmax, vv[2 * g]);
+                            kv[2 * g] *= qsc;
+                        }
+                        vmax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(vmax)));
+                        // P <= 2^kLazy, so P times a step stays below 2^15
+                        const int e = vmax > 0.f ? min(vexp, 133 - pa::biased_exponent(vmax)) : vexp;
+                        if (e < vexp) {
+                            rs = e - vexp >= -126 ? pa::exp2_int(e - vexp) : 0.f;
+                            vexp = e;
+                        }
+                        const float up = pa::exp2_int(vexp);
+#pragma unroll
+                        for (int g = 0; g < NG; ++g) vv[2 * g] *= up;
+                        store_row<NG>(krows + lane * NG * 8, kv);
+                        store_row<NG>(vrows + lane * NG * 8, vv);
+                    }
+                    __syncwarp();
                     // ---- S^T = K Q^T per group, then base-2 logits
-                    float x[kTiles][NT][4];
+                    float x[kTiles][NT][2][NJ];   // [key half][head]
 #pragma unroll
                     for (int mt = 0; mt < kTiles; ++mt) {
                         float st[NG][NT][4];
@@ -449,11 +560,10 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) decode_int4_kernel(
 #pragma unroll
                             for (int nt = 0; nt < NT; ++nt)
                                 st[g][nt][0] = st[g][nt][1] = st[g][nt][2] = st[g][nt][3] = 0.f;
-                        const uint32_t row0 = 16 * mt + cr;
 #pragma unroll
                         for (int g = 0; g < NG; ++g) {
-                            const uint2 w0 = pa::lds64(kt + row0 * kRow + 32 * g + 8 * c4);
-                            const uint2 w1 = pa::lds64(kt + (row0 + 8) * kRow + 32 * g + 8 * c4);
+                            const uint2 w0 = pa::lds64(kt + 16 * mt * kRow + 32 * g);
+                            const uint2 w1 = pa::lds64(kt + (16 * mt + 8) * kRow + 32 * g);
 #pragma unroll
                             for (int ks = 0; ks < 4; ++ks) {
                                 const uint32_t y0 = (ks < 2 ? w0.x : w0.y) >> (8 * (ks & 1));
@@ -467,75 +577,59 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) decode_int4_kernel(
                         }
 #pragma unroll
                         for (int r = 0; r < 2; ++r) {
-                            float ks[NG], km[NG];
-                            load_scales<NG>(kst + (row0 + 8 * r) * kSRow, ks, km);
+                            float kv[2 * NG];
+                            load_row<NG>(krow + (16 * mt + 8 * r) * NG * 8, kv);
 #pragma unroll
                             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                                for (int j = 0; j < 2; ++j) {
+                                for (int j = 0; j < NJ; ++j) {
                                     float v = 0.f;
 #pragma unroll
                                     for (int g = 0; g < NG; ++g)
-                                        v += km[g] * qsum[nt][g][j] + ks[g] * qsc * st[g][nt][2 * r + j];
-                                    x[mt][nt][2 * r + j] =
-                                        (int)row0 + 8 * r < valid ? v : -INFINITY;
+                                        v += kv[2 * g + 1] * qsum[nt][g][j] + kv[2 * g] * st[g][nt][2 * r + j];
+                                    x[mt][nt][r][j] = v;
                                 }
                         }
                     }
-                    // ---- V's steps and minima of this lane's rows; steps in f16 range
-                    float vs[kTiles][2][NG], vm[kTiles][2][NG], vmax = 0.f, rs = 1.f;
+                    if (valid < kChunk)   // the context's last chunk
 #pragma unroll
-                    for (int mt = 0; mt < kTiles; ++mt)
+                        for (int mt = 0; mt < kTiles; ++mt)
 #pragma unroll
-                        for (int r = 0; r < 2; ++r) {
-                            const int row = 16 * mt + cr + 8 * r;
-                            load_scales<NG>(vst + row * kSRow, vs[mt][r], vm[mt][r]);
+                            for (int r = 0; r < 2; ++r)
 #pragma unroll
-                            for (int g = 0; g < NG; ++g) {
-                                // rows past the context may hold anything: weightless
-                                vs[mt][r][g] = row < valid ? vs[mt][r][g] : 0.f;
-                                vm[mt][r][g] = row < valid ? vm[mt][r][g] : 0.f;
-                                vmax = fmaxf(vmax, vs[mt][r][g]);
-                            }
-                        }
-                    vmax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(vmax)));
-                    if (vmax > 0.f) {
-                        const int e = min(vexp, 141 - pa::biased_exponent(vmax));
-                        if (e < vexp) {
-                            rs = e - vexp >= -126 ? pa::exp2_int(e - vexp) : 0.f;
-                            vexp = e;
-                        }
-                    }
-                    const float vup = pa::exp2_int(vexp);
+                                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                                    for (int j = 0; j < NJ; ++j)
+                                        if (16 * mt + cr + 8 * r >= valid) x[mt][nt][r][j] = -INFINITY;
                     // ---- online softmax per head
-                    bool grew = false;
-                    float alpha[NT][2];
+                    float top[NT][NJ];
+                    bool above = rs != 1.f;
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                        for (int j = 0; j < 2; ++j) {
-                            float v = x[0][nt][j];
+                        for (int j = 0; j < NJ; ++j) {
+                            top[nt][j] = x[0][nt][0][j];
 #pragma unroll
                             for (int mt = 0; mt < kTiles; ++mt)
-                                v = fmaxf(v, fmaxf(x[mt][nt][j], x[mt][nt][2 + j]));
-                            v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
-                            v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
-                            v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
-                            const float m_new = fmaxf(m_run[nt][j], v);
-                            grew |= m_new > m_run[nt][j];
-                            alpha[nt][j] = pa::fast_exp2(m_run[nt][j] - m_new);
-                            m_run[nt][j] = m_new;
+                                top[nt][j] = fmaxf(top[nt][j], fmaxf(x[mt][nt][0][j], x[mt][nt][1][j]));
+                            above |= top[nt][j] > m_run[nt][j] + kLazy;
                         }
-                    if (__any_sync(0xffffffffu, grew) || rs != 1.f) {
+                    if (__any_sync(0xffffffffu, above)) {
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                            for (int j = 0; j < 2; ++j) {
-                                l_run[nt][j] *= alpha[nt][j];
-                                const float f = alpha[nt][j] * rs;
+                            for (int j = 0; j < NJ; ++j) {
+                                float v = top[nt][j];
+                                v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
+                                v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
+                                v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
+                                const float m_new = fmaxf(m_run[nt][j], v);
+                                const float a = pa::fast_exp2(m_run[nt][j] - m_new), f = a * rs;
+                                m_run[nt][j] = m_new;
+                                l_run[nt][j] *= a;
 #pragma unroll
                                 for (int g = 0; g < NG; ++g) {
-                                    lowv[nt][g][j] *= alpha[nt][j];
+                                    lowv[nt][g][j] *= a;
 #pragma unroll
                                     for (int u = 0; u < 4; ++u) {
                                         o[g][u][nt][j] *= f;
@@ -549,39 +643,39 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) decode_int4_kernel(
                     for (int mt = 0; mt < kTiles; ++mt) {
                         uint32_t pb[NG][NT][2];
 #pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) {
-                            float e[4];
+                        for (int r = 0; r < 2; ++r) {
+                            float vv[2 * NG];
+                            load_row<NG>(vrow + (16 * mt + 8 * r) * NG * 8, vv);
 #pragma unroll
-                            for (int q = 0; q < 4; ++q) {
-                                e[q] = pa::fast_exp2(x[mt][nt][q] - m_run[nt][q & 1]);
-                                l_run[nt][q & 1] += e[q];
-                            }
+                            for (int nt = 0; nt < NT; ++nt) {
+                                float e[2] = {0.f, 0.f};
 #pragma unroll
-                            for (int g = 0; g < NG; ++g)
-#pragma unroll
-                                for (int r = 0; r < 2; ++r) {
-                                    // rounded to f16: P's only rounding
-                                    const float f = vs[mt][r][g] * vup;
-                                    pb[g][nt][r] = pa::movmatrix_trans(
-                                        pa::pack2<false>(e[2 * r] * f, e[2 * r + 1] * f));
-                                    lowv[nt][g][0] += e[2 * r] * vm[mt][r][g];
-                                    lowv[nt][g][1] += e[2 * r + 1] * vm[mt][r][g];
+                                for (int j = 0; j < NJ; ++j) {
+                                    e[j] = pa::fast_exp2(x[mt][nt][r][j] - m_run[nt][j]);
+                                    l_run[nt][j] += e[j];
                                 }
+#pragma unroll
+                                for (int g = 0; g < NG; ++g) {
+                                    // rounded to f16: P's only rounding
+                                    pb[g][nt][r] = pa::movmatrix_trans(
+                                        pa::pack2<false>(e[0] * vv[2 * g], e[1] * vv[2 * g]));
+#pragma unroll
+                                    for (int j = 0; j < NJ; ++j) lowv[nt][g][j] += e[j] * vv[2 * g + 1];
+                                }
+                            }
                         }
                         // The fragment's key pairs: 16 mt + 8 r + 2 c4 + {0, 1}; odd c4 read
                         // the pair's second row first, so that the four rows of a load lie in
                         // both halves of the 128 bytes, and swap in the byte permutation.
-                        const uint32_t odd = c4 & 1;
-                        const uint32_t row = 16 * mt + 2 * c4;
 #pragma unroll
                         for (int g = 0; g < NG; ++g) {
                             uint32_t z[2][2];   // [key half][values 0..3 | 4..7]
 #pragma unroll
                             for (int r = 0; r < 2; ++r) {
-                                const uint32_t at = vt + (row + 8 * r) * kRow + 32 * g + 4 * cr;
-                                const uint32_t w0 = lds32(at + odd * kRow), w1 = lds32(at + (odd ^ 1) * kRow);
-                                z[r][0] = __byte_perm(w0, w1, odd ? 0x1054 : 0x5410);
-                                z[r][1] = __byte_perm(w0, w1, odd ? 0x3276 : 0x7632);
+                                const uint32_t w0 = lds32(vt0 + (16 * mt + 8 * r) * kRow + 32 * g);
+                                const uint32_t w1 = lds32(vt1 + (16 * mt + 8 * r) * kRow + 32 * g);
+                                z[r][0] = __byte_perm(w0, w1, perm0);
+                                z[r][1] = __byte_perm(w0, w1, perm1);
                             }
 #pragma unroll
                             for (int u = 0; u < 4; ++u) {
@@ -597,11 +691,9 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) decode_int4_kernel(
                     }
                 }
                 __syncwarp();   // every lane has read the stage: it may be filled again
-                if (++stage == S) {
-                    stage = 0;
-                    phase ^= 1u;
-                }
-                if (ipos < hi && !dead) issue();
+                stage = stage + kStage == ring + S * kStage ? ring : stage + kStage;
+                if (ipos < hi) issue();
+                commit_group();
             }
             pos += c_end - c0;
 
@@ -609,7 +701,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) decode_int4_kernel(
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
+                for (int j = 0; j < NJ; ++j) {
 #pragma unroll
                     for (int off = 4; off < 32; off <<= 1) {
                         l_run[nt][j] += __shfl_xor_sync(0xffffffffu, l_run[nt][j], off);
@@ -622,13 +714,13 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) decode_int4_kernel(
             // The warp's first run may end while its ring is in use: a slot of its own.
             // A later unfinished run is its last: the ring is free.
             const uint32_t at = segn == 0 ? L.slots + (uint32_t)warp * slot_floats(G, D) * 4
-                                          : (uint32_t)warp * S * L.stage;
+                                          : (uint32_t)warp * S * kStage;
             float* slot = reinterpret_cast<float*>(smem + at);
             const float low = pa::exp2_int(min(24 - vexp, 127)), high = low * 0.0625f;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
+                for (int j = 0; j < NJ; ++j) {
                     const int h = 8 * nt + 2 * c4 + j;
                     if (h >= G) continue;
                     const float inv = whole ? 1.f / l_run[nt][j] : 1.f;
@@ -671,9 +763,6 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) decode_int4_kernel(
                 load_q(s);
             }
         }
-        if (dead)   // copies still in flight land before the CTA may exit
-            for (int st = 0; st < S && st < ipos - lo; ++st)
-                pa::mbar_wait(bars_p + st, (uint32_t)((ipos - lo - 1 - st) / S) & 1u, kWaitLimitNs);
     }
     __syncthreads();
 
@@ -707,7 +796,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) decode_int4_kernel(
     };
     auto span = [&](int first) {   // runs from `first` on that may belong to its pair
         int last = first;
-        for (int k = first + 1; k < 2 * kWarps; ++k)
+        for (int k = first + 1; k < 2 * nw; ++k)
             if (runs[k].a == runs[first].a) last = k;
         return last - first + 1;
     };
@@ -739,19 +828,18 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) decode_int4_kernel(
         if (k < 0) continue;
         const Run r = runs[k];
         const int count = span(k);
-        const int64_t c_first = ((int64_t)(r.a + 1) * C - 1) / W;
-        const int64_t c_last = ((int64_t)(r.a + r.nc) * C - 1) / W;
+        const int64_t c_first = cut.part(r.a), c_last = cut.part(r.a + r.nc - 1);
         // A CTA's first slot holds the pair that its share begins in or with, its
         // second the one that begins later.
-        float* mine = p.partials + (2 * (int64_t)blockIdx.x + (cta_lo >= r.a ? 0 : 1)) * kSlot;
-        for (int e = tid; e < G * D / 4; e += kThreads) {
+        float* ps = p.partials + (2 * (int64_t)blockIdx.x + (cta_lo >= r.a ? 0 : 1)) * kSlot;
+        for (int e = tid; e < G * D / 4; e += threads) {
             const int h = e / (D / 4), d4 = (e % (D / 4)) * 4;
             float M, l;
             const float4 v = merged4(k, count, h, d4, M, l);
-            *reinterpret_cast<float4*>(mine + 2 * kMaxG + h * D + d4) = v;
+            *reinterpret_cast<float4*>(ps + 2 * kMaxG + h * D + d4) = v;
             if (d4 == 0) {
-                mine[h] = M;
-                mine[kMaxG + h] = l;
+                ps[h] = M;
+                ps[kMaxG + h] = l;
             }
         }
         __syncthreads();
@@ -764,8 +852,8 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) decode_int4_kernel(
         __syncthreads();
         if (*is_last) {
             const int n = (int)(c_last - c_first + 1);
-            const int64_t slot0 = 2 * c_first + (share(c_first, W, C) == r.a ? 0 : 1);
-            for (int e = tid; e < G * D / 4; e += kThreads) {
+            const int64_t slot0 = 2 * c_first + (cut.begin((int32_t)c_first) == r.a ? 0 : 1);
+            for (int e = tid; e < G * D / 4; e += threads) {
                 const int h = e / (D / 4), d4 = (e % (D / 4)) * 4;
                 float M = -INFINITY, l = 0.f;
                 float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -818,17 +906,25 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) decode_int4_kernel(
 // Shared memory per CTA that leaves room for ctas_per_sm(NT) of them on an SM.
 uint32_t smem_budget(int NT) { return (NT == 1 ? 113 : 226) * 1024; }
 
-int choose_stages(int D, int G, int B) {
-    const int NT = G <= 8 ? 1 : 2;
-    const Layout L = make_layout(D, G, B, 0);
-    if (L.total >= smem_budget(NT)) return 0;
-    const int s = (int)((smem_budget(NT) - L.total) / (kWarps * L.stage));
-    return s > kMaxStages ? kMaxStages : s;
+// As many warps as leave each a ring of two stages or more, then as many stages
+// as fit (a warp computes on one while the other fills).
+bool choose_shape(int D, int G, int B, int* warps, int* stages) {
+    const uint32_t budget = smem_budget(G <= 8 ? 1 : 2);
+    for (int w = kMaxWarps; w >= 4; --w) {
+        int s = kMaxStages;
+        while (s >= 2 && make_layout(D, G, B, w, s).total > budget) --s;
+        if (s >= 2) {
+            *warps = w;
+            *stages = s;
+            return true;
+        }
+    }
+    return false;
 }
 
-template <int D, bool kBF16, int NT>
+template <int D, bool kBF16, int NT, bool kOne, int kShift>
 pa_status launch(const Int4Params& p, cudaStream_t stream) {
-    auto kern = decode_int4_kernel<D, kBF16, NT>;
+    auto kern = decode_int4_kernel<D, kBF16, NT, kOne, kShift>;
     // The shared-memory limit is set once per device.
     static std::mutex mu;
     static uint64_t done = 0;
@@ -846,9 +942,22 @@ pa_status launch(const Int4Params& p, cudaStream_t stream) {
     int ctas = pa::device_sm_count() * ctas_per_sm(NT);
     if (ctas <= 0) return PA_ERR_CUDA;
     if (ctas > kMaxCtas) ctas = kMaxCtas;
-    const Layout L = make_layout(D, p.G, p.B, p.stages);
-    kern<<<ctas, kThreads, L.total, stream>>>(p);
+    const Layout L = make_layout(D, p.G, p.B, p.warps, p.stages);
+    kern<<<ctas, p.warps * 32, L.total, stream>>>(p);
     return pa::cuda_status(cudaGetLastError());
+}
+
+template <int D, bool kBF16, int NT, bool kOne>
+pa_status launch_b(const Int4Params& p, cudaStream_t stream) {
+    if (p.bs_shift == 3) return launch<D, kBF16, NT, kOne, 3>(p, stream);
+    if (p.bs_shift == 4) return launch<D, kBF16, NT, kOne, 4>(p, stream);
+    return launch<D, kBF16, NT, kOne, 5>(p, stream);
+}
+
+template <int D, bool kBF16>
+pa_status launch_g(const Int4Params& p, cudaStream_t stream) {
+    if (p.G == 1) return launch_b<D, kBF16, 1, true>(p, stream);
+    return p.G <= 8 ? launch_b<D, kBF16, 1, false>(p, stream) : launch_b<D, kBF16, 2, false>(p, stream);
 }
 
 }  // namespace
@@ -875,7 +984,7 @@ PA_API pa_status pa_decode_int4(const void* q, const void* k_cache, const void* 
     }
     if (d != 64 && d != 128) return PA_ERR_UNSUPPORTED;
     if (block_size != 8 && block_size != 16 && block_size != 32) return PA_ERR_UNSUPPORTED;
-    if (B > kMaxBatch || (int64_t)num_blocks * block_size > INT32_MAX ||
+    if ((int64_t)num_blocks * Hkv > INT32_MAX || B > kMaxBatch || (int64_t)num_blocks * block_size > INT32_MAX ||
         (int64_t)max_blocks * block_size > INT32_MAX)
         return PA_ERR_UNSUPPORTED;
     // Flattened chunk indices are int32.
@@ -891,8 +1000,7 @@ PA_API pa_status pa_decode_int4(const void* q, const void* k_cache, const void* 
          reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(out)) & 15u)
         return PA_ERR_INVALID;
     Int4Params p;
-    p.stages = choose_stages(d, G, B);
-    if (p.stages < 2) return PA_ERR_UNSUPPORTED;
+    if (!choose_shape(d, G, B, &p.warps, &p.stages)) return PA_ERR_UNSUPPORTED;
     p.err = pa::device_error_word();
     if (!p.err) return PA_ERR_CUDA;
     p.q = static_cast<const uint16_t*>(q);
@@ -916,14 +1024,9 @@ PA_API pa_status pa_decode_int4(const void* q, const void* k_cache, const void* 
     p.num_blocks = num_blocks;
     p.scale_log2 = scale * kLog2e;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (G <= 8) {
-        if (d == 128)
-            return dtype == PA_BF16 ? launch<128, true, 1>(p, st) : launch<128, false, 1>(p, st);
-        return dtype == PA_BF16 ? launch<64, true, 1>(p, st) : launch<64, false, 1>(p, st);
-    }
     if (d == 128)
-        return dtype == PA_BF16 ? launch<128, true, 2>(p, st) : launch<128, false, 2>(p, st);
-    return dtype == PA_BF16 ? launch<64, true, 2>(p, st) : launch<64, false, 2>(p, st);
+        return dtype == PA_BF16 ? launch_g<128, true>(p, st) : launch_g<128, false>(p, st);
+    return dtype == PA_BF16 ? launch_g<64, true>(p, st) : launch_g<64, false>(p, st);
 }
 
 }  // extern "C"
