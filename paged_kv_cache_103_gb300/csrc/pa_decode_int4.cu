@@ -48,7 +48,8 @@ constexpr int kTiles = kChunk / 16;     // 16-key MMA tiles per chunk
 constexpr int kMaxG = 16;
 constexpr int kMaxBatch = 4096;
 constexpr int kMaxCtas = 512;
-constexpr int kMaxStages = 5;
+// Stages of a warp's ring: it computes on one while the others fill.
+__host__ __device__ constexpr int ring_stages(int D) { return D == 128 ? 2 : 4; }
 constexpr float kLog2e = 1.4426950408889634f;
 
 struct Int4Params {
@@ -61,7 +62,7 @@ struct Int4Params {
     float* partials;     // [2 * CTAs][2 * kMaxG + kMaxG * D]
     unsigned int* err;
     // A KV head with more than kMaxG query heads is `subs` pairs of kMaxG heads.
-    int32_t max_blocks, B, H, Hkv, G, bs_shift, num_blocks, stages, subs, warps;
+    int32_t max_blocks, B, H, Hkv, G, bs_shift, num_blocks, subs, warps;
     float scale_log2;
 };
 
@@ -84,8 +85,8 @@ struct Layout {
     uint32_t stage, rows, slots, runs, open, scan, prefix, total;
 };
 
-__host__ __device__ inline Layout make_layout(int D, int G, int B, int warps,
-                                              int stages) {
+__host__ __device__ inline Layout make_layout(int D, int G, int B, int warps) {
+    const int stages = ring_stages(D);
     Layout L;
     L.stage = 2u * kChunk * (D / 2 + D / 64 * 4);            // K, V codes, K, V scales
     L.rows = warps * stages * L.stage;                      // per warp: K and V of 32 rows
@@ -153,14 +154,9 @@ __device__ __forceinline__ void copy16(uint32_t to, const void* from, bool ok, u
                  "r"(ok ? 16 : 0), "l"(policy) : "memory");
 }
 __device__ __forceinline__ void commit_group() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-// Waits until at most S - 1 of this thread's groups are in flight.
-__device__ __forceinline__ void wait_group(int S) {
-    switch (S) {
-        case 2: asm volatile("cp.async.wait_group 1;" ::: "memory"); break;
-        case 3: asm volatile("cp.async.wait_group 2;" ::: "memory"); break;
-        case 4: asm volatile("cp.async.wait_group 3;" ::: "memory"); break;
-        default: asm volatile("cp.async.wait_group 4;" ::: "memory"); break;
-    }
+template <int N>
+__device__ __forceinline__ void wait_group() {   // until at most N of this thread's groups are in flight
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 __device__ __forceinline__ uint32_t lds32(uint32_t addr) {
@@ -227,6 +223,7 @@ __device__ __forceinline__ void store_row(uint32_t addr, const float (&v)[2 * NG
 
 constexpr uint32_t kLowNibbles = 0x000F000Fu;    // c 2^-24 each
 constexpr uint32_t kHighNibbles = 0x00F000F0u;   // c 2^-20 each
+constexpr uint32_t kBytes = 0x00FF00FFu;         // (c + 16 c') 2^-24 each
 
 // A head's running maximum is raised only when a logit exceeds it by more than this
 // (base 2): probabilities reach 2^8, which fp32 sums and the f16 range of P bear, and
@@ -240,10 +237,11 @@ __global__ void __launch_bounds__(kMaxWarps * 32, ctas_per_sm(NT)) decode_int4_k
     constexpr uint32_t kRow = D / 2, kSRow = NG * 4;         // bytes of a row's codes and scales
     constexpr uint32_t kCodes = kChunk * kRow, kScales = kChunk * kSRow;
     constexpr uint32_t kStage = 2 * (kCodes + kScales);   // K, V codes, K, V scales
-    const int32_t B = p.B, Hkv = p.Hkv, G = p.G, S = p.stages;
+    constexpr int S = ring_stages(D);
+    const int32_t B = p.B, Hkv = p.Hkv, G = p.G;
     constexpr int bs_shift = kShift, bmask = (1 << kShift) - 1;
     const int nw = p.warps, threads = nw * 32;
-    const Layout L = make_layout(D, G, B, nw, S);
+    const Layout L = make_layout(D, G, B, nw);
     extern __shared__ __align__(128) unsigned char smem[];
     const uint32_t sbase = pa::smem_addr(smem);
     Run* runs = reinterpret_cast<Run*>(smem + L.runs);
@@ -326,13 +324,14 @@ __global__ void __launch_bounds__(kMaxWarps * 32, ctas_per_sm(NT)) decode_int4_k
         const uint8_t* scales = lane < kScaleLanes ? p.k_scale : p.v_scale;
         constexpr int bpc = kChunk >> bs_shift;     // blocks per chunk: 4, 2 or 1
         // A pair's table entries, 32 at a time (lane l holds the window's entry l), with
-        // the window after it and the next pair's first one loaded a step ahead.
+        // the window after it loaded a step ahead.  (The next pair's first window is not:
+        // its registers cost more than the wait, which other warps fill.)
         struct Walk {
             Cursor s;
             uint32_t head;           // the cache's KV head
             int32_t at, left;        // first block of the chunk: in the window, and how many follow
             int32_t went, wnext;
-            const int32_t* next;     // this lane's entry of the window after wnext
+            int32_t next;            // this lane's entry after wnext's
         };
         auto open = [&](const Cursor& s) {
             Walk w;
@@ -345,14 +344,13 @@ __global__ void __launch_bounds__(kMaxWarps * 32, ctas_per_sm(NT)) decode_int4_k
             w.left = ((n + bmask) >> bs_shift) - j0;
             w.went = j < p.max_blocks ? __ldg(row) : -1;
             w.wnext = j + 32 < p.max_blocks ? __ldg(row + 32) : -1;
-            w.next = row + 64;
+            w.next = j + 64;
             return w;
         };
         int32_t ipos = lo;              // next chunk to issue
         uint32_t ito = ring;            // its stage
-        Walk cur = open(find(prefix, B, Hkv, lo)), nxt = cur;
+        Walk cur = open(find(prefix, B, Hkv, lo));
         const Cursor start = cur.s;
-        if (start.a + start.nc < hi) nxt = open(next_pair(prefix, Hkv, start));
         // One chunk's copies, as one group.  Blocks past the context and ids outside the
         // pool are not read: zeros take their place (a step and a minimum of zero: rows of
         // zeros).
@@ -406,13 +404,12 @@ __global__ void __launch_bounds__(kMaxWarps * 32, ctas_per_sm(NT)) decode_int4_k
                 if (cur.at == 32) {     // a window is a whole number of chunks
                     cur.at = 0;
                     cur.went = cur.wnext;
-                    const int32_t j = (int32_t)(cur.next - (p.block_tables + (int64_t)cur.s.i * p.max_blocks));
-                    cur.wnext = j < p.max_blocks ? __ldg(cur.next) : -1;
+                    cur.wnext = cur.next < p.max_blocks
+                        ? __ldg(p.block_tables + (int64_t)cur.s.i * p.max_blocks + cur.next) : -1;
                     cur.next += 32;
                 }
             } else if (ipos < hi) {
-                cur = nxt;
-                if (cur.s.a + cur.s.nc < hi) nxt = open(next_pair(prefix, Hkv, cur.s));
+                cur = open(next_pair(prefix, Hkv, cur.s));
             }
         };
 
@@ -516,11 +513,33 @@ __global__ void __launch_bounds__(kMaxWarps * 32, ctas_per_sm(NT)) decode_int4_k
             int vexp = 126;
             int32_t valid = n - c0 * kChunk;   // tokens of the context from the chunk on
             for (int32_t c = c0; c < c_end; ++c, valid -= kChunk) {
-                wait_group(S);
+                wait_group<S - 1>();
                 __syncwarp();   // every lane's copies have landed
                 {
                     const uint32_t kt = stage + koff, vt0 = stage + voff0, vt1 = stage + voff1;
                     const uint32_t st_at = stage + 2 * kCodes + lane * kSRow;
+                    // ---- S^T = K Q^T over the codes, per group
+                    float st[kTiles][NG][NT][4];
+#pragma unroll
+                    for (int mt = 0; mt < kTiles; ++mt)
+#pragma unroll
+                        for (int g = 0; g < NG; ++g) {
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt)
+                                st[mt][g][nt][0] = st[mt][g][nt][1] = st[mt][g][nt][2] = st[mt][g][nt][3] = 0.f;
+                            const uint2 w0 = pa::lds64(kt + 16 * mt * kRow + 32 * g);
+                            const uint2 w1 = pa::lds64(kt + (16 * mt + 8) * kRow + 32 * g);
+#pragma unroll
+                            for (int ks = 0; ks < 4; ++ks) {
+                                const uint32_t y0 = (ks < 2 ? w0.x : w0.y) >> (8 * (ks & 1));
+                                const uint32_t y1 = (ks < 2 ? w1.x : w1.y) >> (8 * (ks & 1));
+                                const uint32_t a[4] = {y0 & kLowNibbles, y1 & kLowNibbles,
+                                                       y0 & kHighNibbles, y1 & kHighNibbles};
+#pragma unroll
+                                for (int nt = 0; nt < NT; ++nt)
+                                    pa::mma_16816<false>(st[mt][g][nt], a, qb[nt][g][ks][0], qb[nt][g][ks][1]);
+                            }
+                        }
                     // ---- steps and minima: lane r takes row r of the chunk to fp32, K's
                     // steps with the score's factor, V's with 2^vexp, for all lanes to read
                     float rs = 1.f;   // what o is to be multiplied by
@@ -550,31 +569,10 @@ __global__ void __launch_bounds__(kMaxWarps * 32, ctas_per_sm(NT)) decode_int4_k
                         store_row<NG>(vrows + lane * NG * 8, vv);
                     }
                     __syncwarp();
-                    // ---- S^T = K Q^T per group, then base-2 logits
+                    // ---- base-2 logits
                     float x[kTiles][NT][2][NJ];   // [key half][head]
 #pragma unroll
-                    for (int mt = 0; mt < kTiles; ++mt) {
-                        float st[NG][NT][4];
-#pragma unroll
-                        for (int g = 0; g < NG; ++g)
-#pragma unroll
-                            for (int nt = 0; nt < NT; ++nt)
-                                st[g][nt][0] = st[g][nt][1] = st[g][nt][2] = st[g][nt][3] = 0.f;
-#pragma unroll
-                        for (int g = 0; g < NG; ++g) {
-                            const uint2 w0 = pa::lds64(kt + 16 * mt * kRow + 32 * g);
-                            const uint2 w1 = pa::lds64(kt + (16 * mt + 8) * kRow + 32 * g);
-#pragma unroll
-                            for (int ks = 0; ks < 4; ++ks) {
-                                const uint32_t y0 = (ks < 2 ? w0.x : w0.y) >> (8 * (ks & 1));
-                                const uint32_t y1 = (ks < 2 ? w1.x : w1.y) >> (8 * (ks & 1));
-                                const uint32_t a[4] = {y0 & kLowNibbles, y1 & kLowNibbles,
-                                                       y0 & kHighNibbles, y1 & kHighNibbles};
-#pragma unroll
-                                for (int nt = 0; nt < NT; ++nt)
-                                    pa::mma_16816<false>(st[g][nt], a, qb[nt][g][ks][0], qb[nt][g][ks][1]);
-                            }
-                        }
+                    for (int mt = 0; mt < kTiles; ++mt)
 #pragma unroll
                         for (int r = 0; r < 2; ++r) {
                             float kv[2 * NG];
@@ -583,14 +581,13 @@ __global__ void __launch_bounds__(kMaxWarps * 32, ctas_per_sm(NT)) decode_int4_k
                             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                                 for (int j = 0; j < NJ; ++j) {
-                                    float v = 0.f;
+                                    float v = kv[1] * qsum[nt][0][j] + kv[0] * st[mt][0][nt][2 * r + j];
 #pragma unroll
-                                    for (int g = 0; g < NG; ++g)
-                                        v += kv[2 * g + 1] * qsum[nt][g][j] + kv[2 * g] * st[g][nt][2 * r + j];
+                                    for (int g = 1; g < NG; ++g)
+                                        v += kv[2 * g + 1] * qsum[nt][g][j] + kv[2 * g] * st[mt][g][nt][2 * r + j];
                                     x[mt][nt][r][j] = v;
                                 }
                         }
-                    }
                     if (valid < kChunk)   // the context's last chunk
 #pragma unroll
                         for (int mt = 0; mt < kTiles; ++mt)
@@ -679,10 +676,16 @@ __global__ void __launch_bounds__(kMaxWarps * 32, ctas_per_sm(NT)) decode_int4_k
                             }
 #pragma unroll
                             for (int u = 0; u < 4; ++u) {
-                                const uint32_t mask = u & 1 ? kHighNibbles : kLowNibbles;
-                                const int sh = 8 * (u >> 1);
-                                const uint32_t a[4] = {(z[0][0] >> sh) & mask, (z[0][1] >> sh) & mask,
-                                                       (z[1][0] >> sh) & mask, (z[1][1] >> sh) & mask};
+                                // u even: the byte's lower code; u odd: the whole byte, lower
+                                // code plus 16 times the upper one, which the end takes apart
+                                const uint32_t mask = u & 1 ? kBytes : kLowNibbles;
+                                uint32_t a[4];
+#pragma unroll
+                                for (int q = 0; q < 4; ++q) {
+                                    const uint32_t w = z[q >> 1][q & 1];
+                                    // bytes 1 and 3 to the low half of each half
+                                    a[q] = (u < 2 ? w : __byte_perm(w, 0, 0x4341)) & mask;
+                                }
 #pragma unroll
                                 for (int nt = 0; nt < NT; ++nt)
                                     pa::mma_16816<false>(o[g][u][nt], a, pb[g][nt][0], pb[g][nt][1]);
@@ -732,9 +735,12 @@ __global__ void __launch_bounds__(kMaxWarps * 32, ctas_per_sm(NT)) decode_int4_k
                     for (int g = 0; g < NG; ++g) {
                         float v[8];
 #pragma unroll
-                        for (int u = 0; u < 8; ++u)
-                            v[u] = (o[g][u & 3][nt][2 * (u >> 2) + j] * (u & 1 ? high : low) +
-                                    lowv[nt][g][j]) * inv;
+                        for (int u = 0; u < 8; ++u) {
+                            const int e = 2 * (u >> 2) + j;
+                            const float sum = u & 1 ? (o[g][u & 3][nt][e] - o[g][(u & 3) - 1][nt][e]) * high
+                                                    : o[g][u & 3][nt][e] * low;
+                            v[u] = (sum + lowv[nt][g][j]) * inv;
+                        }
                         const int at_d = 64 * g + 8 * cr;
                         if (whole) {
                             *reinterpret_cast<uint4*>(p.out + ((int64_t)s.i * p.H + s.g * G + h) * D + at_d) =
@@ -906,20 +912,11 @@ __global__ void __launch_bounds__(kMaxWarps * 32, ctas_per_sm(NT)) decode_int4_k
 // Shared memory per CTA that leaves room for ctas_per_sm(NT) of them on an SM.
 uint32_t smem_budget(int NT) { return (NT == 1 ? 113 : 226) * 1024; }
 
-// As many warps as leave each a ring of two stages or more, then as many stages
-// as fit (a warp computes on one while the other fills).
-bool choose_shape(int D, int G, int B, int* warps, int* stages) {
-    const uint32_t budget = smem_budget(G <= 8 ? 1 : 2);
-    for (int w = kMaxWarps; w >= 4; --w) {
-        int s = kMaxStages;
-        while (s >= 2 && make_layout(D, G, B, w, s).total > budget) --s;
-        if (s >= 2) {
-            *warps = w;
-            *stages = s;
-            return true;
-        }
-    }
-    return false;
+// As many warps as shared memory holds rings and slots for; 0: not even four.
+int choose_warps(int D, int G, int B) {
+    for (int w = kMaxWarps; w >= 4; --w)
+        if (make_layout(D, G, B, w).total <= smem_budget(G <= 8 ? 1 : 2)) return w;
+    return 0;
 }
 
 template <int D, bool kBF16, int NT, bool kOne, int kShift>
@@ -942,7 +939,7 @@ pa_status launch(const Int4Params& p, cudaStream_t stream) {
     int ctas = pa::device_sm_count() * ctas_per_sm(NT);
     if (ctas <= 0) return PA_ERR_CUDA;
     if (ctas > kMaxCtas) ctas = kMaxCtas;
-    const Layout L = make_layout(D, p.G, p.B, p.warps, p.stages);
+    const Layout L = make_layout(D, p.G, p.B, p.warps);
     kern<<<ctas, p.warps * 32, L.total, stream>>>(p);
     return pa::cuda_status(cudaGetLastError());
 }
@@ -1000,7 +997,8 @@ PA_API pa_status pa_decode_int4(const void* q, const void* k_cache, const void* 
          reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(out)) & 15u)
         return PA_ERR_INVALID;
     Int4Params p;
-    if (!choose_shape(d, G, B, &p.warps, &p.stages)) return PA_ERR_UNSUPPORTED;
+    p.warps = choose_warps(d, G, B);
+    if (!p.warps) return PA_ERR_UNSUPPORTED;
     p.err = pa::device_error_word();
     if (!p.err) return PA_ERR_CUDA;
     p.q = static_cast<const uint16_t*>(q);
