@@ -42,7 +42,6 @@
 
 namespace {
 
-constexpr int kMaxWarps = 8;            // per CTA
 constexpr int kChunk = 32;              // tokens per stage
 constexpr int kTiles = kChunk / 16;     // 16-key MMA tiles per chunk
 constexpr int kMaxG = 16;
@@ -66,23 +65,33 @@ struct Int4Params {
     float scale_log2;
 };
 
-// ctas per SM: two, or one where 9 .. 16 heads need two 8-wide MMA tiles and the
-// accumulators with them.
-__host__ __device__ constexpr int ctas_per_sm(int NT) { return NT == 1 ? 2 : 1; }
+// One CTA per SM.  Sixteen warps, or eight where 9 .. 16 heads need two 8-wide MMA
+// tiles and twice the accumulators.
+__host__ __device__ constexpr int max_warps(int NT) { return NT == 1 ? 16 : 8; }
+constexpr uint32_t kSmemBudget = 227 * 1024;
 
-// One partial result: row maxima [kMaxG], row sums [kMaxG], outputs [G][D].
-__host__ __device__ constexpr int slot_floats(int G, int D) { return 2 * kMaxG + G * D; }
+// A warp may be this many chunks ahead of the slowest one of its CTA.  The schedulers
+// favour some warps; left alone, those end early and the others finish on a half-empty
+// SM (two 8-warp CTAs per SM ended 25 us apart of 109).
+constexpr int kLead = 4;
+constexpr int kPaceTries = 1 << 14;
+
+// One partial result in shared memory: row maxima [G], row sums [G], padding to 16 bytes,
+// outputs [G][D]; in the workspace: maxima and sums [kMaxG] each.
+__host__ __device__ constexpr int slot_head(int G) { return (2 * G + 3) & ~3; }
+__host__ __device__ constexpr int slot_floats(int G, int D) { return slot_head(G) + G * D; }
+__host__ __device__ constexpr int partial_floats(int D) { return 2 * kMaxG + kMaxG * D; }
 
 // A run of chunks [c0, end) of one pair that a warp left in shared memory.
 struct Run {
     int32_t a;    // flattened index of the pair's first chunk; -1: none
     int32_t i, g, c0, end, nc;
-    uint32_t at;  // byte offset of its slot
-    int32_t pad;
+    uint32_t at;  // at the end, entry x: the set of runs of the CTA's x-th pair,
+    int32_t pad;  // and the first of them (+ 256: other CTAs hold more)
 };
 
 struct Layout {
-    uint32_t stage, rows, slots, runs, open, scan, prefix, total;
+    uint32_t stage, rows, slots, runs, last, pace, scan, prefix, total;
 };
 
 __host__ __device__ inline Layout make_layout(int D, int G, int B, int warps) {
@@ -92,8 +101,9 @@ __host__ __device__ inline Layout make_layout(int D, int G, int B, int warps) {
     L.rows = warps * stages * L.stage;                      // per warp: K and V of 32 rows
     L.slots = L.rows + warps * 2 * kChunk * (D / 64) * 8;   // a slot per warp
     L.runs = L.slots + warps * slot_floats(G, D) * 4;       // [2 * warps]
-    L.open = L.runs + 2 * warps * (uint32_t)sizeof(Run);     // runs left to other CTAs
-    L.scan = L.open + 16;
+    L.last = L.runs + 2 * warps * (uint32_t)sizeof(Run);     // "the last CTA of the pair"
+    L.pace = L.last + 8;                                     // chunks done by each warp
+    L.scan = L.pace + warps * 4;
     L.prefix = L.scan + warps * 4;                          // [B + 1]
     L.total = L.prefix + (uint32_t)(B + 1) * 4;
     return L;
@@ -122,6 +132,7 @@ struct Cursor {
 
 __device__ __forceinline__ Cursor find(const int32_t* prefix, int32_t B, int32_t Hkv, int32_t pos) {
     int32_t lo = 0, hi = B;   // largest i with prefix[i] <= pos
+#pragma unroll 1
     while (hi - lo > 1) {
         const int32_t mid = (lo + hi) >> 1;
         if (prefix[mid] <= pos) lo = mid; else hi = mid;
@@ -157,6 +168,10 @@ __device__ __forceinline__ void commit_group() { asm volatile("cp.async.commit_g
 template <int N>
 __device__ __forceinline__ void wait_group() {   // until at most N of this thread's groups are in flight
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ void prefetch_l2(const void* p) {
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
 }
 
 __device__ __forceinline__ uint32_t lds32(uint32_t addr) {
@@ -232,7 +247,7 @@ constexpr float kLazy = 8.f;
 
 // kOne: one query head per KV head; a lane then tracks one column instead of two.
 template <int D, bool kBF16, int NT, bool kOne, int kShift>
-__global__ void __launch_bounds__(kMaxWarps * 32, ctas_per_sm(NT)) decode_int4_kernel(const Int4Params p) {
+__global__ void __launch_bounds__(max_warps(NT) * 32, 1) decode_int4_kernel(const Int4Params p) {
     constexpr int NG = D / 64, NJ = kOne ? 1 : 2;
     constexpr uint32_t kRow = D / 2, kSRow = NG * 4;         // bytes of a row's codes and scales
     constexpr uint32_t kCodes = kChunk * kRow, kScales = kChunk * kSRow;
@@ -245,17 +260,28 @@ __global__ void __launch_bounds__(kMaxWarps * 32, ctas_per_sm(NT)) decode_int4_k
     extern __shared__ __align__(128) unsigned char smem[];
     const uint32_t sbase = pa::smem_addr(smem);
     Run* runs = reinterpret_cast<Run*>(smem + L.runs);
-    int32_t* open_run = reinterpret_cast<int32_t*>(smem + L.open);
+    int32_t* is_last = reinterpret_cast<int32_t*>(smem + L.last);
+    volatile int32_t* pace = reinterpret_cast<int32_t*>(smem + L.pace);
     int32_t* scan = reinterpret_cast<int32_t*>(smem + L.scan);
     int32_t* prefix = reinterpret_cast<int32_t*>(smem + L.prefix);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int32_t max_len = p.max_blocks << bs_shift;
+
+    // The tables and queries are read a dependent load or two from now: into L2 with
+    // them, a line per thread (what they cover is shared by all CTAs).
+    {
+        const int64_t line = ((int64_t)blockIdx.x * threads + tid) * 128;
+        if (line < (int64_t)B * p.max_blocks * 4)
+            prefetch_l2(reinterpret_cast<const char*>(p.block_tables) + line);
+        if (line < (int64_t)B * p.H * D * 2) prefetch_l2(reinterpret_cast<const char*>(p.q) + line);
+    }
 
     // ---- prefix[i] = Hkv * chunks of the sequences before i
     {
         const int per = (B + threads - 1) / threads;
         const int beg = min(tid * per, B), end = min(beg + per, B);
         int32_t local = 0;
+#pragma unroll 1
         for (int i = beg; i < end; ++i) {
             const int32_t raw = __ldg(p.context_lens + i);
             if (blockIdx.x == 0) {
@@ -272,16 +298,19 @@ __global__ void __launch_bounds__(kMaxWarps * 32, ctas_per_sm(NT)) decode_int4_k
         }
         if (lane == 31) scan[warp] = x;
         if (tid < 2 * nw) runs[tid].a = -1;
-        if (tid < 2) open_run[tid] = -1;
+        if (tid < nw) pace[tid] = 0;
         __syncthreads();
         int32_t run = x - local;
+#pragma unroll 1
         for (int w = 0; w < warp; ++w) run += scan[w];
+#pragma unroll 1
         for (int i = beg; i < end; ++i) {
             prefix[i] = run * Hkv;
             run += (clamp_len(__ldg(p.context_lens + i), max_len) + kChunk - 1) / kChunk;
         }
         if (tid == 0) {
             int32_t total = 0;
+#pragma unroll 1
             for (int w = 0; w < nw; ++w) total += scan[w];
             prefix[B] = total * Hkv;
         }
@@ -289,9 +318,11 @@ __global__ void __launch_bounds__(kMaxWarps * 32, ctas_per_sm(NT)) decode_int4_k
     }
 
     // ---- zero rows of empty contexts
+#pragma unroll 1
     for (int32_t i = blockIdx.x; i < B; i += gridDim.x) {
         if (prefix[i + 1] != prefix[i]) continue;
         uint4* row = reinterpret_cast<uint4*>(p.out + (int64_t)i * p.H * D);
+#pragma unroll 1
         for (int v = tid; v < p.H * D / 8; v += threads) row[v] = make_uint4(0, 0, 0, 0);
     }
 
@@ -418,13 +449,12 @@ __global__ void __launch_bounds__(kMaxWarps * 32, ctas_per_sm(NT)) decode_int4_k
         uint32_t qb[NT][NG][4][2];      // Q^T fragments: lane holds query head 8 nt + cr
         float qsum[NT][NG][2];          // sum of q times scale, heads 8 nt + 2 c4 + {0, 1}
         float qsc = 0.f;                // from an MMA score over a step to a base-2 logit
-        auto load_q = [&](const Cursor& s) {
-            // In k-step ks of a group the lane's fragment pairs values v0 + {0, 4} (b0) and
-            // v0 + {1, 5} (b1), v0 = 16 c4 + 8 (ks / 2) + 2 (ks % 2): the nibbles that the
-            // masks leave.  q is scaled by 2^e so that its largest value lies in
-            // [2^14, 2^15), and by 1/16 more where it meets upper nibbles.
-            float amax = 0.f;
-            uint32_t raw[NT][NG][8];
+        // In k-step ks of a group the lane's fragment pairs values v0 + {0, 4} (b0) and
+        // v0 + {1, 5} (b1), v0 = 16 c4 + 8 (ks / 2) + 2 (ks % 2): the nibbles that the
+        // masks leave.  q is scaled by 2^e so that its largest value lies in [2^14, 2^15),
+        // and by 1/16 more where it meets upper nibbles.
+        uint32_t raw[NT][NG][8];
+        auto fetch_q = [&](const Cursor& s) {
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
                 const int h = 8 * nt + cr;
@@ -439,6 +469,9 @@ __global__ void __launch_bounds__(kMaxWarps * 32, ctas_per_sm(NT)) decode_int4_k
                     raw[nt][g][4] = b.x, raw[nt][g][5] = b.y, raw[nt][g][6] = b.z, raw[nt][g][7] = b.w;
                 }
             }
+        };
+        auto convert_q = [&]() {
+            float amax = 0.f;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -474,11 +507,6 @@ __global__ void __launch_bounds__(kMaxWarps * 32, ctas_per_sm(NT)) decode_int4_k
         };
 
         Cursor s = start;
-        load_q(s);
-        for (int k = 0; k < S; ++k) {   // a group per stage, empty or not
-            if (ipos < hi) issue();
-            commit_group();
-        }
         uint32_t stage = ring;   // the chunk to compute
         // Offsets of this lane in a stage: K rows cr, V rows 2 c4 + {0, 1} in its order.
         const uint32_t odd = c4 & 1;
@@ -488,7 +516,17 @@ __global__ void __launch_bounds__(kMaxWarps * 32, ctas_per_sm(NT)) decode_int4_k
         const uint32_t perm0 = odd ? 0x1054 : 0x5410, perm1 = odd ? 0x3276 : 0x7632;
         const uint32_t krow = krows + cr * NG * 8, vrow = vrows + cr * NG * 8;
         int segn = 0;
+#pragma unroll 1
         for (int32_t pos = lo; pos < hi;) {
+            fetch_q(s);
+            if (segn == 0) {
+#pragma unroll 1
+                for (int k = 0; k < S; ++k) {   // a group per stage, empty or not
+                    if (ipos < hi) issue();
+                    commit_group();
+                }
+            }
+            convert_q();
             const int32_t c0 = s.c, c_end = min(s.nc, s.c + hi - pos);
             const int32_t n = clamp_len(__ldg(p.context_lens + s.i), max_len);
             // Running state for heads 8 nt + 2 c4 + {0, 1}: maximum, sum, sums of P times
@@ -512,7 +550,14 @@ __global__ void __launch_bounds__(kMaxWarps * 32, ctas_per_sm(NT)) decode_int4_k
             // P times V's step is kept in f16 range by 2^vexp, which o carries.
             int vexp = 126;
             int32_t valid = n - c0 * kChunk;   // tokens of the context from the chunk on
+#pragma unroll 1
             for (int32_t c = c0; c < c_end; ++c, valid -= kChunk) {
+                const int32_t done = pos - lo + c - c0;
+#pragma unroll 1
+                for (int t = 0; t < kPaceTries; ++t) {   // pacing only: giving up is harmless
+                    if (__all_sync(0xffffffffu, pace[lane < nw ? lane : 0] + kLead >= done)) break;
+                    __nanosleep(100);
+                }
                 wait_group<S - 1>();
                 __syncwarp();   // every lane's copies have landed
                 {
@@ -694,6 +739,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, ctas_per_sm(NT)) decode_int4_k
                     }
                 }
                 __syncwarp();   // every lane has read the stage: it may be filled again
+                if (lane == 0) pace[warp] = done + 1;
                 stage = stage + kStage == ring + S * kStage ? ring : stage + kStage;
                 if (ipos < hi) issue();
                 commit_group();
@@ -729,7 +775,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, ctas_per_sm(NT)) decode_int4_k
                     const float inv = whole ? 1.f / l_run[nt][j] : 1.f;
                     if (!whole && cr == 0) {
                         slot[h] = m_run[nt][j];
-                        slot[kMaxG + h] = l_run[nt][j];
+                        slot[G + h] = l_run[nt][j];
                     }
 #pragma unroll
                     for (int g = 0; g < NG; ++g) {
@@ -747,7 +793,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, ctas_per_sm(NT)) decode_int4_k
                                 make_uint4(pa::pack2<kBF16>(v[0], v[1]), pa::pack2<kBF16>(v[2], v[3]),
                                            pa::pack2<kBF16>(v[4], v[5]), pa::pack2<kBF16>(v[6], v[7]));
                         } else {
-                            float4* to = reinterpret_cast<float4*>(slot + 2 * kMaxG + h * D + at_d);
+                            float4* to = reinterpret_cast<float4*>(slot + slot_head(G) + h * D + at_d);
                             to[0] = make_float4(v[0], v[1], v[2], v[3]);
                             to[1] = make_float4(v[4], v[5], v[6], v[7]);
                         }
@@ -760,162 +806,218 @@ __global__ void __launch_bounds__(kMaxWarps * 32, ctas_per_sm(NT)) decode_int4_k
                 r.c0 = c0;
                 r.end = c_end;
                 r.nc = s.nc;
-                r.at = at;
                 r.a = s.a;
             }
             ++segn;
-            if (pos < hi) {
-                s = next_pair(prefix, Hkv, s);
-                load_q(s);
-            }
+            if (pos < hi) s = next_pair(prefix, Hkv, s);
         }
     }
+    if (lane == 0) pace[warp] = INT32_MAX - kLead;
     __syncthreads();
 
     // ====================== runs of one pair in several warps ======================
-    // Runs lie in list order, so a pair's runs are neighbours.  The warp that holds a
-    // pair's first run merges it if the pair lies in this CTA, and leaves it to the
-    // whole CTA if other CTAs share it (at most the CTA's first and last pair).
-    auto merged4 = [&](int first, int count, int h, int d4, float& M, float& l) -> float4 {
-        M = -INFINITY;
-        for (int k = 0; k < count; ++k)
-            if (runs[first + k].a == runs[first].a)
-                M = fmaxf(M, reinterpret_cast<const float*>(smem + runs[first + k].at)[h]);
-        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-        l = 0.f;
-        for (int k = 0; k < count; ++k) {
-            if (runs[first + k].a != runs[first].a) continue;
-            const float* slot = reinterpret_cast<const float*>(smem + runs[first + k].at);
-            const float f = pa::fast_exp2(slot[h] - M);
-            const float4 x = *reinterpret_cast<const float4*>(slot + 2 * kMaxG + h * D + d4);
-            l += f * slot[kMaxG + h];
-            v.x += f * x.x;
-            v.y += f * x.y;
-            v.z += f * x.z;
-            v.w += f * x.w;
-        }
-        return v;
+    // Runs lie in list order: a pair's runs are neighbours, warps without a second run
+    // between them.  Lane k of every warp looks at run k (such gaps go with the pair
+    // before them): whether it leads its pair, and whether the pair is whole or other CTAs
+    // hold some of it (true of at most the CTA's first and last pair).
+    const Run my = runs[lane < 2 * nw ? lane : 0];
+    const bool valid_run = lane < 2 * nw && my.a >= 0;
+    const uint32_t upto = 0xffffffffu >> (31 - lane);
+    const uint32_t before = __ballot_sync(0xffffffffu, valid_run) & upto;
+    const int32_t pair_of = __shfl_sync(0xffffffffu, my.a, before ? 31 - __clz(before) : 0);
+    const int32_t seg = before ? pair_of : -1;
+    const uint32_t same = __match_any_sync(0xffffffffu, seg);      // a contiguous set
+    const int seg_last = 31 - __clz(same);
+    const bool leads = valid_run && (same & upto) == (1u << lane);
+    const uint32_t in_pair = same & __ballot_sync(0xffffffffu, valid_run);
+    const int32_t pair_end = __shfl_sync(0xffffffffu, my.end, in_pair ? 31 - __clz(in_pair) : 0);
+    const bool shared = my.c0 != 0 || pair_end != my.nc;
+    const uint32_t lead = __ballot_sync(0xffffffffu, leads);
+    const uint32_t open = __ballot_sync(0xffffffffu, leads && shared);
+    // A warp's first run has its slot, a later one its ring.
+    auto slot_at = [&](int k) {
+        return reinterpret_cast<float*>(smem + (k & 1 ? (uint32_t)(k >> 1) * S * kStage
+                                                      : L.slots + (uint32_t)(k >> 1) * slot_floats(G, D) * 4));
     };
+    // A CTA's first partial holds the pair that its share begins in or with, its second
+    // the one that begins later.
+    auto partial_at = [&](int32_t a) {
+        return p.partials + (2 * (int64_t)blockIdx.x + (cta_lo >= a ? 0 : 1)) * partial_floats(D);
+    };
+    // Head by head: maximum and sum over each pair's runs (a segmented scan over the
+    // lanes), each run's factor 2^(m_k - M) in place of its maximum.
+#pragma unroll 1
+    for (int h = warp; h < G; h += nw) {
+        float* slot = slot_at(lane < 2 * nw ? lane : 0);
+        const float m = valid_run ? slot[h] : -INFINITY;
+        float M = m;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const float y = __shfl_up_sync(0xffffffffu, M, o);
+            if (lane >= o && (same >> (lane - o) & 1)) M = fmaxf(M, y);
+        }
+        M = __shfl_sync(0xffffffffu, M, seg_last);
+        const float f = valid_run ? pa::fast_exp2(m - M) : 0.f;
+        float l = valid_run ? f * slot[G + h] : 0.f;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const float y = __shfl_up_sync(0xffffffffu, l, o);
+            if (lane >= o && (same >> (lane - o) & 1)) l += y;
+        }
+        l = __shfl_sync(0xffffffffu, l, seg_last);
+        if (valid_run) slot[h] = f;
+        if (leads && !shared) slot[G + h] = 1.f / l;
+        if (leads && shared) {
+            partial_at(my.a)[h] = M;
+            partial_at(my.a)[kMaxG + h] = l;
+        }
+    }
+    if (warp == 0 && leads) {   // the pairs in order, for the loop below
+        const int at = __popc(lead & (upto >> 1));
+        runs[at].pad = lane | (shared ? 256 : 0);
+        runs[at].at = in_pair;
+    }
+    __syncthreads();
     auto store4 = [&](int32_t i, int32_t h, int d4, float4 v, float inv) {
         *reinterpret_cast<uint2*>(p.out + ((int64_t)i * p.H + h) * D + d4) =
             make_uint2(pa::pack2<kBF16>(v.x * inv, v.y * inv), pa::pack2<kBF16>(v.z * inv, v.w * inv));
     };
-    auto span = [&](int first) {   // runs from `first` on that may belong to its pair
-        int last = first;
-        for (int k = first + 1; k < 2 * nw; ++k)
-            if (runs[k].a == runs[first].a) last = k;
-        return last - first + 1;
-    };
-    for (int k = 2 * warp; k < 2 * warp + 2; ++k) {
-        const int32_t a = runs[k].a;
-        if (a < 0) continue;
-        bool leads = true;
-        for (int b = 0; b < k; ++b) leads &= runs[b].a != a;
-        if (!leads) continue;
-        const int count = span(k);
-        if (runs[k].c0 != 0 || runs[k + count - 1].end != runs[k].nc) {
-            if (lane == 0) open_run[runs[k].a > cta_lo ? 1 : 0] = k;
-            continue;
+    const int outs = G * D / 4;     // four outputs each
+#pragma unroll 1
+    for (int x = tid; x < __popc(lead) * outs; x += threads) {
+        const int at = x / outs, e = x - at * outs;
+        const int k = runs[at].pad & 255;
+        const int h = e / (D / 4), d4 = e % (D / 4) * 4;
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+        for (uint32_t set = runs[at].at; set; set &= set - 1) {
+            const float* slot = slot_at(__ffs(set) - 1);
+            const float f = slot[h];
+            const float4 y = *reinterpret_cast<const float4*>(slot + slot_head(G) + h * D + d4);
+            v.x += f * y.x;
+            v.y += f * y.y;
+            v.z += f * y.z;
+            v.w += f * y.w;
         }
-        for (int e = lane; e < G * D / 4; e += 32) {
-            const int h = e / (D / 4), d4 = (e % (D / 4)) * 4;
-            float M, l;
-            const float4 v = merged4(k, count, h, d4, M, l);
-            store4(runs[k].i, runs[k].g * G + h, d4, v, 1.f / l);
-        }
+        if (runs[at].pad & 256)
+            *reinterpret_cast<float4*>(partial_at(runs[k].a) + 2 * kMaxG + e * 4) = v;
+        else
+            store4(runs[k].i, runs[k].g * G + h, d4, v, slot_at(k)[G + h]);
     }
-    __syncthreads();
+    if (!open) return;
 
     // ================= pairs shared with other CTAs, by the whole CTA =================
-    constexpr int kSlot = slot_floats(kMaxG, D);
-    int32_t* is_last = open_run + 2;
-    for (int which = 0; which < 2; ++which) {
-        const int k = open_run[which];
-        if (k < 0) continue;
-        const Run r = runs[k];
-        const int count = span(k);
-        const int64_t c_first = cut.part(r.a), c_last = cut.part(r.a + r.nc - 1);
-        // A CTA's first slot holds the pair that its share begins in or with, its
-        // second the one that begins later.
-        float* ps = p.partials + (2 * (int64_t)blockIdx.x + (cta_lo >= r.a ? 0 : 1)) * kSlot;
-        for (int e = tid; e < G * D / 4; e += threads) {
-            const int h = e / (D / 4), d4 = (e % (D / 4)) * 4;
-            float M, l;
-            const float4 v = merged4(k, count, h, d4, M, l);
-            *reinterpret_cast<float4*>(ps + 2 * kMaxG + h * D + d4) = v;
-            if (d4 == 0) {
-                ps[h] = M;
-                ps[kMaxG + h] = l;
+    // Publish: the barrier orders every thread's stores before the ticket's release; the
+    // ticket names the pair's last CTA and, for it, acquires the other CTAs' partials.
+    constexpr int kPartial = partial_floats(D);
+    const int n_open = __popc(open);   // one or two
+    auto open_lead = [&](int w) { return w ? 31 - __clz(open) : __ffs(open) - 1; };
+    __syncthreads();
+    if (warp < n_open && lane == 0) {
+        const Run& r = runs[open_lead(warp)];
+        int32_t* ticket = p.counters + (int64_t)r.i * Hkv + r.g;
+        const int last = pa::atomic_add_acq_rel_gpu(ticket, 1) == cut.part(r.a + r.nc - 1) - cut.part(r.a);
+        if (last) atomicExch(ticket, 0);   // ready for the next launch
+        is_last[warp] = last;
+    }
+    __syncthreads();
+#pragma unroll 1
+    for (int w = 0; w < n_open; ++w) {
+        if (!is_last[w]) continue;
+        const Run r = runs[open_lead(w)];
+        const int c_first = cut.part(r.a), n = cut.part(r.a + r.nc - 1) - c_first + 1;
+        const float* first = p.partials + (2 * (int64_t)c_first + (cut.begin(c_first) == r.a ? 0 : 1)) * kPartial;
+        const float* rest = p.partials + 2 * (int64_t)c_first * kPartial;
+        // A group of threads has the outputs, four each; the groups take the partials in
+        // turn, eight loads in flight, and join through shared memory.
+        const int wide = min(outs, threads), groups = threads / wide;
+        const int grp = tid / wide;
+        float4* acc_at = reinterpret_cast<float4*>(smem);              // [groups][outs]
+        float2* ml_at = reinterpret_cast<float2*>(acc_at + threads);
+#pragma unroll 1
+        for (int e = tid - grp * wide; e < outs && grp < groups; e += wide) {
+            const int h = e / (D / 4);
+            float M = -INFINITY, l = 0.f;
+            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+            for (int c0 = grp; c0 < n; c0 += 8 * groups) {
+                float pm[8], pl[8];
+                float4 po[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const int c = c0 + j * groups;
+                    if (c < n) {
+                        const float* q = c ? rest + 2 * (int64_t)c * kPartial : first;
+                        pm[j] = __ldcg(q + h);
+                        pl[j] = __ldcg(q + kMaxG + h);
+                        po[j] = __ldcg(reinterpret_cast<const float4*>(q + 2 * kMaxG) + e);
+                    } else {
+                        pm[j] = -INFINITY;
+                        pl[j] = 0.f;
+                        po[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    }
+                }
+                float Mb = M;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) Mb = fmaxf(Mb, pm[j]);
+                if (Mb == -INFINITY) continue;
+                const float f0 = pa::fast_exp2(M - Mb);   // 0 while M = -inf
+                l *= f0;
+                acc.x *= f0;
+                acc.y *= f0;
+                acc.z *= f0;
+                acc.w *= f0;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const float f = pa::fast_exp2(pm[j] - Mb);
+                    l += f * pl[j];
+                    acc.x += f * po[j].x;
+                    acc.y += f * po[j].y;
+                    acc.z += f * po[j].z;
+                    acc.w += f * po[j].w;
+                }
+                M = Mb;
+            }
+            if (groups == 1) {
+                store4(r.i, r.g * G + h, e % (D / 4) * 4, acc, 1.f / l);
+            } else {
+                acc_at[grp * outs + e] = acc;
+                ml_at[grp * outs + e] = make_float2(M, l);
             }
         }
-        __syncthreads();
-        if (tid == 0) {
-            int32_t* ticket = p.counters + (int64_t)r.i * Hkv + r.g;
-            const int last = pa::atomic_add_acq_rel_gpu(ticket, 1) == (int)(c_last - c_first);
-            if (last) atomicExch(ticket, 0);   // ready for the next launch
-            *is_last = last;
-        }
-        __syncthreads();
-        if (*is_last) {
-            const int n = (int)(c_last - c_first + 1);
-            const int64_t slot0 = 2 * c_first + (cut.begin((int32_t)c_first) == r.a ? 0 : 1);
-            for (int e = tid; e < G * D / 4; e += threads) {
-                const int h = e / (D / 4), d4 = (e % (D / 4)) * 4;
+        if (groups > 1) {
+            __syncthreads();
+#pragma unroll 1
+            for (int e = tid; e < outs; e += threads) {
+                const int use = min(groups, n);
                 float M = -INFINITY, l = 0.f;
                 float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-                for (int c0 = 0; c0 < n; c0 += 8) {
-                    float pm[8], pl[8];
-                    float4 po[8];
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const int c = c0 + j;
-                        if (c < n) {
-                            const float* q = p.partials + (c ? 2 * (c_first + c) : slot0) * kSlot;
-                            pm[j] = __ldcg(q + h);
-                            pl[j] = __ldcg(q + kMaxG + h);
-                            po[j] = __ldcg(reinterpret_cast<const float4*>(q + 2 * kMaxG + h * D + d4));
-                        } else {
-                            pm[j] = -INFINITY;
-                            pl[j] = 0.f;
-                            po[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-                        }
-                    }
-                    float Mb = M;
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) Mb = fmaxf(Mb, pm[j]);
-                    if (Mb == -INFINITY) continue;
-                    const float f0 = pa::fast_exp2(M - Mb);   // 0 while M = -inf
-                    l *= f0;
-                    acc.x *= f0;
-                    acc.y *= f0;
-                    acc.z *= f0;
-                    acc.w *= f0;
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const float f = pa::fast_exp2(pm[j] - Mb);
-                        l += f * pl[j];
-                        acc.x += f * po[j].x;
-                        acc.y += f * po[j].y;
-                        acc.z += f * po[j].z;
-                        acc.w += f * po[j].w;
-                    }
-                    M = Mb;
+#pragma unroll 1
+                for (int q = 0; q < use; ++q) M = fmaxf(M, ml_at[q * outs + e].x);
+#pragma unroll 1
+                for (int q = 0; q < use; ++q) {
+                    const float2 ml = ml_at[q * outs + e];
+                    const float4 y = acc_at[q * outs + e];
+                    const float f = pa::fast_exp2(ml.x - M);
+                    l += f * ml.y;
+                    acc.x += f * y.x;
+                    acc.y += f * y.y;
+                    acc.z += f * y.z;
+                    acc.w += f * y.w;
                 }
-                store4(r.i, r.g * G + h, d4, acc, 1.f / l);
+                store4(r.i, r.g * G + e / (D / 4), e % (D / 4) * 4, acc, 1.f / l);
             }
+            __syncthreads();
         }
     }
 }
 
 // ---- host side -----------------------------------------------------------------
 
-// Shared memory per CTA that leaves room for ctas_per_sm(NT) of them on an SM.
-uint32_t smem_budget(int NT) { return (NT == 1 ? 113 : 226) * 1024; }
-
 // As many warps as shared memory holds rings and slots for; 0: not even four.
 int choose_warps(int D, int G, int B) {
-    for (int w = kMaxWarps; w >= 4; --w)
-        if (make_layout(D, G, B, w).total <= smem_budget(G <= 8 ? 1 : 2)) return w;
+    for (int w = max_warps(G <= 8 ? 1 : 2); w >= 4; --w)
+        if (make_layout(D, G, B, w).total <= kSmemBudget) return w;
     return 0;
 }
 
@@ -931,12 +1033,12 @@ pa_status launch(const Int4Params& p, cudaStream_t stream) {
         std::lock_guard<std::mutex> g(mu);
         if (!(done >> dev & 1)) {
             if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                     (int)smem_budget(NT)) != cudaSuccess)
+                                     (int)kSmemBudget) != cudaSuccess)
                 return PA_ERR_CUDA;
             done |= 1ull << dev;
         }
     }
-    int ctas = pa::device_sm_count() * ctas_per_sm(NT);
+    int ctas = pa::device_sm_count();
     if (ctas <= 0) return PA_ERR_CUDA;
     if (ctas > kMaxCtas) ctas = kMaxCtas;
     const Layout L = make_layout(D, p.G, p.B, p.warps);
