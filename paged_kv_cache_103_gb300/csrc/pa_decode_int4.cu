@@ -70,12 +70,6 @@ struct Int4Params {
 __host__ __device__ constexpr int max_warps(int NT) { return NT == 1 ? 16 : 8; }
 constexpr uint32_t kSmemBudget = 227 * 1024;
 
-// A warp may be this many chunks ahead of the slowest one of its CTA.  The schedulers
-// favour some warps; left alone, those end early and the others finish on a half-empty
-// SM (two 8-warp CTAs per SM ended 25 us apart of 109).
-constexpr int kLead = 4;
-constexpr int kPaceTries = 1 << 14;
-
 // One partial result in shared memory: row maxima [G], row sums [G], padding to 16 bytes,
 // outputs [G][D]; in the workspace: maxima and sums [kMaxG] each.
 __host__ __device__ constexpr int slot_head(int G) { return (2 * G + 3) & ~3; }
@@ -91,7 +85,7 @@ struct Run {
 };
 
 struct Layout {
-    uint32_t stage, rows, slots, runs, last, pace, scan, prefix, total;
+    uint32_t stage, rows, slots, runs, last, scan, prefix, total;
 };
 
 __host__ __device__ inline Layout make_layout(int D, int G, int B, int warps) {
@@ -102,8 +96,7 @@ __host__ __device__ inline Layout make_layout(int D, int G, int B, int warps) {
     L.slots = L.rows + warps * 2 * kChunk * (D / 64) * 8;   // a slot per warp
     L.runs = L.slots + warps * slot_floats(G, D) * 4;       // [2 * warps]
     L.last = L.runs + 2 * warps * (uint32_t)sizeof(Run);     // "the last CTA of the pair"
-    L.pace = L.last + 8;                                     // chunks done by each warp
-    L.scan = L.pace + warps * 4;
+    L.scan = L.last + 8;
     L.prefix = L.scan + warps * 4;                          // [B + 1]
     L.total = L.prefix + (uint32_t)(B + 1) * 4;
     return L;
@@ -261,7 +254,6 @@ __global__ void __launch_bounds__(max_warps(NT) * 32, 1) decode_int4_kernel(cons
     const uint32_t sbase = pa::smem_addr(smem);
     Run* runs = reinterpret_cast<Run*>(smem + L.runs);
     int32_t* is_last = reinterpret_cast<int32_t*>(smem + L.last);
-    volatile int32_t* pace = reinterpret_cast<int32_t*>(smem + L.pace);
     int32_t* scan = reinterpret_cast<int32_t*>(smem + L.scan);
     int32_t* prefix = reinterpret_cast<int32_t*>(smem + L.prefix);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -298,7 +290,6 @@ __global__ void __launch_bounds__(max_warps(NT) * 32, 1) decode_int4_kernel(cons
         }
         if (lane == 31) scan[warp] = x;
         if (tid < 2 * nw) runs[tid].a = -1;
-        if (tid < nw) pace[tid] = 0;
         __syncthreads();
         int32_t run = x - local;
 #pragma unroll 1
@@ -350,32 +341,45 @@ __global__ void __launch_bounds__(max_warps(NT) * 32, 1) decode_int4_kernel(cons
         const uint32_t lcol = lane % (kRow / 16) * 16;
         constexpr uint32_t kTile = kRow << bs_shift, kSTile = kSRow << bs_shift;
         const uint32_t heads = (uint32_t)(Hkv / p.subs);
+        // Bytes between blocks; a pass lies in one block unless blocks are shorter than it.
+        const uint32_t stride = heads * kTile, sstride = heads * kSTile;
+        constexpr bool kOneBlock = kPass <= bmask + 1;
+        const uint32_t lane_bytes = kOneBlock ? lane * 16 : (lrow & bmask) * kRow + lcol;
+        const uint8_t* scales = lane % (2 * kScaleLanes) < kScaleLanes ? p.k_scale : p.v_scale;
         const uint64_t policy = pa::l2_policy_evict_first();
-        const int64_t k_to_v = p.v_cache - p.k_cache;
-        const uint8_t* scales = lane < kScaleLanes ? p.k_scale : p.v_scale;
         constexpr int bpc = kChunk >> bs_shift;     // blocks per chunk: 4, 2 or 1
         // A pair's table entries, 32 at a time (lane l holds the window's entry l), with
-        // the window after it loaded a step ahead.  (The next pair's first window is not:
-        // its registers cost more than the wait, which other warps fill.)
+        // the window after it loaded a step ahead; an entry past the context is -1, as is
+        // an id outside the pool.  (The next pair's first window is not loaded ahead: its
+        // registers cost more than the wait, which other warps fill.)
         struct Walk {
             Cursor s;
-            uint32_t head;           // the cache's KV head
-            int32_t at, left;        // first block of the chunk: in the window, and how many follow
+            int32_t at;              // the chunk's first block in the window
             int32_t went, wnext;
-            int32_t next;            // this lane's entry after wnext's
+            int32_t next, nb;        // this lane's entry after wnext's; blocks of the context
+            const uint8_t *k, *v, *sc;   // the pair's KV head in each tensor, at this lane's bytes
+        };
+        auto entry = [&](int32_t i, int32_t j, int32_t nb) {
+            if (j >= nb) return -1;
+            const int32_t blk = __ldg(p.block_tables + (int64_t)i * p.max_blocks + j);
+            if ((uint32_t)blk < (uint32_t)p.num_blocks) return blk;
+            pa::raise_error(p.err, PA_DEVERR_BLOCK_ID);
+            return -1;
         };
         auto open = [&](const Cursor& s) {
             Walk w;
             w.s = s;
             const int32_t j0 = (s.c * kChunk) >> bs_shift, j = j0 + lane;
-            const int32_t* row = p.block_tables + (int64_t)s.i * p.max_blocks + j;
             const int32_t n = clamp_len(__ldg(p.context_lens + s.i), max_len);
-            w.head = (uint32_t)(s.g / p.subs);
+            const uint32_t head = (uint32_t)(s.g / p.subs);
             w.at = 0;
-            w.left = ((n + bmask) >> bs_shift) - j0;
-            w.went = j < p.max_blocks ? __ldg(row) : -1;
-            w.wnext = j + 32 < p.max_blocks ? __ldg(row + 32) : -1;
+            w.nb = (n + bmask) >> bs_shift;
+            w.went = entry(s.i, j, w.nb);
+            w.wnext = entry(s.i, j + 32, w.nb);
             w.next = j + 64;
+            w.k = p.k_cache + (uint64_t)head * kTile + lane_bytes;
+            w.v = p.v_cache + (uint64_t)head * kTile + lane_bytes;
+            w.sc = scales + (uint64_t)head * kSTile + (srow & bmask) * kSRow;
             return w;
         };
         int32_t ipos = lo;              // next chunk to issue
@@ -386,57 +390,42 @@ __global__ void __launch_bounds__(max_warps(NT) * 32, 1) decode_int4_kernel(cons
         // pool are not read: zeros take their place (a step and a minimum of zero: rows of
         // zeros).
         auto issue = [&]() {
-            bool bad = false;
-            // tile index of the lane's row of pass or scales; b: the row's block in the chunk
-            auto tile_of = [&](int b, bool& ok) {
-                const int32_t blk = __shfl_sync(0xffffffffu, cur.went, cur.at + b);
-                ok = b < cur.left && (uint32_t)blk < (uint32_t)p.num_blocks;
-                bad |= b < cur.left && !ok;
-                return (uint64_t)((ok ? (uint32_t)blk : 0u) * heads + cur.head);
-            };
-            if constexpr (kPass <= bmask + 1) {   // a pass lies in one block
-                constexpr int kPasses = (bmask + 1) / kPass < kChunk / kPass ? (bmask + 1) / kPass : kChunk / kPass;
+            auto block = [&](int b) { return __shfl_sync(0xffffffffu, cur.went, cur.at + b); };
+            if constexpr (kOneBlock) {
+                constexpr int kPasses = kChunk / kPass / bpc;
 #pragma unroll
                 for (int b = 0; b < bpc; ++b) {
-                    bool ok;
-                    const uint8_t* from = p.k_cache + tile_of(b, ok) * kTile + lane * 16;
-                    const uint8_t* vfrom = from + k_to_v;
+                    const int32_t blk = block(b);
+                    const uint64_t at = (uint64_t)(uint32_t)max(blk, 0) * stride;
                     const uint32_t to = ito + b * kTile + lane * 16;
 #pragma unroll
                     for (int t = 0; t < kPasses; ++t) {
-                        copy16(to + t * 512, from + t * 512, ok, policy);
-                        copy16(to + t * 512 + kCodes, vfrom + t * 512, ok, policy);
+                        copy16(to + t * 512, cur.k + at + t * 512, blk >= 0, policy);
+                        copy16(to + t * 512 + kCodes, cur.v + at + t * 512, blk >= 0, policy);
                     }
                 }
             } else {
 #pragma unroll
                 for (int t = 0; t < kChunk / kPass; ++t) {
-                    const int row = t * kPass + lrow;
-                    bool ok;
-                    const uint8_t* from = p.k_cache + tile_of(row >> bs_shift, ok) * kTile +
-                                          ((row & bmask) * kRow + lcol);
+                    const int32_t blk = block((t * kPass + lrow) >> bs_shift);
+                    const uint64_t at = (uint64_t)(uint32_t)max(blk, 0) * stride;
                     const uint32_t to = ito + t * 512 + lane * 16;
-                    copy16(to, from, ok, policy);
-                    copy16(to + kCodes, from + k_to_v, ok, policy);
+                    copy16(to, cur.k + at, blk >= 0, policy);
+                    copy16(to + kCodes, cur.v + at, blk >= 0, policy);
                 }
             }
-            {
-                bool ok;
-                const uint8_t* from = scales + tile_of(srow >> bs_shift, ok) * kSTile +
-                                      (srow & bmask) * kSRow;
-                if (lane < 2 * kScaleLanes) copy16(ito + 2 * kCodes + lane * 16, from, ok, policy);
-            }
-            if (bad) pa::raise_error(p.err, PA_DEVERR_BLOCK_ID);
+            const int32_t sblk = block(srow >> bs_shift);
+            if (lane < 2 * kScaleLanes)
+                copy16(ito + 2 * kCodes + lane * 16, cur.sc + (uint64_t)(uint32_t)max(sblk, 0) * sstride,
+                       sblk >= 0, policy);
             ito = ito + kStage == ring + S * kStage ? ring : ito + kStage;
             ++ipos;
             if (++cur.s.c < cur.s.nc) {
-                cur.left -= bpc;
                 cur.at += bpc;
                 if (cur.at == 32) {     // a window is a whole number of chunks
                     cur.at = 0;
                     cur.went = cur.wnext;
-                    cur.wnext = cur.next < p.max_blocks
-                        ? __ldg(p.block_tables + (int64_t)cur.s.i * p.max_blocks + cur.next) : -1;
+                    cur.wnext = entry(cur.s.i, cur.next, cur.nb);
                     cur.next += 32;
                 }
             } else if (ipos < hi) {
@@ -529,14 +518,15 @@ __global__ void __launch_bounds__(max_warps(NT) * 32, 1) decode_int4_kernel(cons
             convert_q();
             const int32_t c0 = s.c, c_end = min(s.nc, s.c + hi - pos);
             const int32_t n = clamp_len(__ldg(p.context_lens + s.i), max_len);
-            // Running state for heads 8 nt + 2 c4 + {0, 1}: maximum, sum, sums of P times
+            // Running state for heads 8 nt + 2 c4 + {0, 1}: the negative of the
+            // maximum (bias; the logits below are relative to it), sum, sums of P times
             // V's minima; o: rows are values 64 g + 8 cr + u (e < 2) and + 4 + u.
-            float m_run[NT][NJ], l_run[NT][NJ], lowv[NT][NG][NJ], o[NG][4][NT][4];
+            float bias[NT][NJ], l_run[NT][NJ], lowv[NT][NG][NJ], o[NG][4][NT][4];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
                 for (int j = 0; j < NJ; ++j) {
-                    m_run[nt][j] = -INFINITY;
+                    bias[nt][j] = 0.f;
                     l_run[nt][j] = 0.f;
 #pragma unroll
                     for (int g = 0; g < NG; ++g) lowv[nt][g][j] = 0.f;
@@ -547,17 +537,13 @@ __global__ void __launch_bounds__(max_warps(NT) * 32, 1) decode_int4_kernel(cons
                     for (int u = 0; u < 4; ++u)
                         o[g][u][nt][0] = o[g][u][nt][1] = o[g][u][nt][2] = o[g][u][nt][3] = 0.f;
             }
+            bool fresh = true;   // no maximum yet
             // P times V's step is kept in f16 range by 2^vexp, which o carries.
             int vexp = 126;
+            float vup = pa::exp2_int(126);
             int32_t valid = n - c0 * kChunk;   // tokens of the context from the chunk on
 #pragma unroll 1
             for (int32_t c = c0; c < c_end; ++c, valid -= kChunk) {
-                const int32_t done = pos - lo + c - c0;
-#pragma unroll 1
-                for (int t = 0; t < kPaceTries; ++t) {   // pacing only: giving up is harmless
-                    if (__all_sync(0xffffffffu, pace[lane < nw ? lane : 0] + kLead >= done)) break;
-                    __nanosleep(100);
-                }
                 wait_group<S - 1>();
                 __syncwarp();   // every lane's copies have landed
                 {
@@ -589,32 +575,33 @@ __global__ void __launch_bounds__(max_warps(NT) * 32, 1) decode_int4_kernel(cons
                     // steps with the score's factor, V's with 2^vexp, for all lanes to read
                     float rs = 1.f;   // what o is to be multiplied by
                     {
-                        float kv[2 * NG], vv[2 * NG], vmax = 0.f;
+                        float kv[2 * NG], vv[2 * NG];
                         load_f16_scales<NG>(st_at, kv);
                         load_f16_scales<NG>(st_at + kScales, vv);
+                        if (lane >= valid)   // a row past the context may hold anything
 #pragma unroll
-                        for (int g = 0; g < NG; ++g) {
-                            // rows past the context may hold anything: weightless
-                            vv[2 * g] = lane < valid ? vv[2 * g] : 0.f;
-                            vv[2 * g + 1] = lane < valid ? vv[2 * g + 1] : 0.f;
-                            vmax = fmaxf(vmax, vv[2 * g]);
-                            kv[2 * g] *= qsc;
-                        }
-                        vmax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(vmax)));
-                        // P <= 2^kLazy, so P times a step stays below 2^15
-                        const int e = vmax > 0.f ? min(vexp, 133 - pa::biased_exponent(vmax)) : vexp;
-                        if (e < vexp) {
+                            for (int g = 0; g < 2 * NG; ++g) vv[g] = 0.f;
+                        float vmax = vv[0];
+#pragma unroll
+                        for (int g = 1; g < NG; ++g) vmax = fmaxf(vmax, vv[2 * g]);
+                        // P <= 2^kLazy and steps below 2^7: their product stays below 2^15
+                        if (__any_sync(0xffffffffu, vmax * vup >= 128.f)) {
+                            vmax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(vmax)));
+                            const int e = 133 - pa::biased_exponent(vmax);   // < vexp
                             rs = e - vexp >= -126 ? pa::exp2_int(e - vexp) : 0.f;
                             vexp = e;
+                            vup = pa::exp2_int(e);
                         }
-                        const float up = pa::exp2_int(vexp);
 #pragma unroll
-                        for (int g = 0; g < NG; ++g) vv[2 * g] *= up;
+                        for (int g = 0; g < NG; ++g) {
+                            kv[2 * g] *= qsc;
+                            vv[2 * g] *= vup;
+                        }
                         store_row<NG>(krows + lane * NG * 8, kv);
                         store_row<NG>(vrows + lane * NG * 8, vv);
                     }
                     __syncwarp();
-                    // ---- base-2 logits
+                    // ---- base-2 logits, relative to the running maxima
                     float x[kTiles][NT][2][NJ];   // [key half][head]
 #pragma unroll
                     for (int mt = 0; mt < kTiles; ++mt)
@@ -626,10 +613,11 @@ __global__ void __launch_bounds__(max_warps(NT) * 32, 1) decode_int4_kernel(cons
                             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                                 for (int j = 0; j < NJ; ++j) {
-                                    float v = kv[1] * qsum[nt][0][j] + kv[0] * st[mt][0][nt][2 * r + j];
+                                    float v = bias[nt][j];
 #pragma unroll
-                                    for (int g = 1; g < NG; ++g)
-                                        v += kv[2 * g + 1] * qsum[nt][g][j] + kv[2 * g] * st[mt][g][nt][2 * r + j];
+                                    for (int g = 0; g < NG; ++g) v += kv[2 * g + 1] * qsum[nt][g][j];
+#pragma unroll
+                                    for (int g = 0; g < NG; ++g) v += kv[2 * g] * st[mt][g][nt][2 * r + j];
                                     x[mt][nt][r][j] = v;
                                 }
                         }
@@ -645,7 +633,7 @@ __global__ void __launch_bounds__(max_warps(NT) * 32, 1) decode_int4_kernel(cons
                                         if (16 * mt + cr + 8 * r >= valid) x[mt][nt][r][j] = -INFINITY;
                     // ---- online softmax per head
                     float top[NT][NJ];
-                    bool above = rs != 1.f;
+                    bool above = fresh || rs != 1.f;
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -654,7 +642,7 @@ __global__ void __launch_bounds__(max_warps(NT) * 32, 1) decode_int4_kernel(cons
 #pragma unroll
                             for (int mt = 0; mt < kTiles; ++mt)
                                 top[nt][j] = fmaxf(top[nt][j], fmaxf(x[mt][nt][0][j], x[mt][nt][1][j]));
-                            above |= top[nt][j] > m_run[nt][j] + kLazy;
+                            above |= top[nt][j] > kLazy;
                         }
                     if (__any_sync(0xffffffffu, above)) {
 #pragma unroll
@@ -665,9 +653,13 @@ __global__ void __launch_bounds__(max_warps(NT) * 32, 1) decode_int4_kernel(cons
                                 v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
                                 v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
                                 v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
-                                const float m_new = fmaxf(m_run[nt][j], v);
-                                const float a = pa::fast_exp2(m_run[nt][j] - m_new), f = a * rs;
-                                m_run[nt][j] = m_new;
+                                const float up = fresh ? v : fmaxf(v, 0.f);
+                                const float a = fresh ? 0.f : pa::fast_exp2(-up), f = a * rs;
+                                bias[nt][j] -= up;
+#pragma unroll
+                                for (int mt = 0; mt < kTiles; ++mt)
+#pragma unroll
+                                    for (int r = 0; r < 2; ++r) x[mt][nt][r][j] -= up;
                                 l_run[nt][j] *= a;
 #pragma unroll
                                 for (int g = 0; g < NG; ++g) {
@@ -680,6 +672,7 @@ __global__ void __launch_bounds__(max_warps(NT) * 32, 1) decode_int4_kernel(cons
                                 }
                             }
                     }
+                    fresh = false;
                     // ---- P, and O^T += V^T P^T
 #pragma unroll
                     for (int mt = 0; mt < kTiles; ++mt) {
@@ -693,7 +686,7 @@ __global__ void __launch_bounds__(max_warps(NT) * 32, 1) decode_int4_kernel(cons
                                 float e[2] = {0.f, 0.f};
 #pragma unroll
                                 for (int j = 0; j < NJ; ++j) {
-                                    e[j] = pa::fast_exp2(x[mt][nt][r][j] - m_run[nt][j]);
+                                    e[j] = pa::fast_exp2(x[mt][nt][r][j]);
                                     l_run[nt][j] += e[j];
                                 }
 #pragma unroll
@@ -739,7 +732,6 @@ __global__ void __launch_bounds__(max_warps(NT) * 32, 1) decode_int4_kernel(cons
                     }
                 }
                 __syncwarp();   // every lane has read the stage: it may be filled again
-                if (lane == 0) pace[warp] = done + 1;
                 stage = stage + kStage == ring + S * kStage ? ring : stage + kStage;
                 if (ipos < hi) issue();
                 commit_group();
@@ -774,7 +766,7 @@ __global__ void __launch_bounds__(max_warps(NT) * 32, 1) decode_int4_kernel(cons
                     if (h >= G) continue;
                     const float inv = whole ? 1.f / l_run[nt][j] : 1.f;
                     if (!whole && cr == 0) {
-                        slot[h] = m_run[nt][j];
+                        slot[h] = -bias[nt][j];
                         slot[G + h] = l_run[nt][j];
                     }
 #pragma unroll
@@ -812,7 +804,6 @@ __global__ void __launch_bounds__(max_warps(NT) * 32, 1) decode_int4_kernel(cons
             if (pos < hi) s = next_pair(prefix, Hkv, s);
         }
     }
-    if (lane == 0) pace[warp] = INT32_MAX - kLead;
     __syncthreads();
 
     // ====================== runs of one pair in several warps ======================
