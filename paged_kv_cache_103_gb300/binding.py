@@ -394,40 +394,59 @@ def pa_decode_noalloc(q, k_cache, v_cache, block_tables, context_lens, max_conte
            "pa_decode_noalloc")
 
 
-def _same_device(*tensors):
-    """The library launches on the current device: refuses tensors of another one."""
+# The 4-bit and block-sparse calls check every tensor against the others before a pointer
+# leaves Python.  Their smallest launches take a few microseconds, so the checks are one
+# comparison each, and the words of a refusal are put together only where there is one.
+def _ptr(t, dtype, device: int) -> int:
+    """Pointer of a contiguous tensor of ``dtype`` on the current device ``device``."""
+    if t.dtype is not dtype or t.get_device() != device or not t.is_contiguous():
+        if not t.is_cuda or not t.is_contiguous():
+            raise ValueError("contiguous CUDA tensor expected")
+        if t.dtype is not dtype:
+            raise TypeError("%s expected, got %s" % (dtype, t.dtype))
+        raise ValueError("tensor on %s, but the current device is cuda:%d" % (t.device, device))
+    return t.data_ptr()
+
+
+def _where(t, stream):
+    """(current device, raw stream) of a call whose first tensor is ``t``."""
     import torch
-    cur = torch.cuda.current_device()
-    for t in tensors:
-        if t.is_cuda and t.device.index != cur:
-            raise ValueError("tensor on %s, but the current device is cuda:%d" % (t.device, cur))
+    if not t.is_cuda:
+        raise ValueError("contiguous CUDA tensor expected")
+    device = torch._C._cuda_getDevice()
+    if stream is None:
+        return device, torch._C._cuda_getCurrentRawStream(device)
+    return device, _stream_ptr(stream)
 
 
-def _shape(name, t, shape):
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError("%s must be %s, got %s" % (name, tuple(shape), tuple(t.shape)))
+def _misfit(**shapes):
+    raise ValueError("tensors do not fit each other: " + ", ".join(
+        "%s %s (wanted %s)" % (k, tuple(t.shape), want) for k, (t, want) in shapes.items()
+        if tuple(t.shape) != want))
 
 
-def _check_int4_cache(k_cache, v_cache, k_scale, v_scale, Hkv: int, d: int):
+def _int4_cache(k_cache, v_cache, k_scale, v_scale, Hkv: int, d: int):
     """(num_blocks, block_size) of a 4-bit cache whose four tensors fit each other."""
     if k_cache.dim() != 4 or d % 64:
         raise ValueError("4-bit caches are [num_blocks, Hkv, block_size, d / 2], d a multiple of 64")
-    N, bs = int(k_cache.shape[0]), int(k_cache.shape[2])
-    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
-        _shape(name, t, (N, Hkv, bs, d // 2))
-    for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
-        _shape(name, t, (N, Hkv, bs, d // 64, 2))
+    N, _, bs, _ = k_cache.shape
+    codes, scales = (N, Hkv, bs, d // 2), (N, Hkv, bs, d // 64, 2)
+    if (k_cache.shape != codes or v_cache.shape != codes or k_scale.shape != scales
+            or v_scale.shape != scales):
+        _misfit(k_cache=(k_cache, codes), v_cache=(v_cache, codes), k_scale=(k_scale, scales),
+                v_scale=(v_scale, scales))
     return N, bs
 
 
-def _check_q8_cache(k_cache, v_cache, k_scale, v_scale, Hkv: int, d: int):
+def _q8_cache(k_cache, v_cache, k_scale, v_scale, Hkv: int, d: int):
     if k_cache.dim() != 4:
         raise ValueError("8-bit caches are [num_blocks, block_size, Hkv, d]")
-    N, bs = int(k_cache.shape[0]), int(k_cache.shape[1])
-    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
-        _shape(name, t, (N, bs, Hkv, d))
-    for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
-        _shape(name, t, (N, Hkv, bs))
+    N, bs, _, _ = k_cache.shape
+    codes, scales = (N, bs, Hkv, d), (N, Hkv, bs)
+    if (k_cache.shape != codes or v_cache.shape != codes or k_scale.shape != scales
+            or v_scale.shape != scales):
+        _misfit(k_cache=(k_cache, codes), v_cache=(v_cache, codes), k_scale=(k_scale, scales),
+                v_scale=(v_scale, scales))
     return N, bs
 
 
@@ -439,14 +458,15 @@ def pa_reshape_and_cache_int4(k_new, v_new, slot_mapping, k_cache, v_cache, k_sc
     ``[N, Hkv, bs, d / 64, 2]`` float16 (step and minimum of each group of 64)."""
     import torch
     T, Hkv, d = k_new.shape
-    N, bs = _check_int4_cache(k_cache, v_cache, k_scale, v_scale, Hkv, d)
-    _shape("v_new", v_new, k_new.shape)
-    _shape("slot_mapping", slot_mapping, (T,))
-    _same_device(k_new, v_new, slot_mapping, k_cache, v_cache, k_scale, v_scale)
+    N, bs = _int4_cache(k_cache, v_cache, k_scale, v_scale, Hkv, d)
+    if v_new.shape != k_new.shape or slot_mapping.shape != (T,):
+        _misfit(v_new=(v_new, (T, Hkv, d)), slot_mapping=(slot_mapping, (T,)))
+    dev, st = _where(k_new, stream)
+    dt, u8, f16 = k_new.dtype, torch.uint8, torch.float16
     _check(load().pa_reshape_and_cache_int4(
-        _dev(k_new), _dev(v_new, k_new.dtype), _dev(slot_mapping, torch.int64), T,
-        _dev(k_cache, torch.uint8), _dev(v_cache, torch.uint8), _dev(k_scale, torch.float16),
-        _dev(v_scale, torch.float16), N, bs, Hkv, d, _dtype_code(k_new), _stream_ptr(stream)),
+        _ptr(k_new, dt, dev), _ptr(v_new, dt, dev), _ptr(slot_mapping, torch.int64, dev), T,
+        _ptr(k_cache, u8, dev), _ptr(v_cache, u8, dev), _ptr(k_scale, f16, dev),
+        _ptr(v_scale, f16, dev), N, bs, Hkv, d, _dtype_code(k_new), st),
         "pa_reshape_and_cache_int4")
 
 
@@ -455,8 +475,8 @@ def pa_gather_cache_int4(k_cache, v_cache, k_scale, v_scale, slot_mapping, k_out
     """Reads a 4-bit cache back: row ``t`` of ``k_out/v_out [T, Hkv, d]`` (fp16/bf16)
     becomes the values at ``slot_mapping[t]``; a negative slot leaves its row as it is."""
     import torch
-    T, Hkv, d = k_out.shape
-    N, bs = _check_int4_cache(k_cache, v_cache, k_scale, v_scale, Hkv, d)
+    _, Hkv, d = k_out.shape
+    N, bs = _int4_cache(k_cache, v_cache, k_scale, v_scale, Hkv, d)
     _gather("pa_gather_cache_int4", torch.float16, k_cache, v_cache, k_scale, v_scale,
             slot_mapping, k_out, v_out, N, bs, stream)
 
@@ -466,8 +486,8 @@ def pa_gather_cache_int8(k_cache, v_cache, k_scale, v_scale, slot_mapping, k_out
     """``pa_gather_cache_int4`` for an INT8 cache (``[N, bs, Hkv, 128]`` uint8 codes,
     ``[N, Hkv, bs]`` float32 scales)."""
     import torch
-    T, Hkv, d = k_out.shape
-    N, bs = _check_q8_cache(k_cache, v_cache, k_scale, v_scale, Hkv, d)
+    _, Hkv, d = k_out.shape
+    N, bs = _q8_cache(k_cache, v_cache, k_scale, v_scale, Hkv, d)
     _gather("pa_gather_cache_int8", torch.float32, k_cache, v_cache, k_scale, v_scale,
             slot_mapping, k_out, v_out, N, bs, stream)
 
@@ -476,8 +496,8 @@ def pa_gather_cache_fp8(k_cache, v_cache, k_scale, v_scale, slot_mapping, k_out,
                         stream=None) -> None:
     """``pa_gather_cache_int8`` for a cache of E4M3 codes."""
     import torch
-    T, Hkv, d = k_out.shape
-    N, bs = _check_q8_cache(k_cache, v_cache, k_scale, v_scale, Hkv, d)
+    _, Hkv, d = k_out.shape
+    N, bs = _q8_cache(k_cache, v_cache, k_scale, v_scale, Hkv, d)
     _gather("pa_gather_cache_fp8", torch.float32, k_cache, v_cache, k_scale, v_scale,
             slot_mapping, k_out, v_out, N, bs, stream)
 
@@ -486,13 +506,14 @@ def _gather(name, scale_dtype, k_cache, v_cache, k_scale, v_scale, slot_mapping,
             bs, stream):
     import torch
     T, Hkv, d = k_out.shape
-    _shape("v_out", v_out, k_out.shape)
-    _shape("slot_mapping", slot_mapping, (T,))
-    _same_device(k_cache, v_cache, k_scale, v_scale, slot_mapping, k_out, v_out)
+    if v_out.shape != k_out.shape or slot_mapping.shape != (T,):
+        _misfit(v_out=(v_out, (T, Hkv, d)), slot_mapping=(slot_mapping, (T,)))
+    dev, st = _where(k_out, stream)
+    dt, u8 = k_out.dtype, torch.uint8
     _check(getattr(load(), name)(
-        _dev(k_cache, torch.uint8), _dev(v_cache, torch.uint8), _dev(k_scale, scale_dtype),
-        _dev(v_scale, scale_dtype), _dev(slot_mapping, torch.int64), T, _dev(k_out),
-        _dev(v_out, k_out.dtype), N, bs, Hkv, d, _dtype_code(k_out), _stream_ptr(stream)), name)
+        _ptr(k_cache, u8, dev), _ptr(v_cache, u8, dev), _ptr(k_scale, scale_dtype, dev),
+        _ptr(v_scale, scale_dtype, dev), _ptr(slot_mapping, torch.int64, dev), T,
+        _ptr(k_out, dt, dev), _ptr(v_out, dt, dev), N, bs, Hkv, d, _dtype_code(k_out), st), name)
 
 
 def pa_decode_int4(q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens,
@@ -502,20 +523,20 @@ def pa_decode_int4(q, k_cache, v_cache, k_scale, v_scale, block_tables, context_
     ``[N, Hkv, bs, d / 64, 2]`` float16."""
     import torch
     B, H, d = q.shape
-    Hkv = int(k_cache.shape[1])
-    N, bs = _check_int4_cache(k_cache, v_cache, k_scale, v_scale, Hkv, d)
-    _shape("block_tables", block_tables, (B, block_tables.shape[-1]))
-    _shape("context_lens", context_lens, (B,))
-    _shape("out", out, q.shape)
-    _same_device(q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, out, workspace)
-    _check(load().pa_decode_int4(_dev(q), _dev(k_cache, torch.uint8), _dev(v_cache, torch.uint8),
-                                 _dev(k_scale, torch.float16), _dev(v_scale, torch.float16),
-                                 _dev(block_tables, torch.int32), int(block_tables.shape[1]),
-                                 _dev(context_lens, torch.int32), int(max_context_len), B, H, Hkv,
-                                 d, bs, N, float(scale), _dtype_code(q), _dev(out, q.dtype),
-                                 _dev(workspace), workspace.numel() * workspace.element_size(),
-                                 _stream_ptr(stream)),
-           "pa_decode_int4")
+    Hkv = k_cache.shape[1]
+    N, bs = _int4_cache(k_cache, v_cache, k_scale, v_scale, Hkv, d)
+    if (block_tables.dim() != 2 or block_tables.shape[0] != B or context_lens.shape != (B,)
+            or out.shape != q.shape):
+        _misfit(block_tables=(block_tables, (B, block_tables.shape[-1])),
+                context_lens=(context_lens, (B,)), out=(out, (B, H, d)))
+    dev, st = _where(q, stream)
+    dt, u8, f16, i32 = q.dtype, torch.uint8, torch.float16, torch.int32
+    _check(load().pa_decode_int4(
+        _ptr(q, dt, dev), _ptr(k_cache, u8, dev), _ptr(v_cache, u8, dev), _ptr(k_scale, f16, dev),
+        _ptr(v_scale, f16, dev), _ptr(block_tables, i32, dev), block_tables.shape[1],
+        _ptr(context_lens, i32, dev), int(max_context_len), B, H, Hkv, d, bs, N, float(scale),
+        _dtype_code(q), _ptr(out, dt, dev), _ptr(workspace, workspace.dtype, dev),
+        workspace.nbytes, st), "pa_decode_int4")
 
 
 def pa_summarize_blocks(k_cache, block_ids, boxes, box_scale, fills=None, stream=None) -> None:
@@ -524,18 +545,17 @@ def pa_summarize_blocks(k_cache, block_ids, boxes, box_scale, fills=None, stream
     (int32) gives the rows in use of each (all of them by default)."""
     import torch
     N, bs, Hkv, d = k_cache.shape
-    n = int(block_ids.shape[0])
-    _shape("block_ids", block_ids, (n,))
-    _shape("boxes", boxes, (N, Hkv, 2, d))
-    _shape("box_scale", box_scale, (N, Hkv))
-    _same_device(k_cache, block_ids, boxes, box_scale)
-    if fills is not None:
-        _shape("fills", fills, (n,))
-        _same_device(fills)
+    n = block_ids.shape[0]
+    if (block_ids.dim() != 1 or boxes.shape != (N, Hkv, 2, d) or box_scale.shape != (N, Hkv)
+            or (fills is not None and fills.shape != (n,))):
+        _misfit(block_ids=(block_ids, (n,)), boxes=(boxes, (N, Hkv, 2, d)),
+                box_scale=(box_scale, (N, Hkv)),
+                **({} if fills is None else {"fills": (fills, (n,))}))
+    dev, st = _where(k_cache, stream)
     _check(load().pa_summarize_blocks(
-        _dev(k_cache), _dev(block_ids, torch.int32),
-        None if fills is None else _dev(fills, torch.int32), n, _dev(boxes, torch.int8),
-        _dev(box_scale, torch.float32), N, bs, Hkv, d, _dtype_code(k_cache), _stream_ptr(stream)),
+        _ptr(k_cache, k_cache.dtype, dev), _ptr(block_ids, torch.int32, dev),
+        None if fills is None else _ptr(fills, torch.int32, dev), n, _ptr(boxes, torch.int8, dev),
+        _ptr(box_scale, torch.float32, dev), N, bs, Hkv, d, _dtype_code(k_cache), st),
         "pa_summarize_blocks")
 
 
@@ -551,22 +571,23 @@ def pa_select_blocks(q, boxes, box_scale, block_tables, context_lens, block_size
     kept.  ``workspace``: ``pa_select_blocks_workspace_size`` zeroed bytes."""
     import torch
     B, H, d = q.shape
-    N, Hkv = int(boxes.shape[0]), int(boxes.shape[1])
-    keep = int(sel_blocks.shape[-1])
-    _shape("boxes", boxes, (N, Hkv, 2, d))
-    _shape("box_scale", box_scale, (N, Hkv))
-    _shape("block_tables", block_tables, (B, block_tables.shape[-1]))
-    _shape("context_lens", context_lens, (B,))
-    _shape("sel_blocks", sel_blocks, (B, Hkv, keep))
-    _shape("sel_lens", sel_lens, (B, Hkv))
-    _same_device(q, boxes, box_scale, block_tables, context_lens, sel_blocks, sel_lens, workspace)
+    N, Hkv = boxes.shape[0], boxes.shape[1]
+    keep = sel_blocks.shape[-1]
+    if (boxes.shape != (N, Hkv, 2, d) or box_scale.shape != (N, Hkv) or block_tables.dim() != 2
+            or block_tables.shape[0] != B or context_lens.shape != (B,)
+            or sel_blocks.shape != (B, Hkv, keep) or sel_lens.shape != (B, Hkv)):
+        _misfit(boxes=(boxes, (N, Hkv, 2, d)), box_scale=(box_scale, (N, Hkv)),
+                block_tables=(block_tables, (B, block_tables.shape[-1])),
+                context_lens=(context_lens, (B,)), sel_blocks=(sel_blocks, (B, Hkv, keep)),
+                sel_lens=(sel_lens, (B, Hkv)))
+    dev, st = _where(q, stream)
+    i32 = torch.int32
     _check(load().pa_select_blocks(
-        _dev(q), _dev(boxes, torch.int8), _dev(box_scale, torch.float32),
-        _dev(block_tables, torch.int32), int(block_tables.shape[1]),
-        _dev(context_lens, torch.int32), B, H, Hkv, d, int(block_size), N, keep, int(first),
-        int(last), _dtype_code(q), _dev(sel_blocks, torch.int32), _dev(sel_lens, torch.int32),
-        _dev(workspace), workspace.numel() * workspace.element_size(), _stream_ptr(stream)),
-        "pa_select_blocks")
+        _ptr(q, q.dtype, dev), _ptr(boxes, torch.int8, dev), _ptr(box_scale, torch.float32, dev),
+        _ptr(block_tables, i32, dev), block_tables.shape[1], _ptr(context_lens, i32, dev), B, H,
+        Hkv, d, int(block_size), N, keep, int(first), int(last), _dtype_code(q),
+        _ptr(sel_blocks, i32, dev), _ptr(sel_lens, i32, dev),
+        _ptr(workspace, workspace.dtype, dev), workspace.nbytes, st), "pa_select_blocks")
 
 
 def pa_decode_selected(q, k_cache, v_cache, sel_blocks, sel_lens, max_sel_len: int, scale: float,
@@ -577,18 +598,20 @@ def pa_decode_selected(q, k_cache, v_cache, sel_blocks, sel_lens, max_sel_len: i
     import torch
     B, H, d = q.shape
     N, bs, Hkv, _ = k_cache.shape
-    keep = int(sel_blocks.shape[-1])
-    _shape("k_cache", k_cache, (N, bs, Hkv, d))
-    _shape("v_cache", v_cache, k_cache.shape)
-    _shape("sel_blocks", sel_blocks, (B, Hkv, keep))
-    _shape("sel_lens", sel_lens, (B, Hkv))
-    _shape("out", out, q.shape)
-    _same_device(q, k_cache, v_cache, sel_blocks, sel_lens, out, workspace)
+    keep = sel_blocks.shape[-1]
+    if (k_cache.shape != (N, bs, Hkv, d) or v_cache.shape != k_cache.shape
+            or sel_blocks.shape != (B, Hkv, keep) or sel_lens.shape != (B, Hkv)
+            or out.shape != q.shape):
+        _misfit(k_cache=(k_cache, (N, bs, Hkv, d)), v_cache=(v_cache, tuple(k_cache.shape)),
+                sel_blocks=(sel_blocks, (B, Hkv, keep)), sel_lens=(sel_lens, (B, Hkv)),
+                out=(out, (B, H, d)))
+    dev, st = _where(q, stream)
+    dt, i32 = q.dtype, torch.int32
     _check(load().pa_decode_selected(
-        _dev(q), _dev(k_cache, q.dtype), _dev(v_cache, q.dtype), _dev(sel_blocks, torch.int32),
-        keep, _dev(sel_lens, torch.int32), int(max_sel_len), B, H, Hkv, d, bs, N, float(scale),
-        _dtype_code(q), _dev(out, q.dtype), _dev(workspace),
-        workspace.numel() * workspace.element_size(), _stream_ptr(stream)), "pa_decode_selected")
+        _ptr(q, dt, dev), _ptr(k_cache, dt, dev), _ptr(v_cache, dt, dev),
+        _ptr(sel_blocks, i32, dev), keep, _ptr(sel_lens, i32, dev), int(max_sel_len), B, H, Hkv, d,
+        bs, N, float(scale), _dtype_code(q), _ptr(out, dt, dev),
+        _ptr(workspace, workspace.dtype, dev), workspace.nbytes, st), "pa_decode_selected")
 
 
 def pa_check_device_errors(stream=None) -> int:
