@@ -602,9 +602,8 @@ PA_API pa_status pa_summarize_blocks(const void* k_cache, const int32_t* block_i
  *   keep         >= first + last, first >= 0, last >= 1;  H / Hkv <= 128
  *   sel_blocks   (device) [B][Hkv][keep] int32;  sel_lens (device) [B][Hkv] int32
  *   workspace    (device, 4-byte aligned) >= pa_select_blocks_workspace_size(B,
- *                Hkv, max_blocks) bytes, zeroed once (pa_decode_workspace_init);
- *                every call leaves its counters at zero.  Calls that overlap on
- *                the GPU must not share one. */
+ *                Hkv, max_blocks) bytes of any contents (the scores).  Calls that
+ *                overlap on the GPU must not share one. */
 PA_API size_t pa_select_blocks_workspace_size(int32_t B, int32_t Hkv, int32_t max_blocks);
 PA_API pa_status pa_select_blocks(const void* q, const void* boxes, const float* box_scale,
                                   const int32_t* block_tables, int32_t max_blocks,

@@ -568,7 +568,7 @@ def pa_select_blocks(q, boxes, box_scale, block_tables, context_lens, block_size
     """Chooses at most ``keep`` blocks per (sequence, KV head) by the scores that ``boxes``
     promise for ``q [B, H, d]``: ``sel_blocks [B, Hkv, keep]`` and ``sel_lens [B, Hkv]``
     (int32) receive the lists; the ``first`` and ``last`` blocks of a context are always
-    kept.  ``workspace``: ``pa_select_blocks_workspace_size`` zeroed bytes."""
+    kept.  ``workspace``: ``pa_select_blocks_workspace_size`` bytes."""
     import torch
     B, H, d = q.shape
     N, Hkv = boxes.shape[0], boxes.shape[1]

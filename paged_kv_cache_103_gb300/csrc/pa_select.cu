@@ -134,9 +134,10 @@ struct SelectParams {
     const int32_t* context_lens;
     int32_t* sel_blocks;
     int32_t* sel_lens;
-    uint32_t* keys;      // [B * Hkv][max_blocks]
+    uint32_t* keys;      // [B * Hkv][max_blocks]: the scores, as ordered numbers
     unsigned int* err;
     int32_t max_blocks, H, Hkv, G, bs, num_blocks, keep, first, last;
+    int32_t tile, heads;   // of a scoring CTA: blocks, and KV heads at most
 };
 
 // A float as an unsigned number of the same order (-0 as +0).
@@ -145,143 +146,262 @@ __device__ __forceinline__ uint32_t ordered(float x) {
     return (u >> 31) ? ~u : (u | 0x80000000u);
 }
 
-// One CTA per (sequence, KV head): scores, the k-th largest by radix, and the
-// chosen ids in context order.
+__device__ __forceinline__ int32_t context_of(const SelectParams& p, int32_t i) {
+    const int32_t n = __ldg(p.context_lens + i);
+    return max(0, min(n, p.max_blocks * p.bs));
+}
+
+// 0xFF in the bytes that are negative.
+__device__ __forceinline__ uint32_t sign_bytes(uint32_t x) {
+    uint32_t r;
+    asm("prmt.b32 %0, %1, 0, 0xBA98;" : "=r"(r) : "r"(x));
+    return r;
+}
+
+// Scores of `tile` blocks of one sequence under up to `heads` KV heads: blockIdx = (tile,
+// sequence, group of KV heads).  What bounds it is HBM: the boxes, 260 bytes a (block,
+// KV head) at d = 128.  A box belongs to D / 16 lanes, 16 channels of lo and of hi each,
+// and neighbouring lane groups take neighbouring KV heads, whose boxes are contiguous; a
+// group works on four boxes at once (eight 16-byte loads in flight per lane) and keeps its
+// KV head, so a query head's codes are read from shared memory once for the four.
 template <bool kBF16, int D>
-__global__ void __launch_bounds__(kThreads) select_kernel(const SelectParams p) {
-    constexpr int kLanes = D / 16;           // lanes per block: 16 channels each
-    constexpr int kPerWarp = 32 / kLanes;    // blocks per warp and step
-    constexpr int kWarps = kThreads / 32;
-    extern __shared__ uint32_t smem[];
-    uint32_t* qc = smem;                                       // [G][D / 4] query codes
-    float* sq = reinterpret_cast<float*>(smem + p.G * (D / 4));  // [G]
-    __shared__ uint32_t hist[256];
-    __shared__ uint32_t wsum[2][kWarps], s_prefix, s_rank;
+__global__ void __launch_bounds__(kThreads) score_kernel(const SelectParams p) {
+    constexpr int kLanes = D / 16, kItems = 4, kUnits = kThreads / kLanes;
+    extern __shared__ __align__(16) uint32_t smem[];
+    asm volatile("griddepcontrol.launch_dependents;");   // the selection may be launched: it waits
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int32_t g = blockIdx.x, i = blockIdx.y;
-    const int64_t pair = (int64_t)i * p.Hkv + g;
-    int32_t n = __ldg(p.context_lens + i);
-    if (tid == 0 && g == 0) {
-        if (n < 0) pa::raise_error(p.err, PA_DEVERR_CONTEXT);
-        if (n > (int64_t)p.max_blocks * p.bs) pa::raise_error(p.err, PA_DEVERR_TABLE_WIDTH);
-    }
-    n = (int32_t)max((int64_t)0, min((int64_t)n, (int64_t)p.max_blocks * p.bs));
-    const int32_t nb = (n + p.bs - 1) / p.bs;
+    const int32_t i = blockIdx.y, g0 = blockIdx.z * p.heads, heads = min(p.heads, p.Hkv - g0);
+    const int32_t nb = (context_of(p, i) + p.bs - 1) / p.bs;
+    const int32_t j0 = p.first + blockIdx.x * p.tile, j1 = min(nb - p.last, j0 + p.tile);
+    if (nb <= p.keep || j0 >= j1) return;
     const int32_t* table = p.block_tables + (int64_t)i * p.max_blocks;
-    int32_t* sel = p.sel_blocks + pair * p.keep;
-    const int32_t count = min(nb, p.keep);
-    if (tid == 0) p.sel_lens[pair] = nb ? (count - 1) * p.bs + n - (nb - 1) * p.bs : 0;
-    for (int32_t j = count + tid; j < p.keep; j += kThreads) sel[j] = -1;
-    if (nb <= p.keep) {
-        for (int32_t j = tid; j < nb; j += kThreads) sel[j] = __ldg(table + j);
-        return;
-    }
-    // ---- query codes
-    for (int h = warp; h < p.G; h += kWarps) {
-        const uint16_t* q = p.q + ((int64_t)i * p.H + g * p.G + h) * D;
+    // ---- query codes [heads * G][D / 4] and steps
+    const int nq = heads * p.G;
+    float* sq = reinterpret_cast<float*>(smem + nq * (D / 4));
+    for (int h = warp; h < nq; h += kThreads / 32) {
+        const uint16_t* q = p.q + ((int64_t)i * p.H + g0 * p.G + h) * D;
         float2 x[D / 64];
         float a = 0.f;
 #pragma unroll
         for (int j = 0; j < D / 64; ++j) {
-            x[j] = widen2<kBF16>(*reinterpret_cast<const uint32_t*>(q + j * 64 + lane * 2));
+            x[j] = widen2<kBF16>(__ldg(reinterpret_cast<const uint32_t*>(q + j * 64 + lane * 2)));
             a = fmaxf(a, fmaxf(fabsf(x[j].x), fabsf(x[j].y)));
         }
-        for (int o = 16; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
+        // the bit patterns of non-negative floats order like the values
+        a = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(a)));
         const float s = __fdiv_rn(a, 127.f);
 #pragma unroll
         for (int j = 0; j < D / 64; ++j)
-            reinterpret_cast<uint16_t*>(qc)[h * (D / 2) + j * 32 + lane] =
+            reinterpret_cast<uint16_t*>(smem)[h * (D / 2) + j * 32 + lane] =
                 s > 0.f ? (uint16_t)(code8(x[j].x, s) | code8(x[j].y, s) << 8) : 0;
         if (lane == 0) sq[h] = s;
     }
     __syncthreads();
-    // ---- scores of the blocks that are not kept anyway
-    const int32_t lo = p.first, hi = nb - p.last;
-    uint32_t* keys = p.keys + pair * p.max_blocks;
-    const int sub = lane / kLanes, l = lane % kLanes;
-    for (int32_t j0 = lo + warp * kPerWarp; j0 < hi; j0 += kWarps * kPerWarp) {
-        const int32_t j = j0 + sub;
-        const int32_t id = j < hi ? __ldg(table + j) : -1;
-        const bool ok = id >= 0 && id < p.num_blocks;
-        if (j < hi && !ok && l == 0) pa::raise_error(p.err, PA_DEVERR_BLOCK_ID);
-        const int64_t row = (int64_t)(ok ? id : 0) * p.Hkv + g;
-        const uint4 a = __ldg(p.boxes + row * 2 * kLanes + l);
-        const uint4 b = __ldg(p.boxes + row * 2 * kLanes + kLanes + l);
-        const float S = __ldg(p.box_scale + row);
-        const uint32_t lw[4] = {a.x, a.y, a.z, a.w}, hw[4] = {b.x, b.y, b.z, b.w};
+    const int unit = tid / kLanes, l = tid % kLanes, rows = kUnits / heads;
+    // KV head, and which of the blocks in flight (none for the lane groups left over, which
+    // go along for the shuffles' sake)
+    const int g = unit % heads, r = unit / heads < rows ? unit / heads : 1 << 28;
+    const uint4* qc = reinterpret_cast<const uint4*>(smem) + g * p.G * kLanes + l;
+    uint32_t* keys = p.keys + ((int64_t)i * p.Hkv + g0 + g) * p.max_blocks;
+    const int32_t steps = (j1 - j0 + kItems * rows - 1) / (kItems * rows);
+    for (int32_t step = 0; step < steps; ++step) {
+        const int32_t j = j0 + step * kItems * rows + r;
+        uint32_t lo[kItems][4], hi[kItems][4];
+        int64_t row[kItems];
+        bool ok[kItems];
+#pragma unroll
+        for (int q = 0; q < kItems; ++q) {
+            const int32_t jq = j + q * rows;
+            const int32_t id = jq < j1 ? __ldg(table + jq) : 0;
+            ok[q] = (uint32_t)id < (uint32_t)p.num_blocks;
+            if (jq < j1 && !ok[q] && l == 0) pa::raise_error(p.err, PA_DEVERR_BLOCK_ID);
+            row[q] = (int64_t)(ok[q] ? id : 0) * p.Hkv + g0 + g;
+        }
+#pragma unroll
+        for (int q = 0; q < kItems; ++q) {
+            const uint4 a = __ldg(p.boxes + row[q] * 2 * kLanes + l);
+            const uint4 b = __ldg(p.boxes + row[q] * 2 * kLanes + kLanes + l);
+            lo[q][0] = a.x, lo[q][1] = a.y, lo[q][2] = a.z, lo[q][3] = a.w;
+            hi[q][0] = b.x, hi[q][1] = b.y, hi[q][2] = b.z, hi[q][3] = b.w;
+        }
+        // the box that this lane finishes, after the sums below
+        const int mine = kLanes == 8 ? (l >> 1) & 3 : l & 3;
+        const int64_t my_row = mine == 0 ? row[0] : mine == 1 ? row[1] : mine == 2 ? row[2] : row[3];
+        const float S = __ldg(p.box_scale + my_row);
         float best = 0.f;
         for (int h = 0; h < p.G; ++h) {
-            int dot = 0;
+            const uint4 cv = qc[h * kLanes];
+            const uint32_t c[4] = {cv.x, cv.y, cv.z, cv.w};
+            uint32_t neg[4];
 #pragma unroll
-            for (int w = 0; w < 4; ++w) {
-                const uint32_t c = qc[h * (D / 4) + l * 4 + w];
-                const uint32_t neg = __vcmpgts4(0u, c);
-                dot = __dp4a((int)((lw[w] & neg) | (hw[w] & ~neg)), (int)c, dot);
-            }
+            for (int w = 0; w < 4; ++w) neg[w] = sign_bytes(c[w]);
+            int dot[kItems] = {};
 #pragma unroll
-            for (int o = 1; o < kLanes; o <<= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
-            const float x = __fmul_rn(__fmul_rn((float)dot, sq[h]), S);
+            for (int q = 0; q < kItems; ++q)
+#pragma unroll
+                for (int w = 0; w < 4; ++w)
+                    dot[q] = __dp4a((int)((lo[q][w] & neg[w]) | (hi[q][w] & ~neg[w])), (int)c[w], dot[q]);
+            // Sums over the lanes, halving the boxes of each lane on the way.
+            constexpr int kTop = kLanes / 2;
+            const bool up = l & kTop, up2 = l & (kTop / 2);
+            const int d0 = (up ? dot[2] : dot[0]) + __shfl_xor_sync(0xffffffffu, up ? dot[0] : dot[2], kTop);
+            const int d1 = (up ? dot[3] : dot[1]) + __shfl_xor_sync(0xffffffffu, up ? dot[1] : dot[3], kTop);
+            int sum = (up2 ? d1 : d0) + __shfl_xor_sync(0xffffffffu, up2 ? d0 : d1, kTop / 2);
+            if constexpr (kLanes == 8) sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+            // S >= 0 and rounding is monotonic: the largest (dot sq) S is the largest dot sq's
+            const float x = __fmul_rn((float)sum, sq[g * p.G + h]);
             best = h ? fmaxf(best, x) : x;
         }
-        if (l == 0 && j < hi) keys[j] = ok ? ordered(best) : 0u;
+        const int32_t jm = j + mine * rows;
+        const bool my_ok = mine == 0 ? ok[0] : mine == 1 ? ok[1] : mine == 2 ? ok[2] : ok[3];
+        if (jm < j1 && (kLanes == 4 || !(l & 1))) keys[jm] = my_ok ? ordered(__fmul_rn(best, S)) : 0u;
     }
+}
+
+constexpr int kSelThreads = 512;
+constexpr int kSelWarps = kSelThreads / 32;
+constexpr int kBinBits = 11, kBins = 1 << kBinBits;
+constexpr int kStaged = 8192;    // keys held in shared memory; more are read again from L2
+
+// Largest (and, negated, smallest) of a value over the CTA: scratch of kSelWarps words.
+__device__ __forceinline__ uint32_t cta_max(uint32_t v, uint32_t* scratch) {
+    v = __reduce_max_sync(0xffffffffu, v);
+    if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = v;
     __syncthreads();
-    // ---- the k-th largest key, eight bits at a time
-    const int32_t k = p.keep - p.first - p.last;
-    if (tid == 0) {
-        s_prefix = 0;
-        s_rank = (uint32_t)k;
+    const int lane = threadIdx.x & 31;
+    return __reduce_max_sync(0xffffffffu, lane < kSelWarps ? scratch[lane] : 0u);
+}
+
+// One CTA per (sequence, KV head): the k-th largest score, then the chosen ids in context
+// order.  Bound by latency (a handful of barriers).  The keys' range is cut into 2048 bins,
+// whose counts from the top name the bin of the k-th largest; that bin is cut again until
+// it is one key wide or wanted whole (three passes at most, one or two in practice).
+__global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams p) {
+    __shared__ uint32_t staged[kStaged];
+    __shared__ uint32_t hist[kBins];
+    __shared__ uint32_t scratch[2][kSelWarps];
+    __shared__ uint32_t s_bin, s_rank, s_count;
+    __shared__ uint2 wsum[kSelWarps];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int32_t g = blockIdx.x, i = blockIdx.y;
+    const int64_t pair = (int64_t)i * p.Hkv + g;
+    if (tid == 0 && g == 0) {
+        const int32_t raw = __ldg(p.context_lens + i);
+        if (raw < 0) pa::raise_error(p.err, PA_DEVERR_CONTEXT);
+        if (raw > p.max_blocks * p.bs) pa::raise_error(p.err, PA_DEVERR_TABLE_WIDTH);
     }
-    for (int pass = 3; pass >= 0; --pass) {
-        hist[tid] = 0;
-        __syncthreads();
-        const uint32_t want = s_prefix;
-        for (int32_t j = lo + tid; j < hi; j += kThreads) {
-            const uint32_t x = keys[j];
-            if (pass == 3 || (x >> (8 * pass + 8)) == want) atomicAdd(&hist[(x >> (8 * pass)) & 255], 1u);
-        }
-        __syncthreads();
-        if (tid == 0 && k > 0) {
-            uint32_t rank = s_rank;
-            int b = 255;
-            while (b > 0 && hist[b] < rank) rank -= hist[b--];
-            s_prefix = want << 8 | (uint32_t)b;
-            s_rank = rank;   // how many of this digit's keys are still wanted
-        }
-        __syncthreads();
+    const int32_t n = context_of(p, i), nb = (n + p.bs - 1) / p.bs;
+    const int32_t* table = p.block_tables + (int64_t)i * p.max_blocks;
+    int32_t* sel = p.sel_blocks + pair * p.keep;
+    const int32_t count = min(nb, p.keep);
+    if (tid == 0) p.sel_lens[pair] = nb ? (count - 1) * p.bs + n - (nb - 1) * p.bs : 0;
+    for (int32_t j = count + tid; j < p.keep; j += kSelThreads) sel[j] = -1;
+    const int32_t k = p.keep - p.first - p.last, m = nb - p.first - p.last;   // k < m below
+    const int32_t head = nb <= p.keep ? nb : p.first;
+    for (int32_t j = tid; j < head; j += kSelThreads) sel[j] = __ldg(table + j);
+    if (nb > p.keep)
+        for (int32_t j = tid; j < p.last; j += kSelThreads)
+            sel[p.keep - p.last + j] = __ldg(table + nb - p.last + j);
+    // The scores; CTAs that need none wait too, so that this grid ends after theirs.
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (nb <= p.keep || k == 0) return;
+    const uint32_t* keys = p.keys + pair * p.max_blocks + p.first;
+    const bool fits = m <= kStaged;
+    auto key = [&](int32_t j) { return fits ? staged[j] : __ldcg(keys + j); };
+    uint32_t top = 0, low = 0;    // the largest key, and the smallest's complement
+    for (int32_t j = tid; j < m; j += kSelThreads) {
+        const uint32_t x = __ldcg(keys + j);
+        if (fits) staged[j] = x;
+        top = max(top, x);
+        low = max(low, ~x);
     }
-    const uint32_t limit = k > 0 ? s_prefix : 0xffffffffu;
-    const uint32_t ties = k > 0 ? s_rank : 0u;   // keys equal to the limit, lowest index first
-    // ---- ids in context order
-    for (int32_t j = tid; j < p.first; j += kThreads) sel[j] = __ldg(table + j);
-    for (int32_t j = tid; j < p.last; j += kThreads)
-        sel[p.keep - p.last + j] = __ldg(table + nb - p.last + j);
-    uint32_t taken = 0, tied = 0;   // over the tiles before this one
-    for (int32_t j0 = lo; j0 < hi; j0 += kThreads) {
-        const int32_t j = j0 + tid;
-        const uint32_t x = j < hi ? keys[j] : 0u;
-        const bool eq = j < hi && x == limit;
-        const uint32_t meq = __ballot_sync(0xffffffffu, eq);
-        const uint32_t below = (1u << lane) - 1u;
-        if (lane == 0) wsum[0][warp] = __popc(meq);
-        __syncthreads();
-        uint32_t before = tied, all = 0;
-        for (int w = 0; w < kWarps; ++w) {
-            if (w < warp) before += wsum[0][w];
-            all += wsum[0][w];
+    for (int b = tid; b < kBins; b += kSelThreads) hist[b] = 0;
+    top = cta_max(top, scratch[0]);
+    uint32_t base = ~cta_max(low, scratch[1]);
+    const int bits = 32 - __clz(top - base);       // 0 where all keys are equal
+    int shift = max(0, bits - kBinBits), width = bits;   // of the range under the knife
+    uint32_t rank = (uint32_t)k, limit, ties;      // chosen: keys above limit, and `ties` equal ones
+    for (;;) {
+        for (int32_t j = tid; j < m; j += kSelThreads) {
+            const uint32_t x = key(j) - base;      // keys below base wrap to large numbers
+            if (width == 32 || (x >> width) == 0) atomicAdd(&hist[x >> shift], 1u);
         }
-        const bool take = k > 0 && j < hi && (x > limit || (eq && before + __popc(meq & below) < ties));
-        const uint32_t mt = __ballot_sync(0xffffffffu, take);
-        if (lane == 0) wsum[1][warp] = __popc(mt);
         __syncthreads();
-        uint32_t at = taken, sum = 0;
-        for (int w = 0; w < kWarps; ++w) {
-            if (w < warp) at += wsum[1][w];
-            sum += wsum[1][w];
+        // Counts from the top: thread t owns bins 4 t' .. 4 t' + 3 with t' = 511 - t.
+        const int b0 = (kSelThreads - 1 - tid) * (kBins / kSelThreads);
+        uint32_t c[4], mine = 0;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            c[q] = hist[b0 + q];
+            mine += c[q];
+            hist[b0 + q] = 0;
         }
-        if (take) sel[p.first + at + __popc(mt & below)] = __ldg(table + j);
-        taken += sum;
-        tied += all;
+        uint32_t upto = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t y = __shfl_up_sync(0xffffffffu, upto, o);
+            if (lane >= o) upto += y;
+        }
+        if (lane == 31) scratch[0][warp] = upto;
+        __syncthreads();
+        for (int w = 0; w < warp; ++w) upto += scratch[0][w];
+        if (upto >= rank && upto - mine < rank) {   // one thread
+            uint32_t want = rank - (upto - mine);
+            int q = 3;
+            while (c[q] < want) want -= c[q--];
+            s_bin = b0 + q;
+            s_rank = want;
+            s_count = c[q];
+        }
+        __syncthreads();
+        base += s_bin << shift;
+        rank = s_rank;
+        if (shift == 0) {
+            limit = base;
+            ties = rank;
+            break;
+        }
+        if (rank == s_count) {      // the whole bin is wanted; base > 0, for k < m
+            limit = base - 1;
+            ties = 0;
+            break;
+        }
+        width = shift;
+        shift = max(0, shift - kBinBits);
+        __syncthreads();            // s_bin and scratch are read
+    }
+    // ---- ids in context order: each thread a contiguous stretch
+    const int32_t per = (m + kSelThreads - 1) / kSelThreads;
+    const int32_t beg = min(m, tid * per), end = min(m, beg + per);
+    uint32_t above = 0, equal = 0;
+    for (int32_t j = beg; j < end; ++j) {
+        const uint32_t x = key(j);
+        above += x > limit;
+        equal += x == limit;
+    }
+    uint32_t a = above, e = equal;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t ya = __shfl_up_sync(0xffffffffu, a, o), ye = __shfl_up_sync(0xffffffffu, e, o);
+        if (lane >= o) {
+            a += ya;
+            e += ye;
+        }
+    }
+    if (lane == 31) wsum[warp] = make_uint2(a, e);
+    __syncthreads();
+    a -= above;
+    e -= equal;
+    for (int w = 0; w < warp; ++w) {
+        a += wsum[w].x;
+        e += wsum[w].y;
+    }
+    uint32_t at = a + min(e, ties);
+    for (int32_t j = beg; j < end; ++j) {
+        const uint32_t x = key(j);
+        const bool take = x > limit || (x == limit && e < ties);
+        e += x == limit;
+        if (take) sel[p.first + at++] = __ldg(table + p.first + j);
     }
 }
 
@@ -316,7 +436,7 @@ PA_API pa_status pa_summarize_blocks(const void* k_cache, const int32_t* block_i
 
 PA_API size_t pa_select_blocks_workspace_size(int32_t B, int32_t Hkv, int32_t max_blocks) {
     if (B < 0 || Hkv <= 0 || max_blocks <= 0) return 0;
-    return (size_t)B * Hkv * ((size_t)max_blocks + 1) * sizeof(uint32_t);
+    return (size_t)B * Hkv * (size_t)max_blocks * sizeof(uint32_t);
 }
 
 PA_API pa_status pa_select_blocks(const void* q, const void* boxes, const float* box_scale,
@@ -349,7 +469,7 @@ PA_API pa_status pa_select_blocks(const void* q, const void* boxes, const float*
     p.context_lens = context_lens;
     p.sel_blocks = sel_blocks;
     p.sel_lens = sel_lens;
-    p.keys = static_cast<uint32_t*>(workspace) + (size_t)B * Hkv;
+    p.keys = static_cast<uint32_t*>(workspace);
     p.err = pa::device_error_word();
     if (!p.err) return PA_ERR_CUDA;
     p.max_blocks = max_blocks;
@@ -361,11 +481,43 @@ PA_API pa_status pa_select_blocks(const void* q, const void* boxes, const float*
     p.keep = keep;
     p.first = first;
     p.last = last;
-    const size_t smem = (size_t)p.G * (d + 4);
-    auto kern = d == 128 ? (dtype == PA_BF16 ? select_kernel<true, 128> : select_kernel<false, 128>)
-                         : (dtype == PA_BF16 ? select_kernel<true, 64> : select_kernel<false, 64>);
-    kern<<<dim3((unsigned)Hkv, (unsigned)B), kThreads, smem, static_cast<cudaStream_t>(stream)>>>(p);
-    return pa::cuda_status(cudaGetLastError());
+    const int sms = pa::device_sm_count();
+    if (!sms) return PA_ERR_CUDA;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const int32_t most = max_blocks - first - last;   // blocks to score, at most
+    if (max_blocks > keep && keep > first + last) {
+        // KV heads of a CTA: as many as it has lane groups for and query codes fit 40 KB.
+        const int units = kThreads / (d / 16);
+        const int fit = 40 * 1024 / (p.G * (d + 4));
+        p.heads = Hkv < units ? Hkv : units;
+        if (p.heads > fit) p.heads = fit;
+        const int groups = (Hkv + p.heads - 1) / p.heads;
+        // Blocks of a CTA: few enough for four CTAs per SM, not so few that the query
+        // codes cost more than the boxes.
+        const int64_t all = (int64_t)B * groups * most;
+        int64_t tile = (all + 4ll * sms - 1) / (4ll * sms);
+        const int least = 4 * (units / p.heads);      // one step of every lane group
+        tile = (tile + least - 1) / least * least;
+        if (tile < least) tile = least;
+        p.tile = (int32_t)(tile < most ? tile : most);
+        const dim3 grid((unsigned)((most + p.tile - 1) / p.tile), (unsigned)B, (unsigned)groups);
+        const size_t smem = (size_t)p.heads * p.G * (d + 4);
+        auto score = d == 128 ? (dtype == PA_BF16 ? score_kernel<true, 128> : score_kernel<false, 128>)
+                              : (dtype == PA_BF16 ? score_kernel<true, 64> : score_kernel<false, 64>);
+        score<<<grid, kThreads, smem, st>>>(p);
+        if (cudaGetLastError() != cudaSuccess) return PA_ERR_CUDA;
+    }
+    // The selection starts while the scores are computed and waits for them.
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)Hkv, (unsigned)B);
+    cfg.blockDim = dim3(kSelThreads);
+    cfg.stream = st;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = max_blocks > keep && keep > first + last ? 1 : 0;
+    return pa::cuda_status(cudaLaunchKernelEx(&cfg, select_kernel, p));
 }
 
 }  // extern "C"
