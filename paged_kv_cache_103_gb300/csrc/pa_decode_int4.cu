@@ -33,9 +33,9 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cmath>
 #include <cstring>
-#include <mutex>
 
 #include "pa.h"
 #include "pa_common.cuh"
@@ -1016,18 +1016,14 @@ template <int D, bool kBF16, int NT, bool kOne, int kShift>
 pa_status launch(const Int4Params& p, cudaStream_t stream) {
     auto kern = decode_int4_kernel<D, kBF16, NT, kOne, kShift>;
     // The shared-memory limit is set once per device.
-    static std::mutex mu;
-    static uint64_t done = 0;
+    static std::atomic<uint64_t> done{0};
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev >= 64) return PA_ERR_CUDA;
-    {
-        std::lock_guard<std::mutex> g(mu);
-        if (!(done >> dev & 1)) {
-            if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                     (int)kSmemBudget) != cudaSuccess)
-                return PA_ERR_CUDA;
-            done |= 1ull << dev;
-        }
+    if (!(done.load() >> dev & 1)) {
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 (int)kSmemBudget) != cudaSuccess)
+            return PA_ERR_CUDA;
+        done.fetch_or(1ull << dev);
     }
     int ctas = pa::device_sm_count();
     if (ctas <= 0) return PA_ERR_CUDA;

@@ -16,6 +16,7 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstring>
 
 #include "pa.h"
@@ -162,11 +163,26 @@ __device__ __forceinline__ uint32_t sign_bytes(uint32_t x) {
 // sequence, group of KV heads).  What bounds it is HBM: the boxes, 260 bytes a (block,
 // KV head) at d = 128.  A box belongs to D / 16 lanes, 16 channels of lo and of hi each,
 // and neighbouring lane groups take neighbouring KV heads, whose boxes are contiguous; a
-// group works on four boxes at once (eight 16-byte loads in flight per lane) and keeps its
-// KV head, so a query head's codes are read from shared memory once for the four.
+// group works on four boxes at once while the next ones arrive in shared memory, each lane's
+// bytes by its own asynchronous copies and for its own reading, so nothing is waited for but
+// the lane's own copies.  A group keeps its KV head, so a query head's codes are read from
+// shared memory once for the four.
+constexpr int kMaxTile = 2048;
+constexpr int kItems = 4, kRing = 3;                       // boxes per step; steps in the ring
+constexpr uint32_t kStepBytes = kThreads * (kItems * 32 + 4);   // lo and hi; one scale a lane
+constexpr int kCodeBytes = 32 * 1024;                      // of query codes and steps, at most
+constexpr int kScoreSmem = kRing * kStepBytes + kCodeBytes + kMaxTile * 4;
+
+__device__ __forceinline__ void copy16(uint32_t to, const void* from) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+}
+__device__ __forceinline__ void copy4(uint32_t to, const void* from) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to), "l"(from) : "memory");
+}
+
 template <bool kBF16, int D>
-__global__ void __launch_bounds__(kThreads) score_kernel(const SelectParams p) {
-    constexpr int kLanes = D / 16, kItems = 4, kUnits = kThreads / kLanes;
+__global__ void __launch_bounds__(kThreads, 2) score_kernel(const SelectParams p) {
+    constexpr int kLanes = D / 16, kUnits = kThreads / kLanes;
     extern __shared__ __align__(16) uint32_t smem[];
     asm volatile("griddepcontrol.launch_dependents;");   // the selection may be launched: it waits
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -174,10 +190,20 @@ __global__ void __launch_bounds__(kThreads) score_kernel(const SelectParams p) {
     const int32_t nb = (context_of(p, i) + p.bs - 1) / p.bs;
     const int32_t j0 = p.first + blockIdx.x * p.tile, j1 = min(nb - p.last, j0 + p.tile);
     if (nb <= p.keep || j0 >= j1) return;
-    const int32_t* table = p.block_tables + (int64_t)i * p.max_blocks;
-    // ---- query codes [heads * G][D / 4] and steps
+    // Shared memory: the ring, the query codes [heads * G][D / 4] and their steps, the tile's
+    // block ids (-1: not the pool's).
     const int nq = heads * p.G;
-    float* sq = reinterpret_cast<float*>(smem + nq * (D / 4));
+    uint32_t* codes = smem + kRing * kStepBytes / 4;
+    float* sq = reinterpret_cast<float*>(codes + nq * (D / 4));
+    int32_t* ids = reinterpret_cast<int32_t*>(sq + nq);
+    for (int32_t t = tid; t < j1 - j0; t += kThreads) {
+        int32_t id = __ldg(p.block_tables + (int64_t)i * p.max_blocks + j0 + t);
+        if ((uint32_t)id >= (uint32_t)p.num_blocks) {
+            if (g0 == 0) pa::raise_error(p.err, PA_DEVERR_BLOCK_ID);
+            id = -1;
+        }
+        ids[t] = id;
+    }
     for (int h = warp; h < nq; h += kThreads / 32) {
         const uint16_t* q = p.q + ((int64_t)i * p.H + g0 * p.G + h) * D;
         float2 x[D / 64];
@@ -192,7 +218,7 @@ __global__ void __launch_bounds__(kThreads) score_kernel(const SelectParams p) {
         const float s = __fdiv_rn(a, 127.f);
 #pragma unroll
         for (int j = 0; j < D / 64; ++j)
-            reinterpret_cast<uint16_t*>(smem)[h * (D / 2) + j * 32 + lane] =
+            reinterpret_cast<uint16_t*>(codes)[h * (D / 2) + j * 32 + lane] =
                 s > 0.f ? (uint16_t)(code8(x[j].x, s) | code8(x[j].y, s) << 8) : 0;
         if (lane == 0) sq[h] = s;
     }
@@ -201,33 +227,41 @@ __global__ void __launch_bounds__(kThreads) score_kernel(const SelectParams p) {
     // KV head, and which of the blocks in flight (none for the lane groups left over, which
     // go along for the shuffles' sake)
     const int g = unit % heads, r = unit / heads < rows ? unit / heads : 1 << 28;
-    const uint4* qc = reinterpret_cast<const uint4*>(smem) + g * p.G * kLanes + l;
-    uint32_t* keys = p.keys + ((int64_t)i * p.Hkv + g0 + g) * p.max_blocks;
-    const int32_t steps = (j1 - j0 + kItems * rows - 1) / (kItems * rows);
+    const uint4* qc = reinterpret_cast<const uint4*>(codes) + g * p.G * kLanes + l;
+    uint32_t* keys = p.keys + ((int64_t)i * p.Hkv + g0 + g) * p.max_blocks + j0;
+    const int32_t count = j1 - j0, stride = kItems * rows, steps = (count + stride - 1) / stride;
+    // the box of four that this lane finishes, after the sums below
+    const int mine = kLanes == 8 ? (l >> 1) & 3 : l & 3;
+    const uint32_t ring = pa::smem_addr(smem);
+    auto load = [&](int32_t step) {   // a group per step, empty or not
+        if (step < steps) {
+            const uint32_t to = ring + step % kRing * kStepBytes + tid * 16;
+#pragma unroll
+            for (int q = 0; q < kItems; ++q) {
+                const int32_t t = r + step * stride + q * rows, id = t < count ? max(ids[t], 0) : 0;
+                const int64_t row = (int64_t)id * p.Hkv + g0 + g;
+                copy16(to + (2 * q) * kThreads * 16, p.boxes + row * 2 * kLanes + l);
+                copy16(to + (2 * q + 1) * kThreads * 16, p.boxes + row * 2 * kLanes + kLanes + l);
+                if (q == mine) copy4(to - tid * 12 + kItems * 32 * kThreads, p.box_scale + row);
+            }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    for (int step = 0; step < kRing - 1; ++step) load(step);
     for (int32_t step = 0; step < steps; ++step) {
-        const int32_t j = j0 + step * kItems * rows + r;
-        uint32_t lo[kItems][4], hi[kItems][4];
-        int64_t row[kItems];
-        bool ok[kItems];
+        load(step + kRing - 1);
+        asm volatile("cp.async.wait_group %0;" ::"n"(kRing - 1) : "memory");
+        const int32_t t = r + step * stride;
+        const unsigned char* at = reinterpret_cast<const unsigned char*>(smem) + step % kRing * kStepBytes;
+        uint32_t lw[kItems][4], hw[kItems][4];
 #pragma unroll
         for (int q = 0; q < kItems; ++q) {
-            const int32_t jq = j + q * rows;
-            const int32_t id = jq < j1 ? __ldg(table + jq) : 0;
-            ok[q] = (uint32_t)id < (uint32_t)p.num_blocks;
-            if (jq < j1 && !ok[q] && l == 0) pa::raise_error(p.err, PA_DEVERR_BLOCK_ID);
-            row[q] = (int64_t)(ok[q] ? id : 0) * p.Hkv + g0 + g;
+            const uint4 lo = reinterpret_cast<const uint4*>(at)[(2 * q) * kThreads + tid];
+            const uint4 hi = reinterpret_cast<const uint4*>(at)[(2 * q + 1) * kThreads + tid];
+            lw[q][0] = lo.x, lw[q][1] = lo.y, lw[q][2] = lo.z, lw[q][3] = lo.w;
+            hw[q][0] = hi.x, hw[q][1] = hi.y, hw[q][2] = hi.z, hw[q][3] = hi.w;
         }
-#pragma unroll
-        for (int q = 0; q < kItems; ++q) {
-            const uint4 a = __ldg(p.boxes + row[q] * 2 * kLanes + l);
-            const uint4 b = __ldg(p.boxes + row[q] * 2 * kLanes + kLanes + l);
-            lo[q][0] = a.x, lo[q][1] = a.y, lo[q][2] = a.z, lo[q][3] = a.w;
-            hi[q][0] = b.x, hi[q][1] = b.y, hi[q][2] = b.z, hi[q][3] = b.w;
-        }
-        // the box that this lane finishes, after the sums below
-        const int mine = kLanes == 8 ? (l >> 1) & 3 : l & 3;
-        const int64_t my_row = mine == 0 ? row[0] : mine == 1 ? row[1] : mine == 2 ? row[2] : row[3];
-        const float S = __ldg(p.box_scale + my_row);
+        const float S = reinterpret_cast<const float*>(at + kItems * 32 * kThreads)[tid];
         float best = 0.f;
         for (int h = 0; h < p.G; ++h) {
             const uint4 cv = qc[h * kLanes];
@@ -240,7 +274,7 @@ __global__ void __launch_bounds__(kThreads) score_kernel(const SelectParams p) {
             for (int q = 0; q < kItems; ++q)
 #pragma unroll
                 for (int w = 0; w < 4; ++w)
-                    dot[q] = __dp4a((int)((lo[q][w] & neg[w]) | (hi[q][w] & ~neg[w])), (int)c[w], dot[q]);
+                    dot[q] = __dp4a((int)((lw[q][w] & neg[w]) | (hw[q][w] & ~neg[w])), (int)c[w], dot[q]);
             // Sums over the lanes, halving the boxes of each lane on the way.
             constexpr int kTop = kLanes / 2;
             const bool up = l & kTop, up2 = l & (kTop / 2);
@@ -252,36 +286,27 @@ __global__ void __launch_bounds__(kThreads) score_kernel(const SelectParams p) {
             const float x = __fmul_rn((float)sum, sq[g * p.G + h]);
             best = h ? fmaxf(best, x) : x;
         }
-        const int32_t jm = j + mine * rows;
-        const bool my_ok = mine == 0 ? ok[0] : mine == 1 ? ok[1] : mine == 2 ? ok[2] : ok[3];
-        if (jm < j1 && (kLanes == 4 || !(l & 1))) keys[jm] = my_ok ? ordered(__fmul_rn(best, S)) : 0u;
+        const int32_t tm = t + mine * rows;
+        if (tm < count && (kLanes == 4 || !(l & 1)))
+            keys[tm] = ids[tm] >= 0 ? ordered(__fmul_rn(best, S)) : 0u;
     }
 }
 
 constexpr int kSelThreads = 512;
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kBinBits = 11, kBins = 1 << kBinBits;
-constexpr int kStaged = 8192;    // keys held in shared memory; more are read again from L2
-
-// Largest (and, negated, smallest) of a value over the CTA: scratch of kSelWarps words.
-__device__ __forceinline__ uint32_t cta_max(uint32_t v, uint32_t* scratch) {
-    v = __reduce_max_sync(0xffffffffu, v);
-    if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = v;
-    __syncthreads();
-    const int lane = threadIdx.x & 31;
-    return __reduce_max_sync(0xffffffffu, lane < kSelWarps ? scratch[lane] : 0u);
-}
 
 // One CTA per (sequence, KV head): the k-th largest score, then the chosen ids in context
 // order.  Bound by latency (a handful of barriers).  The keys' range is cut into 2048 bins,
 // whose counts from the top name the bin of the k-th largest; that bin is cut again until
-// it is one key wide or wanted whole (three passes at most, one or two in practice).
+// it is one key wide or wanted whole (three passes at most, one or two in practice).  Each
+// thread owns a contiguous stretch of the keys: kPer of them in registers, or (0) any
+// number, read again from L2 by each pass.
+template <int kPer>
 __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams p) {
-    __shared__ uint32_t staged[kStaged];
-    __shared__ uint32_t hist[kBins];
-    __shared__ uint32_t scratch[2][kSelWarps];
+    __shared__ __align__(16) uint32_t hist[kBins];
+    __shared__ uint32_t s_top[kSelWarps], s_low[kSelWarps], wsum[kSelWarps], wsum2[kSelWarps];
     __shared__ uint32_t s_bin, s_rank, s_count;
-    __shared__ uint2 wsum[kSelWarps];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int32_t g = blockIdx.x, i = blockIdx.y;
     const int64_t pair = (int64_t)i * p.Hkv + g;
@@ -302,56 +327,78 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams 
     if (nb > p.keep)
         for (int32_t j = tid; j < p.last; j += kSelThreads)
             sel[p.keep - p.last + j] = __ldg(table + nb - p.last + j);
+    for (int b = tid; b < kBins; b += kSelThreads) hist[b] = 0;
+    const int32_t per = kPer ? kPer : (m + kSelThreads - 1) / kSelThreads;
+    const int32_t beg = min(max(m, 0), tid * per), end = min(max(m, 0), beg + per);
+    int32_t id[kPer ? kPer : 1] = {};
+    if constexpr (kPer > 0)
+#pragma unroll
+        for (int q = 0; q < kPer; ++q)
+            id[q] = beg + q < end && nb > p.keep ? __ldg(table + p.first + beg + q) : 0;
     // The scores; CTAs that need none wait too, so that this grid ends after theirs.
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if (nb <= p.keep || k == 0) return;
     const uint32_t* keys = p.keys + pair * p.max_blocks + p.first;
-    const bool fits = m <= kStaged;
-    auto key = [&](int32_t j) { return fits ? staged[j] : __ldcg(keys + j); };
+    uint32_t own[kPer ? kPer : 1];
     uint32_t top = 0, low = 0;    // the largest key, and the smallest's complement
-    for (int32_t j = tid; j < m; j += kSelThreads) {
-        const uint32_t x = __ldcg(keys + j);
-        if (fits) staged[j] = x;
+    // f(key, place in the stretch) for each key of this thread
+    auto each = [&](auto f) {
+        if constexpr (kPer > 0) {
+#pragma unroll
+            for (int q = 0; q < kPer; ++q)
+                if (beg + q < end) f(own[q], q);
+        } else {
+            for (int32_t j = beg; j < end; ++j) f(__ldcg(keys + j), j - beg);
+        }
+    };
+    if constexpr (kPer > 0)
+#pragma unroll
+        for (int q = 0; q < kPer; ++q) own[q] = beg + q < end ? __ldcg(keys + beg + q) : 0;
+    each([&](uint32_t x, int) {
         top = max(top, x);
         low = max(low, ~x);
+    });
+    top = __reduce_max_sync(0xffffffffu, top);
+    low = __reduce_max_sync(0xffffffffu, low);
+    if (lane == 0) {
+        s_top[warp] = top;
+        s_low[warp] = low;
     }
-    for (int b = tid; b < kBins; b += kSelThreads) hist[b] = 0;
-    top = cta_max(top, scratch[0]);
-    uint32_t base = ~cta_max(low, scratch[1]);
-    const int bits = 32 - __clz(top - base);       // 0 where all keys are equal
-    int shift = max(0, bits - kBinBits), width = bits;   // of the range under the knife
+    __syncthreads();
+    top = __reduce_max_sync(0xffffffffu, s_top[lane % kSelWarps]);
+    uint32_t base = ~__reduce_max_sync(0xffffffffu, s_low[lane % kSelWarps]);
+    int width = 32 - __clz(top - base);            // bits of the range; 0: all keys are equal
+    int shift = max(0, width - kBinBits);
     uint32_t rank = (uint32_t)k, limit, ties;      // chosen: keys above limit, and `ties` equal ones
     for (;;) {
-        for (int32_t j = tid; j < m; j += kSelThreads) {
-            const uint32_t x = key(j) - base;      // keys below base wrap to large numbers
+        each([&](uint32_t x, int) {
+            x -= base;                             // keys below base wrap to large numbers
             if (width == 32 || (x >> width) == 0) atomicAdd(&hist[x >> shift], 1u);
-        }
+        });
         __syncthreads();
         // Counts from the top: thread t owns bins 4 t' .. 4 t' + 3 with t' = 511 - t.
         const int b0 = (kSelThreads - 1 - tid) * (kBins / kSelThreads);
-        uint32_t c[4], mine = 0;
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            c[q] = hist[b0 + q];
-            mine += c[q];
-            hist[b0 + q] = 0;
-        }
+        const uint4 c4 = *reinterpret_cast<const uint4*>(hist + b0);
+        *reinterpret_cast<uint4*>(hist + b0) = make_uint4(0, 0, 0, 0);
+        const uint32_t mine = c4.x + c4.y + c4.z + c4.w;
         uint32_t upto = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const uint32_t y = __shfl_up_sync(0xffffffffu, upto, o);
             if (lane >= o) upto += y;
         }
-        if (lane == 31) scratch[0][warp] = upto;
+        if (lane == 31) wsum[warp] = upto;
         __syncthreads();
-        for (int w = 0; w < warp; ++w) upto += scratch[0][w];
+        upto += __reduce_add_sync(0xffffffffu, lane < warp ? wsum[lane % kSelWarps] : 0u);
         if (upto >= rank && upto - mine < rank) {   // one thread
-            uint32_t want = rank - (upto - mine);
+            uint32_t want = rank - (upto - mine), c = c4.w;
             int q = 3;
-            while (c[q] < want) want -= c[q--];
+            if (c < want) want -= c, c = c4.z, q = 2;
+            if (q == 2 && c < want) want -= c, c = c4.y, q = 1;
+            if (q == 1 && c < want) want -= c, c = c4.x, q = 0;
             s_bin = b0 + q;
             s_rank = want;
-            s_count = c[q];
+            s_count = c;
         }
         __syncthreads();
         base += s_bin << shift;
@@ -368,17 +415,13 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams 
         }
         width = shift;
         shift = max(0, shift - kBinBits);
-        __syncthreads();            // s_bin and scratch are read
     }
-    // ---- ids in context order: each thread a contiguous stretch
-    const int32_t per = (m + kSelThreads - 1) / kSelThreads;
-    const int32_t beg = min(m, tid * per), end = min(m, beg + per);
+    // ---- ids in context order
     uint32_t above = 0, equal = 0;
-    for (int32_t j = beg; j < end; ++j) {
-        const uint32_t x = key(j);
+    each([&](uint32_t x, int) {
         above += x > limit;
         equal += x == limit;
-    }
+    });
     uint32_t a = above, e = equal;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -388,21 +431,35 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams 
             e += ye;
         }
     }
-    if (lane == 31) wsum[warp] = make_uint2(a, e);
-    __syncthreads();
-    a -= above;
-    e -= equal;
-    for (int w = 0; w < warp; ++w) {
-        a += wsum[w].x;
-        e += wsum[w].y;
+    if (lane == 31) {
+        wsum[warp] = a;
+        wsum2[warp] = e;
     }
+    __syncthreads();
+    a += __reduce_add_sync(0xffffffffu, lane < warp ? wsum[lane % kSelWarps] : 0u) - above;
+    e += __reduce_add_sync(0xffffffffu, lane < warp ? wsum2[lane % kSelWarps] : 0u) - equal;
     uint32_t at = a + min(e, ties);
-    for (int32_t j = beg; j < end; ++j) {
-        const uint32_t x = key(j);
+    each([&](uint32_t x, int q) {
         const bool take = x > limit || (x == limit && e < ties);
         e += x == limit;
-        if (take) sel[p.first + at++] = __ldg(table + p.first + j);
+        if (take) sel[p.first + at++] = kPer ? id[kPer ? q : 0] : __ldg(table + p.first + beg + q);
+    });
+}
+
+template <bool kBF16, int D>
+pa_status launch_score(const SelectParams& p, dim3 grid, size_t smem, cudaStream_t stream) {
+    auto kern = score_kernel<kBF16, D>;
+    // The shared-memory limit is set once per device.
+    static std::atomic<uint64_t> done{0};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev >= 64) return PA_ERR_CUDA;
+    if (!(done.load() >> dev & 1)) {
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kScoreSmem) != cudaSuccess)
+            return PA_ERR_CUDA;
+        done.fetch_or(1ull << dev);
     }
+    kern<<<grid, kThreads, smem, stream>>>(p);
+    return pa::cuda_status(cudaGetLastError());
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -486,26 +543,27 @@ PA_API pa_status pa_select_blocks(const void* q, const void* boxes, const float*
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const int32_t most = max_blocks - first - last;   // blocks to score, at most
     if (max_blocks > keep && keep > first + last) {
-        // KV heads of a CTA: as many as it has lane groups for and query codes fit 40 KB.
+        // KV heads of a CTA: as many as it has lane groups for and query codes fit.
         const int units = kThreads / (d / 16);
-        const int fit = 40 * 1024 / (p.G * (d + 4));
+        const int fit = kCodeBytes / (p.G * (d + 4));
         p.heads = Hkv < units ? Hkv : units;
         if (p.heads > fit) p.heads = fit;
         const int groups = (Hkv + p.heads - 1) / p.heads;
-        // Blocks of a CTA: few enough for four CTAs per SM, not so few that the query
-        // codes cost more than the boxes.
+        // Blocks of a CTA: two CTAs per SM share all there may be, in whole steps.
         const int64_t all = (int64_t)B * groups * most;
-        int64_t tile = (all + 4ll * sms - 1) / (4ll * sms);
+        int64_t tile = (all + 2ll * sms - 1) / (2ll * sms);
         const int least = 4 * (units / p.heads);      // one step of every lane group
         tile = (tile + least - 1) / least * least;
-        if (tile < least) tile = least;
+        if (tile > kMaxTile) tile = kMaxTile / least * least;
         p.tile = (int32_t)(tile < most ? tile : most);
         const dim3 grid((unsigned)((most + p.tile - 1) / p.tile), (unsigned)B, (unsigned)groups);
-        const size_t smem = (size_t)p.heads * p.G * (d + 4);
-        auto score = d == 128 ? (dtype == PA_BF16 ? score_kernel<true, 128> : score_kernel<false, 128>)
-                              : (dtype == PA_BF16 ? score_kernel<true, 64> : score_kernel<false, 64>);
-        score<<<grid, kThreads, smem, st>>>(p);
-        if (cudaGetLastError() != cudaSuccess) return PA_ERR_CUDA;
+        const size_t smem = kRing * kStepBytes + (size_t)p.heads * p.G * (d + 4) + (size_t)p.tile * 4;
+        const pa_status done =
+            d == 128 ? (dtype == PA_BF16 ? launch_score<true, 128>(p, grid, smem, st)
+                                         : launch_score<false, 128>(p, grid, smem, st))
+                     : (dtype == PA_BF16 ? launch_score<true, 64>(p, grid, smem, st)
+                                         : launch_score<false, 64>(p, grid, smem, st));
+        if (done != PA_OK) return done;
     }
     // The selection starts while the scores are computed and waits for them.
     cudaLaunchConfig_t cfg{};
@@ -517,7 +575,9 @@ PA_API pa_status pa_select_blocks(const void* q, const void* boxes, const float*
     attr.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = max_blocks > keep && keep > first + last ? 1 : 0;
-    return pa::cuda_status(cudaLaunchKernelEx(&cfg, select_kernel, p));
+    auto select = most <= 4 * kSelThreads ? select_kernel<4>
+                  : most <= 16 * kSelThreads ? select_kernel<16> : select_kernel<0>;
+    return pa::cuda_status(cudaLaunchKernelEx(&cfg, select, p));
 }
 
 }  // extern "C"
