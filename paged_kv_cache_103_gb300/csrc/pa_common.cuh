@@ -114,17 +114,6 @@ __device__ __forceinline__ void tma_prefetch_3d(const CUtensorMap* map, int32_t 
                  : "memory");
 }
 
-// Copies `bytes` contiguous bytes global -> shared (addresses and size multiples
-// of 16), counted on `bar`.
-__device__ __forceinline__ void bulk_load(uint32_t smem_dst, const void* src, uint32_t bytes,
-                                          uint32_t bar, uint64_t l2_policy) {
-    asm volatile(
-        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint "
-        "[%0], [%1], %2, [%3], %4;" ::"r"(smem_dst),
-        "l"(src), "r"(bytes), "r"(bar), "l"(l2_policy)
-        : "memory");
-}
-
 // Transposes an 8x8 matrix of 16-bit values held across the warp in the
 // ldmatrix fragment layout (lane l: row l/4, columns 2(l%4), 2(l%4)+1).
 __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t x) {
@@ -235,6 +224,26 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
         asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     else
         asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// Smaller and larger of two pairs of 16-bit values.
+template <bool kBF16>
+__device__ __forceinline__ uint32_t min_x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    if constexpr (kBF16)
+        asm("min.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    else
+        asm("min.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+template <bool kBF16>
+__device__ __forceinline__ uint32_t max_x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    if constexpr (kBF16)
+        asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    else
+        asm("max.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
 }
 

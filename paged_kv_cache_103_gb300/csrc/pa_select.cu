@@ -37,94 +37,79 @@ __device__ __forceinline__ float2 widen2(uint32_t v) {
     }
 }
 
-template <bool kBF16>
-__device__ __forceinline__ uint32_t min2(uint32_t a, uint32_t b) {
-    uint32_t r;
-    if constexpr (kBF16)
-        asm("min.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-    else
-        asm("min.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-    return r;
-}
-
-template <bool kBF16>
-__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
-    uint32_t r;
-    if constexpr (kBF16)
-        asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-    else
-        asm("max.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-    return r;
-}
-
 __device__ __forceinline__ uint32_t code8(float x, float s) {
     return (uint32_t)max(-127, min(127, __float2int_rn(__fdiv_rn(x, s)))) & 0xFFu;
 }
 
-// Thread v: channels 8 (v % (D / 8)) .. + 7 of one (listed block, KV head).
+// One warp per (listed block, KV head): lane l owns channels 8 (l % (D / 8)) .. + 7 of every
+// (32 / (D / 8))-th row, so a block's rows are in flight at once.  Bound by HBM.  Afterwards
+// the first half of the warp has the smallest values to code, the second the largest.
 template <bool kBF16, int D>
 __global__ void __launch_bounds__(kThreads)
 summarize_kernel(const uint4* __restrict__ k_cache, const int32_t* __restrict__ block_ids,
-                 const int32_t* __restrict__ fills, uint32_t vecs, uint32_t Hkv, int32_t bs,
+                 const int32_t* __restrict__ fills, uint32_t pairs, uint32_t Hkv, int32_t bs,
                  int32_t num_blocks, uint2* __restrict__ boxes, float* __restrict__ box_scale,
                  unsigned int* __restrict__ err) {
-    constexpr uint32_t kRow = D / 8;
-    const uint32_t v = blockIdx.x * kThreads + threadIdx.x;
-    const bool live = v < vecs;   // vecs is a multiple of kRow
-    const uint32_t pair = (live ? v : 0) / kRow, l = v % kRow;
-    const uint32_t e = pair / Hkv, h = pair - e * Hkv;
-    const int32_t id = live ? __ldg(block_ids + e) : -1;
-    const bool ok = id >= 0 && id < num_blocks;
-    int32_t fill = live && fills ? __ldg(fills + e) : bs;
-    if (live && l == 0 && h == 0) {
+    constexpr uint32_t kRow = D / 8, kSets = 32 / kRow, kFlight = 8;
+    const uint32_t pair = (blockIdx.x * kThreads + threadIdx.x) >> 5, lane = threadIdx.x & 31;
+    if (pair >= pairs) return;
+    const uint32_t e = pair / Hkv, h = pair - e * Hkv, l = lane % kRow, set = lane / kRow;
+    const int32_t id = __ldg(block_ids + e);
+    const bool ok = (uint32_t)id < (uint32_t)num_blocks;
+    int32_t fill = fills ? __ldg(fills + e) : bs;
+    if (lane == 0 && h == 0) {
         if (!ok) pa::raise_error(err, PA_DEVERR_BLOCK_ID);
         if (fill < 0 || fill > bs) pa::raise_error(err, PA_DEVERR_CONTEXT);
     }
+    if (!ok) return;
     fill = max(0, min(bs, fill));
     uint32_t lo[4] = {0, 0, 0, 0}, hi[4] = {0, 0, 0, 0};
-    if (ok && fill > 0) {
+    if (fill > 0) {
         const int64_t stride = (int64_t)Hkv * kRow;   // between token rows
         const uint4* src = k_cache + (int64_t)id * bs * stride + h * kRow + l;
-        for (int32_t r0 = 0; r0 < fill; r0 += 8) {
-            uint4 x[8];
+        for (int32_t r0 = 0; r0 < fill; r0 += kFlight * kSets) {
+            uint4 x[kFlight];
 #pragma unroll
-            for (int r = 0; r < 8; ++r)   // the last row again past the fill: min and max keep
-                x[r] = __ldg(src + min(r0 + r, fill - 1) * stride);
+            for (int r = 0; r < (int)kFlight; ++r)   // the last row again past the fill
+                x[r] = __ldg(src + min(r0 + r * (int)kSets + (int)set, fill - 1) * stride);
 #pragma unroll
-            for (int r = 0; r < 8; ++r) {
+            for (int r = 0; r < (int)kFlight; ++r) {
                 const uint32_t w[4] = {x[r].x, x[r].y, x[r].z, x[r].w};
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const bool start = r0 == 0 && r == 0;
-                    lo[j] = start ? w[j] : min2<kBF16>(lo[j], w[j]);
-                    hi[j] = start ? w[j] : max2<kBF16>(hi[j], w[j]);
+                    lo[j] = start ? w[j] : pa::min_x2<kBF16>(lo[j], w[j]);
+                    hi[j] = start ? w[j] : pa::max_x2<kBF16>(hi[j], w[j]);
                 }
             }
         }
     }
-    float a = 0.f;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const float2 x = widen2<kBF16>(lo[j]), y = widen2<kBF16>(hi[j]);
-        a = fmaxf(a, fmaxf(fmaxf(fabsf(x.x), fabsf(x.y)), fmaxf(fabsf(y.x), fabsf(y.y))));
-    }
-#pragma unroll
-    for (uint32_t o = 1; o < kRow; o <<= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
-    if (!ok) return;
-    const float s = __fdiv_rn(a, 127.f);
-    uint32_t c[4] = {0, 0, 0, 0};   // lo codes, hi codes
-    if (s > 0.f) {
+    for (uint32_t o = kRow; o < 32; o <<= 1)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const float2 x = widen2<kBF16>(lo[j]), y = widen2<kBF16>(hi[j]);
-            c[j >> 1] |= (code8(x.x, s) | code8(x.y, s) << 8) << (16 * (j & 1));
-            c[2 + (j >> 1)] |= (code8(y.x, s) | code8(y.y, s) << 8) << (16 * (j & 1));
+            lo[j] = pa::min_x2<kBF16>(lo[j], __shfl_xor_sync(0xffffffffu, lo[j], o));
+            hi[j] = pa::max_x2<kBF16>(hi[j], __shfl_xor_sync(0xffffffffu, hi[j], o));
         }
+    const bool upper = lane >= 16;       // codes the largest
+    float x[8], a = 0.f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const float2 f = widen2<kBF16>(upper ? hi[j] : lo[j]);
+        x[2 * j] = f.x;
+        x[2 * j + 1] = f.y;
+        a = fmaxf(a, fmaxf(fabsf(f.x), fabsf(f.y)));
     }
+    // the bit patterns of non-negative floats order like the values
+    a = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(a)));
+    const float s = __fdiv_rn(a, 127.f);
+    uint32_t c[2] = {0, 0};
+    if (s > 0.f)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) c[j >> 2] |= code8(x[j], s) << (8 * (j & 3));
     const int64_t row = (int64_t)id * Hkv + h;
-    boxes[row * 2 * kRow + l] = make_uint2(c[0], c[1]);
-    boxes[row * 2 * kRow + kRow + l] = make_uint2(c[2], c[3]);
-    if (l == 0) box_scale[row] = s;
+    if (lane % 16 < kRow) boxes[(row * 2 + (upper ? 1 : 0)) * kRow + l] = make_uint2(c[0], c[1]);
+    if (lane == 0) box_scale[row] = s;
 }
 
 struct SelectParams {
@@ -476,17 +461,17 @@ PA_API pa_status pa_summarize_blocks(const void* k_cache, const int32_t* block_i
     if (dtype != PA_F16 && dtype != PA_BF16) return PA_ERR_UNSUPPORTED;
     if (d != 64 && d != 128) return PA_ERR_UNSUPPORTED;
     if (block_size != 8 && block_size != 16 && block_size != 32) return PA_ERR_UNSUPPORTED;
-    if ((int64_t)n * Hkv * (d / 8) > ((int64_t)1 << 31)) return PA_ERR_UNSUPPORTED;
+    if ((int64_t)n * Hkv > ((int64_t)1 << 27)) return PA_ERR_UNSUPPORTED;   // a warp each
     if (n == 0) return PA_OK;
     if (!k_cache || !block_ids || !boxes || !box_scale) return PA_ERR_INVALID;
     if (!aligned16(k_cache) || !aligned16(boxes)) return PA_ERR_INVALID;
     unsigned int* err = pa::device_error_word();
     if (!err) return PA_ERR_CUDA;
-    const uint32_t vecs = (uint32_t)((int64_t)n * Hkv * (d / 8));
+    const uint32_t pairs = (uint32_t)((int64_t)n * Hkv);
     auto kern = d == 128 ? (dtype == PA_BF16 ? summarize_kernel<true, 128> : summarize_kernel<false, 128>)
                          : (dtype == PA_BF16 ? summarize_kernel<true, 64> : summarize_kernel<false, 64>);
-    kern<<<(vecs + kThreads - 1) / kThreads, kThreads, 0, static_cast<cudaStream_t>(stream)>>>(
-        static_cast<const uint4*>(k_cache), block_ids, fills, vecs, (uint32_t)Hkv, block_size,
+    kern<<<(pairs + kThreads / 32 - 1) / (kThreads / 32), kThreads, 0, static_cast<cudaStream_t>(stream)>>>(
+        static_cast<const uint4*>(k_cache), block_ids, fills, pairs, (uint32_t)Hkv, block_size,
         num_blocks, static_cast<uint2*>(boxes), box_scale, err);
     return pa::cuda_status(cudaGetLastError());
 }
