@@ -812,7 +812,8 @@ class Step:
     are slot 0's).  Fill a slot's inputs, then :meth:`run` (submit and wait),
     or :meth:`submit` / :meth:`wait` to overlap the next step's host work with
     this one's device work.  With ``kv_format`` "fp8" or "int8" the caches
-    are 8-bit codes (uint8) with ``k_scale``/``v_scale``, and ``dtype`` gives
+    are 8-bit codes (uint8) with ``k_scale``/``v_scale``, with "int4" the 4-bit
+    codes and scales of ``pa_reshape_and_cache_int4``, and ``dtype`` gives
     the 16-bit type of the inputs."""
 
     def __init__(self, alloc: Allocator, B: int, H: int, Hkv: int, d: int, max_blocks: int,
@@ -820,13 +821,18 @@ class Step:
                  v_scale=None, dtype=None, depth: int = 1, kv_format: str = "native"):
         import torch
         self._lib = load()
-        N, bs = int(k_cache.shape[0]), int(k_cache.shape[1])
-        if tuple(k_cache.shape) != (N, bs, Hkv, d) or v_cache.shape != k_cache.shape:
+        q8 = {"native": 0, "fp8": 1, "int8": 2, "int4": 4}[kv_format]
+        int4 = kv_format == "int4"
+        N, bs = int(k_cache.shape[0]), int(k_cache.shape[2 if int4 else 1])
+        if int4:
+            if (tuple(k_cache.shape) != (N, Hkv, bs, d // 2) or v_cache.shape != k_cache.shape
+                    or d % 64):
+                raise ValueError("4-bit caches must be [num_blocks, Hkv, block_size, d / 2]")
+        elif tuple(k_cache.shape) != (N, bs, Hkv, d) or v_cache.shape != k_cache.shape:
             raise ValueError("caches must be [num_blocks, block_size, Hkv, d]")
-        q8 = {"native": 0, "fp8": 1, "int8": 2}[kv_format]
         if q8 and (k_scale is None or v_scale is None or
                    dtype not in (torch.float16, torch.bfloat16)):
-            raise ValueError("an 8-bit cache needs k_scale, v_scale and dtype (of q, k/v_new)")
+            raise ValueError("a quantised cache needs k_scale, v_scale and dtype (of q, k/v_new)")
         # the library sees raw pointers: a pool of the wrong element size
         # would be written past its end, so the format must match the tensors
         want = (torch.uint8,) if q8 else (torch.float16, torch.bfloat16)
@@ -835,9 +841,11 @@ class Step:
                                                                          k_cache.dtype))
         if not q8 and (k_scale is not None or v_scale is not None):
             raise ValueError("scales given for a 16-bit cache: pass kv_format")
-        if q8 and (tuple(k_scale.shape) != (N, Hkv, bs) or tuple(v_scale.shape) != (N, Hkv, bs)
-                   or k_scale.dtype != torch.float32 or v_scale.dtype != torch.float32):
-            raise ValueError("scales must be float32 [num_blocks, Hkv, block_size]")
+        scale_dt = torch.float16 if int4 else torch.float32
+        scale_shape = (N, Hkv, bs, d // 64, 2) if int4 else (N, Hkv, bs)
+        if q8 and (tuple(k_scale.shape) != scale_shape or tuple(v_scale.shape) != scale_shape
+                   or k_scale.dtype != scale_dt or v_scale.dtype != scale_dt):
+            raise ValueError("scales must be %s %s" % (scale_dt, scale_shape))
         dt = dtype if q8 else k_cache.dtype
         self.desc = StepDesc(B, H, Hkv, d, bs, N, max_blocks, max_context_len,
                              PA_F16 if dt == torch.float16 else PA_BF16, scale, q8, depth)
@@ -859,8 +867,8 @@ class Step:
         self._h = ctypes.c_void_p()
         _check(self._lib.pa_step_create(ctypes.byref(self.desc), alloc._h, _dev(k_cache),
                                         _dev(v_cache),
-                                        _dev(k_scale, torch.float32) if q8 else None,
-                                        _dev(v_scale, torch.float32) if q8 else None,
+                                        _dev(k_scale, scale_dt) if q8 else None,
+                                        _dev(v_scale, scale_dt) if q8 else None,
                                         self.host.data_ptr(), self.dev.data_ptr(),
                                         self.ws.data_ptr(), self.ws.numel(),
                                         ctypes.byref(self._h)), "pa_step_create")

@@ -27,7 +27,7 @@
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 constexpr float kF16Max = 65504.f;
 
 // n / d for n < 2^31 by a multiplication (d is the launch's; Granlund and Montgomery's
@@ -58,7 +58,7 @@ __device__ __forceinline__ float2 widen2(uint32_t v) {
 constexpr int kAppend = 16;         // values per thread of the append
 constexpr int kAppendGroup = 4;     // threads per group of 64 values
 
-// 1 / x within two units in the last place.
+// 1 / x, off by at most one unit in the last place.
 __device__ __forceinline__ float about_inverse(float x) {
     float y;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -91,8 +91,10 @@ __device__ __forceinline__ uint2 quantise16(const uint4 (&raw)[2], uint32_t& sm)
     const float m = __half2float(m16), s = __half2float(s16);
     if (!(s > 0.f)) return make_uint2(0, 0);
     // c = rint((x - m) / s), clamped: (x - m) / (15 s) saturates to [0, 1] at no cost, and
-    // 15 times it, within 2^-18 of the quotient, is rounded by adding 1.5 2^23 (nearest
-    // integer, ties to even).  The few threads with a value that near a tie divide.
+    // 15 times it is rounded by adding 1.5 2^23 (nearest integer, ties to even).  It is
+    // within 15 (2^-23 + 3 2^-24) of the quotient (the reciprocal's error and three
+    // roundings) and the quotient's own rounding is at most 15 2^-24: together below 6e-6.
+    // The few threads with a value within 1e-5 of a tie divide.
     constexpr float kRound = 12582912.f;
     const float inv15 = about_inverse(s) * (1.f / 15.f);
     float off = 0.f;      // largest distance from an integer
@@ -111,7 +113,7 @@ __device__ __forceinline__ uint2 quantise16(const uint4 (&raw)[2], uint32_t& sm)
         }
         c[g] = __float_as_uint(__fadd_rn(sum, 8388608.f));   // 2^23: the sum in the low bits
     }
-    if (off <= 0.4999f)
+    if (off <= 0.49999f)
         return make_uint2(__byte_perm(c[0], c[1], 0x5410), __byte_perm(c[2], c[3], 0x5410));
     uint32_t d[2] = {0, 0};
 #pragma unroll

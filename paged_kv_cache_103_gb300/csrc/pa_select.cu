@@ -50,7 +50,7 @@ summarize_kernel(const uint4* __restrict__ k_cache, const int32_t* __restrict__ 
                  const int32_t* __restrict__ fills, uint32_t pairs, uint32_t Hkv, int32_t bs,
                  int32_t num_blocks, uint2* __restrict__ boxes, float* __restrict__ box_scale,
                  unsigned int* __restrict__ err) {
-    constexpr uint32_t kRow = D / 8, kSets = 32 / kRow, kFlight = 8;
+    constexpr uint32_t kRow = D / 8, kSets = 32 / kRow, kFlight = 4;
     const uint32_t pair = (blockIdx.x * kThreads + threadIdx.x) >> 5, lane = threadIdx.x & 31;
     if (pair >= pairs) return;
     const uint32_t e = pair / Hkv, h = pair - e * Hkv, l = lane % kRow, set = lane / kRow;

@@ -22,6 +22,7 @@
 namespace {
 
 constexpr int kMaxDepth = 2;
+constexpr int kInt4 = 4;   // pa_step_desc.q8 of a 4-bit cache
 
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
@@ -31,8 +32,9 @@ bool desc_ok(const pa_step_desc* d) {
            (d->block_size == 8 || d->block_size == 16 || d->block_size == 32) &&
            d->num_blocks > 0 && d->max_blocks > 0 && d->max_context_len > 0 &&
            (int64_t)d->max_context_len <= (int64_t)d->max_blocks * d->block_size &&
-           (d->dtype == PA_F16 || d->dtype == PA_BF16) && d->q8 >= 0 && d->q8 <= 2 &&
-           (d->q8 == 0 || d->d == 128) && d->depth >= 1 && d->depth <= kMaxDepth;
+           (d->dtype == PA_F16 || d->dtype == PA_BF16) && d->q8 >= 0 &&
+           (d->q8 <= 2 || d->q8 == kInt4) && (d->q8 == 0 || d->q8 == kInt4 || d->d == 128) &&
+           d->depth >= 1 && d->depth <= kMaxDepth;
 }
 
 }  // namespace
@@ -43,11 +45,12 @@ struct pa_step {
     pa_allocator* alloc;
     void* k_cache;
     void* v_cache;
-    float* k_scale;         // 8-bit caches only
-    float* v_scale;
+    void* k_scale;          // quantised caches only: fp32, 4-bit: f16 pairs
+    void* v_scale;
     unsigned char* host;    // pinned staging, depth slots
     unsigned char* dev;     // device staging, depth slots
-    int64_t block_bytes;    // one block of one cache (codes for FP8)
+    int64_t block_bytes;    // one block of one cache (of codes where it is quantised)
+    int64_t scale_bytes;    // one block's scales
     int64_t submitted;      // steps submitted so far (the next uses slot submitted % depth)
     cudaStream_t in_stream;   // host->device copies of the inputs
     cudaStream_t out_stream;  // device->host copies of the outputs
@@ -92,18 +95,29 @@ pa_status capture(pa_step* s, int i, void* workspace, size_t ws_bytes, cudaStrea
     const int64_t* slots = reinterpret_cast<const int64_t*>(g + L.slot_mapping);
     const int32_t* tables = reinterpret_cast<const int32_t*>(g + L.block_tables);
     const int32_t* lens = reinterpret_cast<const int32_t*>(g + L.context_lens);
-    if (st == PA_OK && d->q8)
-        st = (d->q8 == 1 ? pa_reshape_and_cache_fp8 : pa_reshape_and_cache_int8)(g + L.k_new, g + L.v_new, slots, d->B, s->k_cache,
-                                      s->v_cache, s->k_scale, s->v_scale, d->num_blocks,
-                                      d->block_size, d->Hkv, d->d, d->dtype, cap);
-    else if (st == PA_OK)
+    float* ks = static_cast<float*>(s->k_scale);
+    float* vs = static_cast<float*>(s->v_scale);
+    if (d->q8 == kInt4)
+        st = pa_reshape_and_cache_int4(g + L.k_new, g + L.v_new, slots, d->B, s->k_cache, s->v_cache,
+                                       s->k_scale, s->v_scale, d->num_blocks, d->block_size, d->Hkv,
+                                       d->d, d->dtype, cap);
+    else if (d->q8)
+        st = (d->q8 == 1 ? pa_reshape_and_cache_fp8 : pa_reshape_and_cache_int8)(
+            g + L.k_new, g + L.v_new, slots, d->B, s->k_cache, s->v_cache, ks, vs, d->num_blocks,
+            d->block_size, d->Hkv, d->d, d->dtype, cap);
+    else
         st = pa_reshape_and_cache(g + L.k_new, g + L.v_new, slots, d->B, s->k_cache, s->v_cache,
                                   d->num_blocks, d->block_size, d->Hkv, d->d, d->dtype, cap);
-    if (st == PA_OK && d->q8)
-        st = (d->q8 == 1 ? pa_decode_fp8 : pa_decode_int8)(g + L.q, s->k_cache, s->v_cache, s->k_scale, s->v_scale, tables,
-                           d->max_blocks, lens, d->max_context_len, d->B, d->H, d->Hkv, d->d,
-                           d->block_size, d->num_blocks, d->scale, d->dtype, g + L.out, workspace,
-                           ws_bytes, cap);
+    if (st == PA_OK && d->q8 == kInt4)
+        st = pa_decode_int4(g + L.q, s->k_cache, s->v_cache, s->k_scale, s->v_scale, tables,
+                            d->max_blocks, lens, d->max_context_len, d->B, d->H, d->Hkv, d->d,
+                            d->block_size, d->num_blocks, d->scale, d->dtype, g + L.out, workspace,
+                            ws_bytes, cap);
+    else if (st == PA_OK && d->q8)
+        st = (d->q8 == 1 ? pa_decode_fp8 : pa_decode_int8)(
+            g + L.q, s->k_cache, s->v_cache, ks, vs, tables, d->max_blocks, lens, d->max_context_len,
+            d->B, d->H, d->Hkv, d->d, d->block_size, d->num_blocks, d->scale, d->dtype, g + L.out,
+            workspace, ws_bytes, cap);
     else if (st == PA_OK)
         st = pa_decode(g + L.q, s->k_cache, s->v_cache, tables, d->max_blocks, lens,
                        d->max_context_len, d->B, d->H, d->Hkv, d->d, d->block_size, d->num_blocks,
@@ -147,7 +161,7 @@ PA_API pa_status pa_step_layout_get(const pa_step_desc* d, pa_step_layout* out) 
 }
 
 PA_API pa_status pa_step_create(const pa_step_desc* d, pa_allocator* alloc, void* k_cache,
-                                void* v_cache, float* k_scale, float* v_scale, void* host_stage,
+                                void* v_cache, void* k_scale, void* v_scale, void* host_stage,
                                 void* dev_stage, void* workspace, size_t ws_bytes,
                                 pa_step** out) {
     if (!desc_ok(d) || !alloc || !k_cache || !v_cache || !host_stage || !dev_stage ||
@@ -174,7 +188,9 @@ PA_API pa_status pa_step_create(const pa_step_desc* d, pa_allocator* alloc, void
     s->v_scale = d->q8 ? v_scale : nullptr;
     s->host = static_cast<unsigned char*>(host_stage);
     s->dev = static_cast<unsigned char*>(dev_stage);
-    s->block_bytes = (int64_t)d->block_size * d->Hkv * d->d * (d->q8 ? 1 : 2);
+    const int64_t rows = (int64_t)d->block_size * d->Hkv;
+    s->block_bytes = d->q8 == kInt4 ? rows * d->d / 2 : rows * d->d * (d->q8 ? 1 : 2);
+    s->scale_bytes = d->q8 == kInt4 ? rows * (d->d / 64) * 4 : d->q8 ? rows * 4 : 0;
     s->submitted = 0;
     s->in_stream = s->out_stream = nullptr;
     for (int i = 0; i < kMaxDepth; ++i) {
@@ -297,11 +313,10 @@ PA_API pa_status pa_step_submit(pa_step* s, const int64_t* seq_ids, void* stream
         void* vc = s->v_cache;
         st = pa_copy_blocks(&kc, &vc, 1, dpairs, ncow, s->block_bytes, d.num_blocks, cs);
         if (st != PA_OK) return fail(st);
-        if (d.q8) {   // and the blocks' scales, [num_blocks][Hkv][block_size] fp32
+        if (d.q8) {   // and the blocks' scales
             void* ks = s->k_scale;
             void* vs = s->v_scale;
-            st = pa_copy_blocks(&ks, &vs, 1, dpairs, ncow, (int64_t)d.Hkv * d.block_size * 4,
-                                d.num_blocks, cs);
+            st = pa_copy_blocks(&ks, &vs, 1, dpairs, ncow, s->scale_bytes, d.num_blocks, cs);
             if (st != PA_OK) return fail(st);
         }
     }

@@ -122,3 +122,22 @@ def test_binding_refuses_tensors_that_do_not_fit():
         binding.pa_decode_selected(q, k, k[:3], sel, n, 8, 0.1, q, torch.zeros(8))
     with pytest.raises(ValueError):
         binding.pa_decode_selected(q, k, k, sel, n[:1], 8, 0.1, q, torch.zeros(8))
+
+
+def test_step_executor_takes_a_4_bit_cache(lib):
+    L = binding.StepLayout()
+
+    def layout(q8, d):
+        desc = binding.StepDesc(4, 8, 2, d, 16, 32, 8, 128, 0, 0.088, q8, 1)
+        return lib.pa_step_layout_get(ctypes.byref(desc), ctypes.byref(L))
+    assert layout(4, 64) == OK and layout(4, 128) == OK
+    assert layout(3, 128) == INVALID and layout(5, 128) == INVALID and layout(1, 64) == INVALID
+    N, bs, Hkv, d = 8, 16, 2, 128
+    c = torch.zeros(N, Hkv, bs, d // 2, dtype=torch.uint8)
+    s = torch.zeros(N, Hkv, bs, 2, 2, dtype=torch.float16)
+    alloc = binding.Allocator(N, bs)
+    for bad in (dict(k_cache=c.transpose(1, 2)), dict(v_cache=c[:4]), dict(k_scale=s.float()), dict(v_scale=s[:, :1]),
+                dict(k_scale=None), dict(dtype=torch.float32), dict(k_cache=c.to(torch.int8), v_cache=c.to(torch.int8))):
+        kw = dict(dict(k_cache=c, v_cache=c, k_scale=s, v_scale=s, dtype=torch.float16), **bad)
+        with pytest.raises(ValueError):
+            binding.Step(alloc, 2, 4, Hkv, d, 4, 64, scale=0.1, kv_format="int4", **kw)
