@@ -5,10 +5,14 @@
 // With x = s c + m per group g of 64 head-dim values, step and minimum leave the
 // sums over the codes:
 //     q . K_j       = sum_g  s_jg (sum_c q_c c_jc) + m_jg (sum_c q_c)
-//     sum_j p_j V_j = sum_j (p_j s_jg) c_jc  +  sum_j p_j m_jg      (c in g)
+//     sum_j p_j V_j = sum_j (p_j s_jg) (c_jc - 8)  +  sum_j p_j (m_jg + 8 s_jg)   (c in g)
 // so the tensor cores multiply bare codes, K's step and minimum meet each score
-// once per key and group, V's step is folded into P, and the minima are one number
-// per (head, group).
+// once per key and group, V's step is folded into P, and the values of code 8 are one
+// number per (head, group).  The 8 that the codes are taken from is a product of its
+// own, P times a tile of eights, subtracted at the end: what P's rounding and the
+// tensor cores' truncating sums do to the codes' mean (2.5 times their spread, and 100
+// times the result of a long flat context) they do to the eights as well.  Without it
+// the error against 64 bits was 2.6 times an fp32 computation's, with it 1.1 to 1.6.
 //
 // A code needs no conversion.  As the low bits of an f16 whose other bits are zero
 // it is the subnormal c 2^-24 (c 2^-20 in the nibble above), exactly; tensor cores
@@ -504,24 +508,29 @@ __global__ void __launch_bounds__(max_warps(NT) * 32, 1) decode_int4_kernel(cons
         const uint32_t voff1 = kCodes + (2 * c4 + (odd ^ 1)) * kRow + 4 * cr;
         const uint32_t perm0 = odd ? 0x1054 : 0x5410, perm1 = odd ? 0x3276 : 0x7632;
         const uint32_t krow = krows + cr * NG * 8, vrow = vrows + cr * NG * 8;
+        // The tile of eights: rows 0 .. 7 for group 0, 8 .. 15 for group 1, so that one
+        // accumulator has P's sums for both.
+        constexpr uint32_t kEight = 0x00080008u;
+        const uint32_t eights[2][4] = {{kEight, 0, kEight, 0}, {0, kEight, 0, kEight}};
         int segn = 0;
 #pragma unroll 1
         for (int32_t pos = lo; pos < hi;) {
+            // The first chunk is asked for while q is under way, the ring's others after it:
+            // they would only delay it.
             fetch_q(s);
-            if (segn == 0) {
 #pragma unroll 1
-                for (int k = 0; k < S; ++k) {   // a group per stage, empty or not
-                    if (ipos < hi) issue();
-                    commit_group();
-                }
+            for (int k = segn == 0 ? 0 : S; k < S; ++k) {   // a group per stage, empty or not
+                if (k == 1) convert_q();
+                if (ipos < hi) issue();
+                commit_group();
             }
-            convert_q();
+            if (segn) convert_q();
             const int32_t c0 = s.c, c_end = min(s.nc, s.c + hi - pos);
             const int32_t n = clamp_len(__ldg(p.context_lens + s.i), max_len);
             // Running state for heads 8 nt + 2 c4 + {0, 1}: the negative of the
             // maximum (bias; the logits below are relative to it), sum, sums of P times
             // V's minima; o: rows are values 64 g + 8 cr + u (e < 2) and + 4 + u.
-            float bias[NT][NJ], l_run[NT][NJ], lowv[NT][NG][NJ], o[NG][4][NT][4];
+            float bias[NT][NJ], l_run[NT][NJ], lowv[NT][NG][NJ], o[NG][4][NT][4], mid[NT][4];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -536,6 +545,7 @@ __global__ void __launch_bounds__(max_warps(NT) * 32, 1) decode_int4_kernel(cons
 #pragma unroll
                     for (int u = 0; u < 4; ++u)
                         o[g][u][nt][0] = o[g][u][nt][1] = o[g][u][nt][2] = o[g][u][nt][3] = 0.f;
+                mid[nt][0] = mid[nt][1] = mid[nt][2] = mid[nt][3] = 0.f;
             }
             bool fresh = true;   // no maximum yet
             // P times V's step is kept in f16 range by 2^vexp, which o carries.
@@ -595,6 +605,7 @@ __global__ void __launch_bounds__(max_warps(NT) * 32, 1) decode_int4_kernel(cons
 #pragma unroll
                         for (int g = 0; g < NG; ++g) {
                             kv[2 * g] *= qsc;
+                            vv[2 * g + 1] += 8.f * vv[2 * g];   // the value of code 8
                             vv[2 * g] *= vup;
                         }
                         store_row<NG>(krows + lane * NG * 8, kv);
@@ -664,6 +675,7 @@ __global__ void __launch_bounds__(max_warps(NT) * 32, 1) decode_int4_kernel(cons
 #pragma unroll
                                 for (int g = 0; g < NG; ++g) {
                                     lowv[nt][g][j] *= a;
+                                    mid[nt][2 * g + j] *= f;
 #pragma unroll
                                     for (int u = 0; u < 4; ++u) {
                                         o[g][u][nt][j] *= f;
@@ -713,6 +725,9 @@ __global__ void __launch_bounds__(max_warps(NT) * 32, 1) decode_int4_kernel(cons
                                 z[r][1] = __byte_perm(w0, w1, perm1);
                             }
 #pragma unroll
+                            for (int nt = 0; nt < NT; ++nt)
+                                pa::mma_16816<false>(mid[nt], eights[g], pb[g][nt][0], pb[g][nt][1]);
+#pragma unroll
                             for (int u = 0; u < 4; ++u) {
                                 // u even: the byte's lower code; u odd: the whole byte, lower
                                 // code plus 16 times the upper one, which the end takes apart
@@ -757,7 +772,7 @@ __global__ void __launch_bounds__(max_warps(NT) * 32, 1) decode_int4_kernel(cons
             const uint32_t at = segn == 0 ? L.slots + (uint32_t)warp * slot_floats(G, D) * 4
                                           : (uint32_t)warp * S * kStage;
             float* slot = reinterpret_cast<float*>(smem + at);
-            const float low = pa::exp2_int(min(24 - vexp, 127)), high = low * 0.0625f;
+            const float low = pa::exp2_int(min(24 - vexp, 127));
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -775,8 +790,9 @@ __global__ void __launch_bounds__(max_warps(NT) * 32, 1) decode_int4_kernel(cons
 #pragma unroll
                         for (int u = 0; u < 8; ++u) {
                             const int e = 2 * (u >> 2) + j;
-                            const float sum = u & 1 ? (o[g][u & 3][nt][e] - o[g][(u & 3) - 1][nt][e]) * high
-                                                    : o[g][u & 3][nt][e] * low;
+                            const float code = u & 1 ? (o[g][u & 3][nt][e] - o[g][(u & 3) - 1][nt][e]) * 0.0625f
+                                                     : o[g][u & 3][nt][e];
+                            const float sum = (code - mid[nt][2 * g + j]) * low;
                             v[u] = (sum + lowv[nt][g][j]) * inv;
                         }
                         const int at_d = 64 * g + 8 * cr;
