@@ -172,17 +172,30 @@ __global__ void __launch_bounds__(kThreads, 2) score_kernel(const SelectParams p
     asm volatile("griddepcontrol.launch_dependents;");   // the selection may be launched: it waits
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int32_t i = blockIdx.y, g0 = blockIdx.z * p.heads, heads = min(p.heads, p.Hkv - g0);
-    const int32_t nb = (context_of(p, i) + p.bs - 1) / p.bs;
-    const int32_t j0 = p.first + blockIdx.x * p.tile, j1 = min(nb - p.last, j0 + p.tile);
-    if (nb <= p.keep || j0 >= j1) return;
+    const int32_t j0 = p.first + blockIdx.x * p.tile;
     // Shared memory: the ring, the query codes [heads * G][D / 4] and their steps, the tile's
-    // block ids (-1: not the pool's).
+    // block ids (-1: not the pool's).  Ids are read up to the table's end and query heads up to
+    // one a warp before the context's length is known: three reads under way at once.
     const int nq = heads * p.G;
     uint32_t* codes = smem + kRing * kStepBytes / 4;
     float* sq = reinterpret_cast<float*>(codes + nq * (D / 4));
     int32_t* ids = reinterpret_cast<int32_t*>(sq + nq);
+    const int32_t* table = p.block_tables + (int64_t)i * p.max_blocks + j0;
+    const int32_t room = p.max_blocks - p.last - j0;
+    const int32_t id0 = tid < min(p.tile, room) ? __ldg(table + tid) : 0;
+    uint32_t qw[D / 64];
+    auto load_q = [&](int h) {
+#pragma unroll
+        for (int j = 0; j < D / 64; ++j)
+            qw[j] = __ldg(reinterpret_cast<const uint32_t*>(
+                p.q + ((int64_t)i * p.H + g0 * p.G + h) * D + j * 64 + lane * 2));
+    };
+    load_q(min(warp, nq - 1));
+    const int32_t nb = (context_of(p, i) + p.bs - 1) / p.bs;
+    const int32_t j1 = min(nb - p.last, j0 + p.tile);
+    if (nb <= p.keep || j0 >= j1) return;
     for (int32_t t = tid; t < j1 - j0; t += kThreads) {
-        int32_t id = __ldg(p.block_tables + (int64_t)i * p.max_blocks + j0 + t);
+        int32_t id = t == tid ? id0 : __ldg(table + t);
         if ((uint32_t)id >= (uint32_t)p.num_blocks) {
             if (g0 == 0) pa::raise_error(p.err, PA_DEVERR_BLOCK_ID);
             id = -1;
@@ -190,12 +203,12 @@ __global__ void __launch_bounds__(kThreads, 2) score_kernel(const SelectParams p
         ids[t] = id;
     }
     for (int h = warp; h < nq; h += kThreads / 32) {
-        const uint16_t* q = p.q + ((int64_t)i * p.H + g0 * p.G + h) * D;
+        if (h != warp) load_q(h);
         float2 x[D / 64];
         float a = 0.f;
 #pragma unroll
         for (int j = 0; j < D / 64; ++j) {
-            x[j] = widen2<kBF16>(__ldg(reinterpret_cast<const uint32_t*>(q + j * 64 + lane * 2)));
+            x[j] = widen2<kBF16>(qw[j]);
             a = fmaxf(a, fmaxf(fabsf(x[j].x), fabsf(x[j].y)));
         }
         // the bit patterns of non-negative floats order like the values
@@ -248,6 +261,7 @@ __global__ void __launch_bounds__(kThreads, 2) score_kernel(const SelectParams p
         }
         const float S = reinterpret_cast<const float*>(at + kItems * 32 * kThreads)[tid];
         float best = 0.f;
+#pragma unroll 4
         for (int h = 0; h < p.G; ++h) {
             const uint4 cv = qc[h * kLanes];
             const uint32_t c[4] = {cv.x, cv.y, cv.z, cv.w};
@@ -277,14 +291,14 @@ __global__ void __launch_bounds__(kThreads, 2) score_kernel(const SelectParams p
     }
 }
 
-constexpr int kSelThreads = 512;
+constexpr int kSelThreads = 256;
 constexpr int kSelWarps = kSelThreads / 32;
-constexpr int kBinBits = 11, kBins = 1 << kBinBits;
+constexpr int kBinBits = 10, kBins = 1 << kBinBits;   // four bins a thread
 
 // One CTA per (sequence, KV head): the k-th largest score, then the chosen ids in context
-// order.  Bound by latency (a handful of barriers).  The keys' range is cut into 2048 bins,
+// order.  Bound by latency (a handful of barriers).  The keys' range is cut into 1024 bins,
 // whose counts from the top name the bin of the k-th largest; that bin is cut again until
-// it is one key wide or wanted whole (three passes at most, one or two in practice).  Each
+// it is one key wide or wanted whole (four passes at most, one or two in practice).  Each
 // thread owns a contiguous stretch of the keys: kPer of them in registers, or (0) any
 // number, read again from L2 by each pass.
 template <int kPer>
@@ -361,7 +375,7 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams 
             if (width == 32 || (x >> width) == 0) atomicAdd(&hist[x >> shift], 1u);
         });
         __syncthreads();
-        // Counts from the top: thread t owns bins 4 t' .. 4 t' + 3 with t' = 511 - t.
+        // Counts from the top: thread t owns bins 4 t' .. 4 t' + 3 with t' = kSelThreads - 1 - t.
         const int b0 = (kSelThreads - 1 - tid) * (kBins / kSelThreads);
         const uint4 c4 = *reinterpret_cast<const uint4*>(hist + b0);
         *reinterpret_cast<uint4*>(hist + b0) = make_uint4(0, 0, 0, 0);
@@ -560,8 +574,9 @@ PA_API pa_status pa_select_blocks(const void* q, const void* boxes, const float*
     attr.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = max_blocks > keep && keep > first + last ? 1 : 0;
-    auto select = most <= 4 * kSelThreads ? select_kernel<4>
-                  : most <= 16 * kSelThreads ? select_kernel<16> : select_kernel<0>;
+    auto select = most <= 2 * kSelThreads ? select_kernel<2>
+                  : most <= 8 * kSelThreads ? select_kernel<8>
+                  : most <= 32 * kSelThreads ? select_kernel<32> : select_kernel<0>;
     return pa::cuda_status(cudaLaunchKernelEx(&cfg, select, p));
 }
 
