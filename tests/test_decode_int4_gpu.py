@@ -228,3 +228,37 @@ def test_append_decode_and_read_back_into_multi_query():
         k, v = (torch.from_numpy(o.gather_int4(c, sm, at)).float().bfloat16().double().numpy()
                 for c, sm in ((host[0], host[2]), (host[1], host[3])))
         assert_close(out[i].cpu(), o.softmax_attention(q[i].double().numpy(), k, v, d ** -0.5))
+
+
+@pytest.mark.parametrize("H,Hkv,d", [(8, 1, 128), (16, 1, 64)])
+def test_the_largest_batch(H, Hkv, d):
+    """4096 sequences: the list's prefix sums take shared memory from the rings."""
+    rng = np.random.default_rng(2)
+    lens = np.where(rng.random(4096) < 0.9, 0, rng.integers(1, 90, 4096))
+    lens[[0, 4095]] = 130, 77
+    bs = 16
+    tbl, N = rand_tables(lens, bs, 2)
+    cache = int4_cache(N, Hkv, bs, d, 8)
+    q = wl.normal_tensor((4096, H, d), torch.bfloat16, 1)
+    got = run(q, cache, tbl, lens, 0.1)
+    assert binding.pa_check_device_errors() == 0
+    check(q, cache, tbl, lens, 0.1, got)
+
+
+def test_seeded_random_shapes():
+    """Groupings, block sizes and length mixes beyond the listed ones."""
+    rng = np.random.default_rng(77)
+    for _ in range(12):
+        G = int(rng.choice([1, 2, 3, 4, 5, 6, 7, 8, 9, 11, 13, 16, 48]))
+        Hkv, d, bs = int(rng.integers(1, 5)), int(rng.choice([64, 128])), int(rng.choice([8, 16, 32]))
+        B = int(rng.integers(1, 9))
+        lens = [int(x) for x in np.exp(rng.uniform(0, np.log(1500), B))]
+        lens[int(rng.integers(0, B))] = 0
+        dtype = torch.float16 if rng.random() < 0.5 else torch.bfloat16
+        tbl, N = rand_tables(lens, bs, G)
+        cache = int4_cache(N, Hkv, bs, d, G + d)
+        nan_behind(cache, lens, tbl, bs)
+        q = wl.normal_tensor((B, Hkv * G, d), dtype, G)
+        got = run(q, cache, tbl, lens, d ** -0.5)
+        assert binding.pa_check_device_errors() == 0, (G, Hkv, d, bs, lens)
+        check(q, cache, tbl, lens, d ** -0.5, got)

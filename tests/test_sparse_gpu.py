@@ -101,6 +101,10 @@ CASES = [  # lens, bs, H, Hkv, d, dtype, keep, first, last
     ([900, 901, 927, 928, 929], 32, 12, 1, 64, torch.float16, 7, 0, 1),
     ([600, 20], 16, 32, 1, 128, torch.float16, 20, 3, 3),          # two groups of 16 heads
     ([40000], 8, 4, 1, 64, torch.bfloat16, 333, 0, 1),
+    ([300, 77], 16, 40, 40, 128, torch.float16, 6, 1, 1),          # more KV heads than lane groups
+    ([260], 16, 70, 70, 64, torch.bfloat16, 5, 0, 2),
+    ([100, 33], 8, 4, 2, 64, torch.float16, 40, 1, 1),             # everything is kept
+    ([200, 90], 8, 4, 2, 64, torch.float16, 3, 1, 2),              # nothing but the ends is
 ]
 
 
@@ -120,7 +124,7 @@ def test_select_then_decode(lens, bs, H, Hkv, d, dtype, keep, first, last):
 
 
 @pytest.mark.parametrize("scores", ["equal", "zero", "two"])
-@pytest.mark.parametrize("nblk,keep", [(50, 7), (1000, 300), (5000, 64)])
+@pytest.mark.parametrize("nblk,keep", [(50, 7), (515, 300), (2052, 300), (5000, 64), (9001, 5000)])
 def test_ties_go_to_the_lower_position(scores, nblk, keep):
     bs, d, Hkv = 8, 64, 2
     lens = [nblk * bs - 3]
@@ -134,6 +138,28 @@ def test_ties_go_to_the_lower_position(scores, nblk, keep):
     sel, n = _select(q, hb, hs, tbl, lens, bs, keep, 2, 2)
     want, wn = o.select_blocks(q.float().numpy(), hb, hs, tbl, lens, bs, keep, 2, 2)
     assert np.array_equal(sel.cpu().numpy(), want) and np.array_equal(n.cpu().numpy(), wn)
+
+
+@pytest.mark.parametrize("H,Hkv,d", [(128, 1, 128), (256, 2, 64)])
+def test_selection_for_wide_groups(H, Hkv, d):
+    """Up to 128 query heads a KV head (the decode takes them sixteen at a time)."""
+    lens, bs = [900, 250], 16
+    q, k, v, tbl, hb, hs = _case(lens, bs, H, Hkv, d, torch.bfloat16, 5)
+    sel, n = _select(q, hb, hs, tbl, lens, bs, 9, 1, 1)
+    want, wn = o.select_blocks(q.float().numpy(), hb, hs, tbl, lens, bs, 9, 1, 1)
+    assert np.array_equal(sel.cpu().numpy(), want) and np.array_equal(n.cpu().numpy(), wn)
+
+
+def test_scores_of_every_sign_zero_and_subnormal_order_alike():
+    """Keys far below one, queries of both signs, boxes of zero scale among them."""
+    lens, bs, Hkv, d = [1600], 8, 2, 64
+    q, k, v, tbl, hb, hs = _case(lens, bs, 4, Hkv, d, torch.float16, 9)
+    hs *= np.float32(2.0) ** np.random.default_rng(3).integers(-140, 20, hs.shape).astype(np.float32)
+    hs[::7] = 0
+    q[0, 1] = 0
+    sel, n = _select(q, hb, hs, tbl, lens, bs, 60, 0, 1)
+    want, wn = o.select_blocks(q.float().numpy(), hb, hs, tbl, lens, bs, 60, 0, 1)
+    assert np.array_equal(sel.cpu().numpy(), want)
 
 
 def test_selection_flags_bad_input():
