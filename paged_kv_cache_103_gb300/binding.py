@@ -189,8 +189,15 @@ def _stream_ptr(stream):
     return stream.cuda_stream
 
 
+_CODES = {}   # torch dtype -> pa_dtype, filled on first use
+
+
 def _dtype_code(t) -> int:
+    code = _CODES.get(t.dtype)
+    if code is not None:
+        return code
     import torch
+    _CODES.update({torch.float16: PA_F16, torch.bfloat16: PA_BF16})
     if t.dtype == torch.float16:
         return PA_F16
     if t.dtype == torch.bfloat16:

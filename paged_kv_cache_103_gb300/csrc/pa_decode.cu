@@ -230,6 +230,8 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap kmap,
                     const __grid_constant__ CUtensorMap ksmap,
                     const __grid_constant__ CUtensorMap vsmap, const DecodeParams p) {
     static_assert(!kFp8 || D == 128, "FP8 rows are one 128-byte swizzle row");
+    // Launched while the kernel before it (the selection of its block lists) may still run.
+    if constexpr (kPair) asm volatile("griddepcontrol.wait;" ::: "memory");
     constexpr int kProducerWarps = producer_warps(kFp8);
     constexpr int kThreads = cta_threads(kFp8);
     constexpr uint32_t kHalves = kFp8 ? 1 : D / 64;  // 128-byte pieces of a token row
@@ -1247,8 +1249,23 @@ pa_status launch(const CUtensorMap& km, const CUtensorMap& vm, const CUtensorMap
     // The 8-bit register split adds up only against this launch allocation: a
     // kernel built with another count would wait forever in setmaxnreg.
     if (kFp8 && regs != kQ8LaunchRegs) return PA_ERR_UNSUPPORTED;
-    kern<<<pa_decode_grid_size(), cta_threads(kFp8), smem, stream>>>(km, vm, ksm, vsm, prm);
-    return pa::cuda_status(cudaGetLastError());
+    if constexpr (kPair) {
+        // Started early, so that its launch hides behind the selection's last barriers.
+        cudaLaunchAttribute attr{};
+        attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr.val.programmaticStreamSerializationAllowed = 1;
+        cudaLaunchConfig_t cfg{};
+        cfg.gridDim = dim3((unsigned)pa_decode_grid_size());
+        cfg.blockDim = dim3((unsigned)cta_threads(kFp8));
+        cfg.dynamicSmemBytes = smem;
+        cfg.stream = stream;
+        cfg.attrs = &attr;
+        cfg.numAttrs = 1;
+        return pa::cuda_status(cudaLaunchKernelEx(&cfg, kern, km, vm, ksm, vsm, prm));
+    } else {
+        kern<<<pa_decode_grid_size(), cta_threads(kFp8), smem, stream>>>(km, vm, ksm, vsm, prm);
+        return pa::cuda_status(cudaGetLastError());
+    }
 }
 
 template <int D, bool kBF16, bool kFp8, bool kInt8 = false, bool kPair = false>

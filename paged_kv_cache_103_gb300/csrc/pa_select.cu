@@ -306,6 +306,8 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams 
     __shared__ __align__(16) uint32_t hist[kBins];
     __shared__ uint32_t s_top[kSelWarps], s_low[kSelWarps], wsum[kSelWarps], wsum2[kSelWarps];
     __shared__ uint32_t s_bin, s_rank, s_count;
+    // What reads the lists may be launched: it waits for this grid's end.
+    asm volatile("griddepcontrol.launch_dependents;");
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int32_t g = blockIdx.x, i = blockIdx.y;
     const int64_t pair = (int64_t)i * p.Hkv + g;
