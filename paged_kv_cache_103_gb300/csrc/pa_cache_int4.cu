@@ -135,6 +135,7 @@ reshape_and_cache_int4_kernel(const uint4* __restrict__ k_new, const uint4* __re
                               uint32_t* __restrict__ k_scale, uint32_t* __restrict__ v_scale,
                               int64_t num_slots, unsigned int* __restrict__ err) {
     constexpr uint32_t kRow = D / kAppend;     // threads per row
+    asm volatile("griddepcontrol.launch_dependents;");   // the decode may be launched: it waits
     const uint32_t v = blockIdx.x * kThreads + threadIdx.x;
     // vecs is a multiple of 4 (a group's threads), so a group is whole or absent; absent
     // threads still take part in the shuffles.
@@ -218,6 +219,7 @@ gather_cache_kernel(const void* __restrict__ k_cache, const void* __restrict__ v
                     uint32_t Hkv, int bs_shift, int64_t num_slots, uint4* __restrict__ k_out,
                     uint4* __restrict__ v_out, unsigned int* __restrict__ err) {
     constexpr uint32_t kRow = D / kVec;
+    asm volatile("griddepcontrol.wait;" ::: "memory");   // launched while an append may run
     int64_t slot[kUnroll];
     uint32_t h[kUnroll];
     uint2 kc[kUnroll], vc[kUnroll];
@@ -324,12 +326,22 @@ pa_status gather(const void* k_cache, const void* v_cache, const void* k_scale,
         const int64_t n = T_tokens - t0 < slab ? T_tokens - t0 : slab;
         const uint32_t vecs = (uint32_t)(n * row), per = vecs >= fill ? 4 : 1;
         auto kern = per == 4 ? gather_cache_kernel<kBF16, F, D, 4> : gather_cache_kernel<kBF16, F, D, 1>;
-        kern<<<(vecs + per * kThreads - 1) / (per * kThreads), kThreads, 0, st>>>(
-            k_cache, v_cache, static_cast<const uint32_t*>(k_scale),
-            static_cast<const uint32_t*>(v_scale), slots + t0, vecs, by_heads, (uint32_t)Hkv,
-            shift_of(block_size), (int64_t)num_blocks * block_size,
-            static_cast<uint4*>(k_out) + t0 * row, static_cast<uint4*>(v_out) + t0 * row, err);
-        if (cudaGetLastError() != cudaSuccess) return PA_ERR_CUDA;
+        // Started early, so that its launch hides behind an append's end.
+        cudaLaunchAttribute attr{};
+        attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr.val.programmaticStreamSerializationAllowed = 1;
+        cudaLaunchConfig_t cfg{};
+        cfg.gridDim = dim3((vecs + per * kThreads - 1) / (per * kThreads));
+        cfg.blockDim = dim3(kThreads);
+        cfg.stream = st;
+        cfg.attrs = &attr;
+        cfg.numAttrs = 1;
+        if (cudaLaunchKernelEx(&cfg, kern, k_cache, v_cache, static_cast<const uint32_t*>(k_scale),
+                               static_cast<const uint32_t*>(v_scale), slots + t0, vecs, by_heads,
+                               (uint32_t)Hkv, shift_of(block_size), (int64_t)num_blocks * block_size,
+                               static_cast<uint4*>(k_out) + t0 * row,
+                               static_cast<uint4*>(v_out) + t0 * row, err) != cudaSuccess)
+            return PA_ERR_CUDA;
     }
     return PA_OK;
 }

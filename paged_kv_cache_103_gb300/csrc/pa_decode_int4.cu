@@ -263,6 +263,8 @@ __global__ void __launch_bounds__(max_warps(NT) * 32, 1) decode_int4_kernel(cons
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int32_t max_len = p.max_blocks << bs_shift;
 
+    asm volatile("griddepcontrol.wait;" ::: "memory");   // launched while the kernel before may run
+
     // The tables and queries are read a dependent load or two from now: into L2 with
     // them, a line per thread (what they cover is shared by all CTAs).
     {
@@ -820,6 +822,7 @@ __global__ void __launch_bounds__(max_warps(NT) * 32, 1) decode_int4_kernel(cons
             if (pos < hi) s = next_pair(prefix, Hkv, s);
         }
     }
+    asm volatile("griddepcontrol.launch_dependents;");   // a next call may be launched: it waits
     __syncthreads();
 
     // ====================== runs of one pair in several warps ======================
@@ -1045,8 +1048,18 @@ pa_status launch(const Int4Params& p, cudaStream_t stream) {
     if (ctas <= 0) return PA_ERR_CUDA;
     if (ctas > kMaxCtas) ctas = kMaxCtas;
     const Layout L = make_layout(D, p.G, p.B, p.warps);
-    kern<<<ctas, p.warps * 32, L.total, stream>>>(p);
-    return pa::cuda_status(cudaGetLastError());
+    // Started early, so that its launch hides behind the append's or another call's end.
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)ctas);
+    cfg.blockDim = dim3((unsigned)p.warps * 32);
+    cfg.dynamicSmemBytes = L.total;
+    cfg.stream = stream;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return pa::cuda_status(cudaLaunchKernelEx(&cfg, kern, p));
 }
 
 template <int D, bool kBF16, int NT, bool kOne>
