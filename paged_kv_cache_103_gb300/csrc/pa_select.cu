@@ -202,24 +202,6 @@ __global__ void __launch_bounds__(kThreads, 2) score_kernel(const SelectParams p
         }
         ids[t] = id;
     }
-    for (int h = warp; h < nq; h += kThreads / 32) {
-        if (h != warp) load_q(h);
-        float2 x[D / 64];
-        float a = 0.f;
-#pragma unroll
-        for (int j = 0; j < D / 64; ++j) {
-            x[j] = widen2<kBF16>(qw[j]);
-            a = fmaxf(a, fmaxf(fabsf(x[j].x), fabsf(x[j].y)));
-        }
-        // the bit patterns of non-negative floats order like the values
-        a = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(a)));
-        const float s = __fdiv_rn(a, 127.f);
-#pragma unroll
-        for (int j = 0; j < D / 64; ++j)
-            reinterpret_cast<uint16_t*>(codes)[h * (D / 2) + j * 32 + lane] =
-                s > 0.f ? (uint16_t)(code8(x[j].x, s) | code8(x[j].y, s) << 8) : 0;
-        if (lane == 0) sq[h] = s;
-    }
     __syncthreads();
     const int unit = tid / kLanes, l = tid % kLanes, rows = kUnits / heads;
     // KV head, and which of the blocks in flight (none for the lane groups left over, which
@@ -246,6 +228,26 @@ __global__ void __launch_bounds__(kThreads, 2) score_kernel(const SelectParams p
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
     for (int step = 0; step < kRing - 1; ++step) load(step);
+    // ---- the query's codes, while the first boxes are under way
+    for (int h = warp; h < nq; h += kThreads / 32) {
+        if (h != warp) load_q(h);
+        float2 x[D / 64];
+        float a = 0.f;
+#pragma unroll
+        for (int j = 0; j < D / 64; ++j) {
+            x[j] = widen2<kBF16>(qw[j]);
+            a = fmaxf(a, fmaxf(fabsf(x[j].x), fabsf(x[j].y)));
+        }
+        // the bit patterns of non-negative floats order like the values
+        a = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(a)));
+        const float s = __fdiv_rn(a, 127.f);
+#pragma unroll
+        for (int j = 0; j < D / 64; ++j)
+            reinterpret_cast<uint16_t*>(codes)[h * (D / 2) + j * 32 + lane] =
+                s > 0.f ? (uint16_t)(code8(x[j].x, s) | code8(x[j].y, s) << 8) : 0;
+        if (lane == 0) sq[h] = s;
+    }
+    __syncthreads();
     for (int32_t step = 0; step < steps; ++step) {
         load(step + kRing - 1);
         asm volatile("cp.async.wait_group %0;" ::"n"(kRing - 1) : "memory");
