@@ -25,7 +25,7 @@
  *     16-byte aligned.  A token's slot is physical_block * block_size +
  *     offset_in_block.
  *   - Supported shapes: head_dim 64 or 128; block_size 8, 16 or 32;
- *     num_heads % num_kv_heads == 0; for pa_decode and pa_decode_fp8 the
+ *     num_heads % num_kv_heads == 0; for the pa_decode family the
  *     group G = num_heads / num_kv_heads is at most 16 or a multiple of 16
  *     (wider groups, e.g. multi-query attention, are processed 16 query heads
  *     at a time); fp16 or bf16 elements.  Other shapes return
@@ -541,7 +541,8 @@ PA_API pa_status pa_decode_int8(const void* q, const void* k_cache, const void* 
  * bf16 q is scaled by a power of two into f16 range first (exact for its elements
  * down to 2^-25 of its largest).  A table entry outside the pool reads rows of
  * zeros and sets PA_DEVERR_BLOCK_ID.  Other arguments, the workspace
- * (pa_decode_workspace_size) and the errors are those of pa_decode.
+ * (pa_decode_workspace_size, here 16-byte aligned) and the errors are those of
+ * pa_decode.
  *   q, out           (device) 16-byte aligned
  *   k_cache, v_cache (device) [num_blocks][Hkv][block_size][d / 2] uint8, 16-byte aligned
  *   k_scale, v_scale (device) [num_blocks][Hkv][block_size][d / 64][2] f16,
@@ -599,7 +600,8 @@ PA_API pa_status pa_summarize_blocks(const void* k_cache, const int32_t* block_i
  * PA_DEVERR_TABLE_WIDTH; an id outside the pool scores lowest, sets
  * PA_DEVERR_BLOCK_ID and is passed on if chosen all the same.
  *   q            (device) [B][H][d] fp16/bf16 (dtype), 16-byte aligned
- *   keep         >= first + last, first >= 0, last >= 1;  H / Hkv <= 128
+ *   keep         >= first + last, first >= 0, last >= 1;  H / Hkv <= 128,
+ *                Hkv <= 65535
  *   sel_blocks   (device) [B][Hkv][keep] int32;  sel_lens (device) [B][Hkv] int32
  *   workspace    (device, 4-byte aligned) >= pa_select_blocks_workspace_size(B,
  *                Hkv, max_blocks) bytes of any contents (the scores).  Calls that
@@ -618,8 +620,8 @@ PA_API pa_status pa_select_blocks(const void* q, const void* boxes, const float*
  * tokens of the blocks sel_blocks[i][h / G][:].  sel_blocks [B][Hkv][keep] and
  * sel_lens [B][Hkv] are those of pa_select_blocks (any lists will do); max_sel_len
  * is an upper bound of sel_lens.  B * Hkv is at most 4096.  Other arguments, the
- * workspace (pa_decode_workspace_size(B, H, d)) and the errors are those of
- * pa_decode; a pair of length 0 gives zero rows. */
+ * workspace (pa_decode_workspace_size(B, H, d) bytes, here 16-byte aligned) and
+ * the errors are those of pa_decode; a pair of length 0 gives zero rows. */
 PA_API pa_status pa_decode_selected(const void* q, const void* k_cache, const void* v_cache,
                                     const int32_t* sel_blocks, int32_t keep,
                                     const int32_t* sel_lens, int32_t max_sel_len, int32_t B,

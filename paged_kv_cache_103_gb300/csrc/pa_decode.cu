@@ -1485,7 +1485,8 @@ PA_API pa_status pa_decode_selected(const void* q, const void* k_cache, const vo
         return PA_ERR_INVALID;
     if ((reinterpret_cast<uintptr_t>(k_cache) | reinterpret_cast<uintptr_t>(v_cache)) & 15u)
         return PA_ERR_INVALID;
-    if ((reinterpret_cast<uintptr_t>(q) & 3u) || (reinterpret_cast<uintptr_t>(out) & 15u))
+    if ((reinterpret_cast<uintptr_t>(q) & 3u) || (reinterpret_cast<uintptr_t>(out) & 15u) ||
+        (reinterpret_cast<uintptr_t>(workspace) & 15u))
         return PA_ERR_INVALID;
 
     unsigned int* err = pa::device_error_word();

@@ -1112,7 +1112,8 @@ PA_API pa_status pa_decode_int4(const void* q, const void* k_cache, const void* 
         return PA_ERR_INVALID;
     if ((reinterpret_cast<uintptr_t>(k_cache) | reinterpret_cast<uintptr_t>(v_cache) |
          reinterpret_cast<uintptr_t>(k_scale) | reinterpret_cast<uintptr_t>(v_scale) |
-         reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(out)) & 15u)
+         reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(out) |
+         reinterpret_cast<uintptr_t>(workspace)) & 15u)
         return PA_ERR_INVALID;
     Int4Params p;
     p.warps = choose_warps(d, G, B);

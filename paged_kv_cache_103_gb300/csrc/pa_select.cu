@@ -510,7 +510,7 @@ PA_API pa_status pa_select_blocks(const void* q, const void* boxes, const float*
         keep < 1 || (int64_t)first + last > keep)
         return PA_ERR_INVALID;
     if (dtype != PA_F16 && dtype != PA_BF16) return PA_ERR_UNSUPPORTED;
-    if (H % Hkv != 0 || H / Hkv > 128) return PA_ERR_UNSUPPORTED;
+    if (H % Hkv != 0 || H / Hkv > 128 || Hkv > 65535) return PA_ERR_UNSUPPORTED;
     if (d != 64 && d != 128) return PA_ERR_UNSUPPORTED;
     if (block_size != 8 && block_size != 16 && block_size != 32) return PA_ERR_UNSUPPORTED;
     if (B > 4096 || (int64_t)max_blocks * block_size > INT32_MAX) return PA_ERR_UNSUPPORTED;

@@ -141,3 +141,17 @@ def test_step_executor_takes_a_4_bit_cache(lib):
         kw = dict(dict(k_cache=c, v_cache=c, k_scale=s, v_scale=s, dtype=torch.float16), **bad)
         with pytest.raises(ValueError):
             binding.Step(alloc, 2, 4, Hkv, d, 4, 64, scale=0.1, kv_format="int4", **kw)
+
+
+def test_workspaces_that_would_fault(lib):
+    """Partial results are stored 16 bytes at a time, so a workspace between two such places is refused."""
+    for ws, want in ((ODD, INVALID), (ctypes.c_void_p(16 * 1024 + 8), INVALID), (None, INVALID)):
+        assert lib.pa_decode_int4(P, P, P, P, P, P, 4, P, 64, 2, 4, 2, 128, 16, 8, 0.1, 0, P, ws, 1 << 24,
+                                  None) == want
+        assert lib.pa_decode_selected(P, P, P, P, 4, P, 64, 2, 4, 2, 128, 16, 8, 0.1, 0, P, ws, 1 << 24,
+                                      None) == want
+
+
+def test_selection_refuses_more_kv_heads_than_a_grid_has_rows(lib):
+    assert lib.pa_select_blocks(P, P, P, P, 4, P, 1, 1 << 17, 1 << 17, 64, 16, 8, 2, 0, 1, 0, P, P, P, 1 << 30,
+                                None) == UNSUPPORTED
