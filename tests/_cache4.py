@@ -62,8 +62,8 @@ def decode_bound(q, cache, tbl, lens, scale, dtype, ref):
     """Largest |gpu - ref| per output element.
 
     * the output is rounded once: eps / 2 of |ref|;
-    * P (a probability times the step s) is rounded to f16 once, 2^-11 of it: its terms
-      s c are nonnegative, so at most 2^-11 of sum_j w_j s c (the minima stay fp32);
+    * P (a probability times the step s) is rounded to f16 once, 2^-11 of it, and multiplies
+      c - 8 (the value of code 8 stays fp32): at most 2^-11 of sum_j w_j s |c - 8|;
     * a logit error of D moves the output by at most 2 D max |v|.  A logit is a sum of at most
       2 d products in fp32, in MMA steps of 16 (each step's rounding 2^-22 of the largest partial
       sum, at most 16 of them) and a handful of fp32 operations: D <= 2^-17 scale sum |q| (s c + |m|);
@@ -87,7 +87,8 @@ def decode_bound(q, cache, tbl, lens, scale, dtype, ref):
         v = np.where(ok[:, None, None], o.gather_int4(codes_v, vs, at), 0)
         mk = np.repeat(np.abs(ks[at // bs, :, at % bs, :, 1].astype(np.float64)), 64, -1)
         mv = np.repeat(vs[at // bs, :, at % bs, :, 1].astype(np.float64), 64, -1)
-        sc_v = np.where(ok[:, None, None], v - mv, 0)          # s c
+        sv = np.repeat(vs[at // bs, :, at % bs, :, 0].astype(np.float64), 64, -1)
+        off_v = np.where(ok[:, None, None], np.abs(v - mv - 8 * sv), 0)     # s |c - 8|
         mag_k = np.where(ok[:, None, None], np.abs(k) + 2 * mk, 0)
         for h in range(H):
             g = h // G
@@ -96,7 +97,7 @@ def decode_bound(q, cache, tbl, lens, scale, dtype, ref):
             w /= w.sum()
             D = 2.0 ** -17 * abs(scale) * (mag_k[:, g] @ np.abs(q[i, h])).max()
             vmax = np.abs(v[:, g]).max()
-            bound[i, h] += 2.0 ** -11 * (w @ sc_v[:, g]) + (2 * D + 2.0 ** -19) * vmax
+            bound[i, h] += 2.0 ** -11 * (w @ off_v[:, g]) + (2 * D + 2.0 ** -19) * vmax
     return bound
 
 
