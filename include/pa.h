@@ -538,8 +538,8 @@ PA_API pa_status pa_decode_int8(const void* q, const void* k_cache, const void* 
 /* pa_decode over a 4-bit cache written by pa_reshape_and_cache_int4: computes
  * what pa_decode computes with the rows K_j, V_j that the codes stand for (s c + m
  * per group of 64 values), for d = 64 or 128.  Both products take fp32 sums; a
- * bf16 q is scaled by a power of two into f16 range first (exact for its elements
- * down to 2^-25 of its largest).  A table entry outside the pool reads rows of
+ * bf16 q is scaled by a power of two into f16 range first (exact for elements
+ * down to 2^-25 of the KV head's largest).  A table entry outside the pool reads rows of
  * zeros and sets PA_DEVERR_BLOCK_ID.  Other arguments, the workspace
  * (pa_decode_workspace_size, here 16-byte aligned) and the errors are those of
  * pa_decode.
