@@ -940,8 +940,13 @@ __global__ void __launch_bounds__(max_warps(NT) * 32, 1) decode_int4_kernel(cons
         is_last[warp] = last;
     }
     __syncthreads();
+    // Two pairs to join: half the threads each, so that their loads are under way together.
+    const bool both = n_open == 2 && is_last[0] && is_last[1];
+    const int team = both ? threads / 2 : threads, my_w = both && tid >= team ? 1 : 0;
+    const int ltid = tid - my_w * team;
 #pragma unroll 1
-    for (int w = 0; w < n_open; ++w) {
+    for (int w0 = 0; w0 < (both ? 1 : n_open); ++w0) {
+        const int w = both ? my_w : w0;
         if (!is_last[w]) continue;
         const Run r = runs[open_lead(w)];
         const int c_first = cut.part(r.a), n = cut.part(r.a + r.nc - 1) - c_first + 1;
@@ -949,12 +954,12 @@ __global__ void __launch_bounds__(max_warps(NT) * 32, 1) decode_int4_kernel(cons
         const float* rest = p.partials + 2 * (int64_t)c_first * kPartial;
         // A group of threads has the outputs, four each; the groups take the partials in
         // turn, eight loads in flight, and join through shared memory.
-        const int wide = min(outs, threads), groups = threads / wide;
-        const int grp = tid / wide;
-        float4* acc_at = reinterpret_cast<float4*>(smem);              // [groups][outs]
-        float2* ml_at = reinterpret_cast<float2*>(acc_at + threads);
+        const int wide = min(outs, team), groups = team / wide;
+        const int grp = ltid / wide;
+        float4* acc_at = reinterpret_cast<float4*>(smem) + my_w * team;   // [groups][outs]
+        float2* ml_at = reinterpret_cast<float2*>(reinterpret_cast<float4*>(smem) + threads) + my_w * team;
 #pragma unroll 1
-        for (int e = tid - grp * wide; e < outs && grp < groups; e += wide) {
+        for (int e = ltid - grp * wide; e < outs && grp < groups; e += wide) {
             const int h = e / (D / 4);
             float M = -INFINITY, l = 0.f;
             float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -1007,7 +1012,7 @@ __global__ void __launch_bounds__(max_warps(NT) * 32, 1) decode_int4_kernel(cons
         if (groups > 1) {
             __syncthreads();
 #pragma unroll 1
-            for (int e = tid; e < outs; e += threads) {
+            for (int e = ltid; e < outs; e += team) {
                 const int use = min(groups, n);
                 float M = -INFINITY, l = 0.f;
                 float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
