@@ -25,23 +25,22 @@
 // the 16-bit cache keeps four math warps and two loading warps per CTA; at a third
 // of the bytes per token the loading warps' hand-offs and the math would both be in
 // the way, so here every warp is on its own.  The list of (sequence, KV head,
-// 32-token chunk) triples is cut evenly over the CTAs and, inside each, over its
-// warps; a warp streams its run of chunks through a ring of its own in shared
+// 32-token chunk) triples is cut into parts of equal cost for the CTAs and, inside each,
+// for its warps; a warp streams its run of chunks through a ring of its own in shared
 // memory by asynchronous 16-byte copies, 512 contiguous bytes an instruction, that it
 // alone waits for.  No two warps meet before the end, when the pairs that cross from
 // warp to warp are merged in shared memory and those that cross from CTA to CTA
 // through the workspace, by the CTA that arrives last:
 //     M = max m_p,  out = sum_p 2^(m_p - M) o_p / sum_p 2^(m_p - M) l_p.
 //
-// Measured (d = 128, device time): 16 x 32768 tokens of 8 KV heads, G = 4: 109 us, 5.5
+// Measured (d = 128, device time): 16 x 32768 tokens of 8 KV heads, G = 4: 107 us, 5.7
 // TB/s, DRAM traffic 1.000 times the bytes above, 54 % of the ALU's and 28 % of the tensor
 // pipe's cycles, 59 % of the issue slots; 64 sequences of 128 .. 2048 tokens, 40 heads, G =
-// 1: 77 us, 5.2 TB/s; 32 long-tailed contexts, 4 heads of G = 7, 70 MB: 28 us, of which the
-// start is some 5 and the merges and uneven ends as much; 4 sequences of up to 64 tokens:
-// 6 us, all latency.  Asynchronous copies took the place of bulk copies (one per tile,
-// each a turn of a loop over the lanes), and one CTA of 16 warps that of two CTAs of 8,
-// whose pairs crossed CTAs twice as often (79.2 against 77.7 us on the 40-head batch, 31.8
-// against 28.2 us on the long-tailed one).
+// 1: 72 us, 5.5 TB/s; 32 long-tailed contexts, 4 heads of G = 7, 70 MB: 25 us, of which
+// the start is some 4 (lengths, table, first copies) and the joining of pairs at the end as
+// much; 4 sequences of up to 64 tokens: 6 us, all latency.  Asynchronous copies took the
+// place of bulk copies (one per tile, each a turn of a loop over the lanes), and one CTA
+// of 16 warps that of two CTAs of 8, whose pairs crossed CTAs twice as often.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -91,7 +90,7 @@ __host__ __device__ constexpr int partial_floats(int D) { return 2 * kMaxG + kMa
 
 // A run of chunks [c0, end) of one pair that a warp left in shared memory.
 struct Run {
-    int32_t a;    // flattened index of the pair's first chunk; -1: none
+    int32_t a;    // position of the pair in the list; -1: none
     int32_t i, g, c0, end, nc;
     uint32_t at;  // at the end, entry x: the set of runs of the CTA's x-th pair,
     int32_t pad;  // and the first of them (+ 256: other CTAs hold more)
@@ -110,7 +109,7 @@ __host__ __device__ inline Layout make_layout(int D, int G, int B, int warps) {
     L.runs = L.slots + warps * slot_floats(G, D) * 4;       // [2 * warps]
     L.last = L.runs + 2 * warps * (uint32_t)sizeof(Run);     // "the last CTA of the pair"
     L.scan = L.last + 8;
-    L.prefix = L.scan + warps * 4;                          // [B + 1]
+    L.prefix = L.scan + warps * 8;                          // [B + 1]
     L.total = L.prefix + (uint32_t)(B + 1) * 4;
     return L;
 }
@@ -119,19 +118,26 @@ __device__ __forceinline__ int32_t clamp_len(int32_t n, int32_t cap) {
     return n < 0 ? 0 : (n > cap ? cap : n);
 }
 
-// W chunks cut into n parts, the first W % n of them one chunk longer.
+// W units cut into n parts, the first W % n of them one unit longer.
 struct Cut {
     int32_t q, r;
     __device__ Cut(int32_t W, int32_t n) : q(W / n), r(W - W / n * n) {}
     __device__ int32_t begin(int32_t x) const { return x * q + min(x, r); }
-    // the part that holds chunk c
+    // the part that holds position c
     __device__ int32_t part(int32_t c) const {
         const int32_t big = r * (q + 1);
         return c < big ? c / (q + 1) : r + (c - big) / q;
     }
 };
 
-// A position in the flattened list: chunk c of pair (i, g), whose nc chunks start at a.
+// The list of pairs is cut by cost, in units of a chunk: kPairCost of them for the pair itself
+// (its q, its table's first entries, its end), then its nc chunks, from position a on.  Cut
+// by chunks alone, CTAs with many short pairs ended 10 us after those with few: 64 sequences
+// of 128 .. 2048 tokens, 40 heads, took 75.5 us against 72.3 with 2 (71.5 with 1, 73.9 with
+// 3), 32 long-tailed contexts 26.5 us against 24.6 (25.4, 24.4).
+constexpr int kPairCost = 2;
+
+// A position in the list: chunk c of pair (i, g).
 struct Cursor {
     int32_t i, g, c, nc, a;
 };
@@ -145,22 +151,22 @@ __device__ __forceinline__ Cursor find(const int32_t* prefix, int32_t B, int32_t
     }
     Cursor s;
     s.i = lo;
-    s.nc = (prefix[lo + 1] - prefix[lo]) / Hkv;
-    const int32_t local = pos - prefix[lo];
-    s.g = local / s.nc;
-    s.c = local - s.g * s.nc;
-    s.a = prefix[lo] + s.g * s.nc;
+    const int32_t cost = (prefix[lo + 1] - prefix[lo]) / Hkv, local = pos - prefix[lo];
+    s.nc = cost - kPairCost;
+    s.g = local / cost;
+    s.a = prefix[lo] + s.g * cost;
+    s.c = max(0, pos - s.a - kPairCost);
     return s;
 }
 
 // The pair after s (there is one).
 __device__ __forceinline__ Cursor next_pair(const int32_t* prefix, int32_t Hkv, Cursor s) {
-    s.a += s.nc;
+    s.a += kPairCost + s.nc;
     s.c = 0;
     if (++s.g == Hkv) {
         s.g = 0;
         do ++s.i; while (prefix[s.i + 1] == prefix[s.i]);
-        s.nc = (prefix[s.i + 1] - prefix[s.i]) / Hkv;
+        s.nc = (prefix[s.i + 1] - prefix[s.i]) / Hkv - kPairCost;
     }
     return s;
 }
@@ -283,11 +289,11 @@ __global__ void __launch_bounds__(max_warps(NT) * 32, 1) decode_int4_kernel(cons
         if (line < (int64_t)B * p.H * D * 2) prefetch_l2(reinterpret_cast<const char*>(p.q) + line);
     }
 
-    // ---- prefix[i] = Hkv * chunks of the sequences before i
+    // ---- prefix[i] = Hkv * (chunks and kPairCost) of the sequences before i that hold any
     {
         const int per = (B + threads - 1) / threads;
         const int beg = min(tid * per, B), end = min(beg + per, B);
-        int32_t local = 0;
+        int32_t local = 0, held = 0;   // cost; sequences that are not empty
 #pragma unroll 1
         for (int i = beg; i < end; ++i) {
             const int32_t raw = __ldg(p.context_lens + i);
@@ -295,15 +301,21 @@ __global__ void __launch_bounds__(max_warps(NT) * 32, 1) decode_int4_kernel(cons
                 if (raw < 0) pa::raise_error(p.err, PA_DEVERR_CONTEXT);
                 if (raw > max_len) pa::raise_error(p.err, PA_DEVERR_TABLE_WIDTH);
             }
-            local += (clamp_len(raw, max_len) + kChunk - 1) / kChunk;
+            const int32_t chunks = (clamp_len(raw, max_len) + kChunk - 1) / kChunk;
+            local += chunks ? chunks + kPairCost : 0;
+            held += chunks > 0;
         }
+        held = __reduce_add_sync(0xffffffffu, held);
         int32_t x = local;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const int32_t y = __shfl_up_sync(0xffffffffu, x, o);
             if (lane >= o) x += y;
         }
-        if (lane == 31) scan[warp] = x;
+        if (lane == 31) {
+            scan[warp] = x;
+            scan[nw + warp] = held;
+        }
         if (tid < 2 * nw) runs[tid].a = -1;
         __syncthreads();
         int32_t run = x - local;
@@ -312,13 +324,18 @@ __global__ void __launch_bounds__(max_warps(NT) * 32, 1) decode_int4_kernel(cons
 #pragma unroll 1
         for (int i = beg; i < end; ++i) {
             prefix[i] = run * Hkv;
-            run += (clamp_len(__ldg(p.context_lens + i), max_len) + kChunk - 1) / kChunk;
+            const int32_t chunks = (clamp_len(__ldg(p.context_lens + i), max_len) + kChunk - 1) / kChunk;
+            run += chunks ? chunks + kPairCost : 0;
         }
         if (tid == 0) {
-            int32_t total = 0;
+            int32_t total = 0, all = 0;
 #pragma unroll 1
-            for (int w = 0; w < nw; ++w) total += scan[w];
+            for (int w = 0; w < nw; ++w) {
+                total += scan[w];
+                all += scan[nw + w];
+            }
             prefix[B] = total * Hkv;
+            is_last[0] = (total - kPairCost * all) * Hkv;   // chunks
         }
         __syncthreads();
     }
@@ -332,12 +349,12 @@ __global__ void __launch_bounds__(max_warps(NT) * 32, 1) decode_int4_kernel(cons
         for (int v = tid; v < p.H * D / 8; v += threads) row[v] = make_uint4(0, 0, 0, 0);
     }
 
-    const int32_t W = prefix[B];
+    const int32_t W = is_last[0];
     // CTAs in use have a chunk per warp at least: smaller batches take fewer CTAs
     // rather than more partial results.
     const int32_t C = min((W + nw - 1) / nw, (int32_t)gridDim.x);
     if ((int32_t)blockIdx.x >= C) return;
-    const Cut cut(W, C);
+    const Cut cut(prefix[B], C);
     const int32_t cta_lo = cut.begin(blockIdx.x), cta_hi = cut.begin(blockIdx.x + 1);
     const Cut mine(cta_hi - cta_lo, nw);
     const int32_t lo = cta_lo + mine.begin(warp), hi = cta_lo + mine.begin(warp + 1);
@@ -346,7 +363,13 @@ __global__ void __launch_bounds__(max_warps(NT) * 32, 1) decode_int4_kernel(cons
     const uint32_t krows = sbase + L.rows + (uint32_t)warp * (2 * kChunk * NG * 8);
     const uint32_t vrows = krows + kChunk * NG * 8;
 
+    Cursor start{};
+    int32_t ipos = hi;              // next chunk to issue
     if (lo < hi) {
+        start = find(prefix, B, Hkv, lo);
+        ipos = start.a + kPairCost + start.c;
+    }
+    if (ipos < hi) {
         // ================= loading: this warp's chunks, in order =================
         // A copy instruction moves 512 bytes: kPass rows of codes.  The lane's row and
         // 16-byte column in a pass, and in the chunk's scales (K's by the lower lanes,
@@ -397,10 +420,8 @@ __global__ void __launch_bounds__(max_warps(NT) * 32, 1) decode_int4_kernel(cons
             w.sc = scales + (uint64_t)head * kSTile + (srow & bmask) * kSRow;
             return w;
         };
-        int32_t ipos = lo;              // next chunk to issue
         uint32_t ito = ring;            // its stage
-        Walk cur = open(find(prefix, B, Hkv, lo));
-        const Cursor start = cur.s;
+        Walk cur = open(start);
         // One chunk's copies, as one group.  Blocks past the context and ids outside the
         // pool are not read: zeros take their place (a step and a minimum of zero: rows of
         // zeros).
@@ -443,7 +464,7 @@ __global__ void __launch_bounds__(max_warps(NT) * 32, 1) decode_int4_kernel(cons
                     cur.wnext = entry(cur.s.i, cur.next, cur.nb);
                     cur.next += 32;
                 }
-            } else if (ipos < hi) {
+            } else if ((ipos += kPairCost) < hi) {
                 cur = open(next_pair(prefix, Hkv, cur.s));
             }
         };
@@ -525,7 +546,7 @@ __global__ void __launch_bounds__(max_warps(NT) * 32, 1) decode_int4_kernel(cons
         const uint32_t eights[2][4] = {{kEight, 0, kEight, 0}, {0, kEight, 0, kEight}};
         int segn = 0;
 #pragma unroll 1
-        for (int32_t pos = lo; pos < hi;) {
+        for (int32_t pos = ipos; pos < hi;) {
             // The first chunk is asked for while q is under way, the ring's others after it:
             // they would only delay it.
             fetch_q(s);
@@ -762,7 +783,7 @@ __global__ void __launch_bounds__(max_warps(NT) * 32, 1) decode_int4_kernel(cons
                 if (ipos < hi) issue();
                 commit_group();
             }
-            pos += c_end - c0;
+            pos += c_end - c0 + (c_end == s.nc ? kPairCost : 0);
 
             // ---- the pair's chunks of this warp are done
 #pragma unroll
@@ -935,7 +956,8 @@ __global__ void __launch_bounds__(max_warps(NT) * 32, 1) decode_int4_kernel(cons
     if (warp < n_open && lane == 0) {
         const Run& r = runs[open_lead(warp)];
         int32_t* ticket = p.counters + (int64_t)r.i * Hkv + r.g;
-        const int last = pa::atomic_add_acq_rel_gpu(ticket, 1) == cut.part(r.a + r.nc - 1) - cut.part(r.a);
+        const int last = pa::atomic_add_acq_rel_gpu(ticket, 1) ==
+                         cut.part(r.a + kPairCost + r.nc - 1) - cut.part(r.a + kPairCost);
         if (last) atomicExch(ticket, 0);   // ready for the next launch
         is_last[warp] = last;
     }
@@ -949,8 +971,9 @@ __global__ void __launch_bounds__(max_warps(NT) * 32, 1) decode_int4_kernel(cons
         const int w = both ? my_w : w0;
         if (!is_last[w]) continue;
         const Run r = runs[open_lead(w)];
-        const int c_first = cut.part(r.a), n = cut.part(r.a + r.nc - 1) - c_first + 1;
-        const float* first = p.partials + (2 * (int64_t)c_first + (cut.begin(c_first) == r.a ? 0 : 1)) * kPartial;
+        const int c_first = cut.part(r.a + kPairCost);
+        const int n = cut.part(r.a + kPairCost + r.nc - 1) - c_first + 1;
+        const float* first = p.partials + (2 * (int64_t)c_first + (cut.begin(c_first) >= r.a ? 0 : 1)) * kPartial;
         const float* rest = p.partials + 2 * (int64_t)c_first * kPartial;
         // A group of threads has the outputs, four each; the groups take the partials in
         // turn, eight loads in flight, and join through shared memory.
@@ -1116,9 +1139,9 @@ PA_API pa_status pa_decode_int4(const void* q, const void* k_cache, const void* 
     if ((int64_t)num_blocks * Hkv > INT32_MAX || B > kMaxBatch || (int64_t)num_blocks * block_size > INT32_MAX ||
         (int64_t)max_blocks * block_size > INT32_MAX)
         return PA_ERR_UNSUPPORTED;
-    // Flattened chunk indices are int32.
+    // Positions in the list are int32.
     const int64_t max_chunks = ((int64_t)max_blocks * block_size + kChunk - 1) / kChunk;
-    if ((int64_t)B * Hkv * subs * max_chunks >= ((int64_t)1 << 30)) return PA_ERR_UNSUPPORTED;
+    if ((int64_t)B * Hkv * subs * (max_chunks + kPairCost) >= ((int64_t)1 << 30)) return PA_ERR_UNSUPPORTED;
     if (B > 0 && ws_bytes < pa_decode_workspace_size(B, H, d)) return PA_ERR_INVALID;
     if (B == 0) return PA_OK;
     if (!q || !k_cache || !v_cache || !k_scale || !v_scale || !block_tables || !context_lens ||
