@@ -956,10 +956,13 @@ __global__ void __launch_bounds__(max_warps(NT) * 32, 1) decode_int4_kernel(cons
     if (warp < n_open && lane == 0) {
         const Run& r = runs[open_lead(warp)];
         int32_t* ticket = p.counters + (int64_t)r.i * Hkv + r.g;
-        const int last = pa::atomic_add_acq_rel_gpu(ticket, 1) ==
-                         cut.part(r.a + kPairCost + r.nc - 1) - cut.part(r.a + kPairCost);
+        const int32_t before_me = pa::atomic_add_acq_rel_gpu(ticket, 1);
+        const int32_t first = cut.part(r.a + kPairCost);
+        const int32_t n = cut.part(r.a + kPairCost + r.nc - 1) - first + 1;
+        const bool last = before_me == n - 1;
         if (last) atomicExch(ticket, 0);   // ready for the next launch
-        is_last[warp] = last;
+        is_last[warp] = last ? n : 0;      // the pair's CTAs
+        scan[warp] = first;
     }
     __syncthreads();
     // Two pairs to join: half the threads each, so that their loads are under way together.
@@ -971,13 +974,12 @@ __global__ void __launch_bounds__(max_warps(NT) * 32, 1) decode_int4_kernel(cons
         const int w = both ? my_w : w0;
         if (!is_last[w]) continue;
         const Run r = runs[open_lead(w)];
-        const int c_first = cut.part(r.a + kPairCost);
-        const int n = cut.part(r.a + kPairCost + r.nc - 1) - c_first + 1;
+        const int c_first = scan[w], n = is_last[w], most = both ? max(is_last[0], is_last[1]) : n;
         const float* first = p.partials + (2 * (int64_t)c_first + (cut.begin(c_first) >= r.a ? 0 : 1)) * kPartial;
         const float* rest = p.partials + 2 * (int64_t)c_first * kPartial;
-        // A group of threads has the outputs, four each; the groups take the partials in
-        // turn, eight loads in flight, and join through shared memory.
-        const int wide = min(outs, team), groups = team / wide;
+        // A group of threads has the outputs, four each, and eight partials' loads in flight;
+        // of more than eight the groups take turns, and join in shared memory.
+        const int wide = min(outs, team), groups = most > 8 ? team / wide : 1;
         const int grp = ltid / wide;
         float4* acc_at = reinterpret_cast<float4*>(smem) + my_w * team;   // [groups][outs]
         float2* ml_at = reinterpret_cast<float2*>(reinterpret_cast<float4*>(smem) + threads) + my_w * team;
