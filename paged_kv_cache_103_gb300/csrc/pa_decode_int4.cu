@@ -929,7 +929,7 @@ __global__ void __launch_bounds__(max_warps(NT) * 32, 1) decode_int4_kernel(cons
         const int k = runs[at].pad & 255;
         const int h = e / (D / 4), d4 = e % (D / 4) * 4;
         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 2
+#pragma unroll 4
         for (uint32_t set = runs[at].at; set; set &= set - 1) {
             const float* slot = slot_at(__ffs(set) - 1);
             const float f = slot[h];
