@@ -262,3 +262,22 @@ def test_seeded_random_shapes():
         got = run(q, cache, tbl, lens, d ** -0.5)
         assert binding.pa_check_device_errors() == 0, (G, Hkv, d, bs, lens)
         check(q, cache, tbl, lens, d ** -0.5, got)
+
+
+@pytest.mark.parametrize("H,Hkv,d,bs,dtype,lens", [
+    (16, 1, 128, 16, torch.bfloat16, [9000]),             # more outputs than threads, over 8 CTAs a pair
+    (16, 2, 64, 32, torch.float16, [12000, 40]),
+    (7, 1, 128, 32, torch.bfloat16, [20000]),
+    (4, 1, 64, 8, torch.float16, [30000, 1]),
+    (2, 2, 128, 16, torch.float16, [1] * 37 + [6000] + [33] * 50),      # short pairs around a long one
+    (12, 4, 128, 16, torch.bfloat16, [40] * 100 + [0] * 20 + [700] * 3),
+])
+def test_pairs_over_many_ctas_and_many_pairs_in_one(H, Hkv, d, bs, dtype, lens):
+    """Shares are cut by cost: a pair's chunks meet every number of CTAs and of joins at the end."""
+    tbl, N = rand_tables(lens, bs, 11)
+    cache = int4_cache(N, Hkv, bs, d, 12)
+    nan_behind(cache, lens, tbl, bs)
+    q = wl.normal_tensor((len(lens), H, d), dtype, 13)
+    got = run(q, cache, tbl, lens, d ** -0.5)
+    assert binding.pa_check_device_errors() == 0
+    check(q, cache, tbl, lens, d ** -0.5, got)
