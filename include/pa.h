@@ -539,7 +539,8 @@ PA_API pa_status pa_decode_int8(const void* q, const void* k_cache, const void* 
  * what pa_decode computes with the rows K_j, V_j that the codes stand for (s c + m
  * per group of 64 values), for d = 64 or 128.  Both products take fp32 sums; a
  * bf16 q is scaled by a power of two into f16 range first (exact for elements
- * down to 2^-25 of the KV head's largest).  A table entry outside the pool reads rows of
+ * down to 2^-25 of the KV head's largest), and a probability times its row's step is
+ * held to 16 bits (off by 2^-16 of itself at most) at any size.  A table entry outside the pool reads rows of
  * zeros and sets PA_DEVERR_BLOCK_ID.  Other arguments, the workspace
  * (pa_decode_workspace_size, here 16-byte aligned) and the errors are those of
  * pa_decode.

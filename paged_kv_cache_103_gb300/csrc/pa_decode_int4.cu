@@ -9,17 +9,25 @@
 // so the tensor cores multiply bare codes, K's step and minimum meet each score
 // once per key and group, V's step is folded into P, and the values of code 8 are one
 // number per (head, group).  The 8 that the codes are taken from is a product of its
-// own, P times a tile of eights, subtracted at the end: what P's rounding and the
-// tensor cores' truncating sums do to the codes' mean (2.5 times their spread, and 100
-// times the result of a long flat context) they do to the eights as well.  Without it
-// the error against 64 bits was 2.6 times an fp32 computation's, with it 1.1 to 1.6.
+// own, P times a tile of eights, subtracted at the end: what the tensor cores' truncating
+// sums do to the codes' mean (2.5 times their spread, and 100 times the result of a long
+// flat context) they do to the eights as well.
+//
+// P times V's step goes to the tensor cores as two bf16 numbers, its upper half and what
+// that leaves, rounded: 16 bits of it (off by 2^-16 of it at most) at every size that fp32
+// holds, whatever the steps of other tokens, groups and heads are.  (One f16 number under a
+// power of two for each warp, as it was, lost the codes of small steps beside a step 2^17
+// times theirs, and gave an f16 result 1.4 times an fp32 computation's error.)  Up to four
+// query heads the second part takes columns of the products that are free, above that
+// products of its own.  Against the single number 16 x 32768 tokens of 8 KV heads take 109.5
+// instead of 106 us with G = 4, 125 instead of 108 with G = 8, 195 instead of 159 with G = 16.
 //
 // A code needs no conversion.  As the low bits of an f16 whose other bits are zero
-// it is the subnormal c 2^-24 (c 2^-20 in the nibble above), exactly; tensor cores
-// take subnormals at full speed, and the powers of two leave through q (K's upper
-// nibbles) and the output (V's).  Eight codes become four f16 pairs with four ANDs
-// and a shift, against one conversion and more per pair for the 8-bit caches,
-// whose conversions bound those kernels.
+// it is the subnormal c 2^-24 (c 2^-20 in the nibble above), exactly, and as a bf16's a
+// byte of two codes is c 2^-133 + c' 2^-129; tensor cores take subnormals at full speed, and the
+// powers of two leave through q (K's upper nibbles) and the output (V's).  Eight codes
+// become four pairs with four ANDs and a shift, against one conversion and more per pair
+// for the 8-bit caches, whose conversions bound those kernels.
 //
 // What bounds it is HBM: 144 bytes a token and KV head at d = 128.  The decode of
 // the 16-bit cache keeps four math warps and two loading warps per CTA; at a third
@@ -77,9 +85,12 @@ struct Int4Params {
     float scale_log2;
 };
 
+// The forms of the kernel by query heads of a KV head: one; up to 4; up to 8; up to 16.
+enum Form { kG1, kG4, kG8, kG16 };
+constexpr Form form_of(int G) { return G == 1 ? kG1 : G <= 4 ? kG4 : G <= 8 ? kG8 : kG16; }
 // One CTA per SM.  Sixteen warps, or eight where 9 .. 16 heads need two 8-wide MMA
 // tiles and twice the accumulators.
-__host__ __device__ constexpr int max_warps(int NT) { return NT == 1 ? 16 : 8; }
+__host__ __device__ constexpr int max_warps(int form) { return form == kG16 ? 8 : 16; }
 constexpr uint32_t kSmemBudget = 227 * 1024;
 
 // One partial result in shared memory: row maxima [G], row sums [G], padding to 16 bytes,
@@ -250,17 +261,29 @@ __device__ __forceinline__ void store_row(uint32_t addr, const float (&v)[2 * NG
 
 constexpr uint32_t kLowNibbles = 0x000F000Fu;    // c 2^-24 each
 constexpr uint32_t kHighNibbles = 0x00F000F0u;   // c 2^-20 each
-constexpr uint32_t kBytes = 0x00FF00FFu;         // (c + 16 c') 2^-24 each
+constexpr uint32_t kBytes = 0x00FF00FFu;         // of a bf16: (c + 16 c') 2^-133 each
 
 // A head's running maximum is raised only when a logit exceeds it by more than this
-// (base 2): probabilities reach 2^8, which fp32 sums and the f16 range of P bear, and
-// most chunks need neither the maximum across lanes nor a rescale.
+// (base 2): probabilities reach 2^8, which fp32 sums bear, and most chunks need neither the
+// maximum across lanes nor a rescale.
 constexpr float kLazy = 8.f;
+// V's steps are held 2^64 times as large, so that what they and P are multiplied by, codes
+// 2^-133 times theirs, leaves normal numbers down to a P of 2^-33 at f16's smallest step, and
+// sums over any context stay far below fp32's largest.
+constexpr int kUp = 64;
 
-// kOne: one query head per KV head; a lane then tracks one column instead of two.
-template <int D, bool kBF16, int NT, bool kOne, int kShift>
-__global__ void __launch_bounds__(max_warps(NT) * 32, 1) decode_int4_kernel(const Int4Params p) {
-    constexpr int NG = D / 64, NJ = kOne ? 1 : 2;
+// A float's upper half as a float: a bf16 number, toward zero.
+__device__ __forceinline__ float upper_half(float x) {
+    return __uint_as_float(__float_as_uint(x) & 0xFFFF0000u);
+}
+
+// kG1: a lane tracks one column, head 0, instead of two; the next one is the second part of P.
+// kG4: columns h and h + 4 are both head h, the latter with the second part of P and the
+// former with minus the first.
+template <int D, bool kBF16, int kForm, int kShift>
+__global__ void __launch_bounds__(max_warps(kForm) * 32, 1) decode_int4_kernel(const Int4Params p) {
+    constexpr bool kOne = kForm == kG1, kDup = kForm == kG4;
+    constexpr int NG = D / 64, NT = kForm == kG16 ? 2 : 1, NJ = kOne ? 1 : 2;
     constexpr uint32_t kRow = D / 2, kSRow = NG * 4;         // bytes of a row's codes and scales
     constexpr uint32_t kCodes = kChunk * kRow, kScales = kChunk * kSRow;
     constexpr uint32_t kStage = 2 * (kCodes + kScales);   // K, V codes, K, V scales
@@ -482,7 +505,7 @@ __global__ void __launch_bounds__(max_warps(NT) * 32, 1) decode_int4_kernel(cons
         auto fetch_q = [&](const Cursor& s) {
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-                const int h = 8 * nt + cr;
+                const int h = kDup ? cr & 3 : 8 * nt + cr;
                 const uint4* row = reinterpret_cast<const uint4*>(
                     p.q + ((int64_t)s.i * p.H + s.g * G + h) * D + 16 * c4);
 #pragma unroll
@@ -544,6 +567,7 @@ __global__ void __launch_bounds__(max_warps(NT) * 32, 1) decode_int4_kernel(cons
         // accumulator has P's sums for both.
         constexpr uint32_t kEight = 0x00080008u;
         const uint32_t eights[2][4] = {{kEight, 0, kEight, 0}, {0, kEight, 0, kEight}};
+        const float dup = c4 < 2 ? 0.f : 1.f;   // kG4: which part of P this lane's columns have
         int segn = 0;
 #pragma unroll 1
         for (int32_t pos = ipos; pos < hi;) {
@@ -559,8 +583,8 @@ __global__ void __launch_bounds__(max_warps(NT) * 32, 1) decode_int4_kernel(cons
             if (segn) convert_q();
             const int32_t c0 = s.c, c_end = min(s.nc, s.c + hi - pos);
             const int32_t n = clamp_len(__ldg(p.context_lens + s.i), max_len);
-            // Running state for heads 8 nt + 2 c4 + {0, 1}: the negative of the
-            // maximum (bias; the logits below are relative to it), sum, sums of P times
+            // Running state for heads 8 nt + 2 c4 + {0, 1} (kG4: of that modulo 4): the negative
+            // of the maximum (bias; the logits below are relative to it), sum, sums of P times
             // V's minima; o: rows are values 64 g + 8 cr + u (e < 2) and + 4 + u.
             float bias[NT][NJ], l_run[NT][NJ], lowv[NT][NG][NJ], o[NG][4][NT][4], mid[NT][4];
 #pragma unroll
@@ -580,9 +604,6 @@ __global__ void __launch_bounds__(max_warps(NT) * 32, 1) decode_int4_kernel(cons
                 mid[nt][0] = mid[nt][1] = mid[nt][2] = mid[nt][3] = 0.f;
             }
             bool fresh = true;   // no maximum yet
-            // P times V's step is kept in f16 range by 2^vexp, which o carries.
-            int vexp = 126;
-            float vup = pa::exp2_int(126);
             int32_t valid = n - c0 * kChunk;   // tokens of the context from the chunk on
 #pragma unroll 1
             for (int32_t c = c0; c < c_end; ++c, valid -= kChunk) {
@@ -614,8 +635,7 @@ __global__ void __launch_bounds__(max_warps(NT) * 32, 1) decode_int4_kernel(cons
                             }
                         }
                     // ---- steps and minima: lane r takes row r of the chunk to fp32, K's
-                    // steps with the score's factor, V's with 2^vexp, for all lanes to read
-                    float rs = 1.f;   // what o is to be multiplied by
+                    // steps with the score's factor, for all lanes to read
                     {
                         float kv[2 * NG], vv[2 * NG];
                         load_f16_scales<NG>(st_at, kv);
@@ -623,22 +643,11 @@ __global__ void __launch_bounds__(max_warps(NT) * 32, 1) decode_int4_kernel(cons
                         if (lane >= valid)   // a row past the context may hold anything
 #pragma unroll
                             for (int g = 0; g < 2 * NG; ++g) vv[g] = 0.f;
-                        float vmax = vv[0];
-#pragma unroll
-                        for (int g = 1; g < NG; ++g) vmax = fmaxf(vmax, vv[2 * g]);
-                        // P <= 2^kLazy and steps below 2^7: their product stays below 2^15
-                        if (__any_sync(0xffffffffu, vmax * vup >= 128.f)) {
-                            vmax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(vmax)));
-                            const int e = 133 - pa::biased_exponent(vmax);   // < vexp
-                            rs = e - vexp >= -126 ? pa::exp2_int(e - vexp) : 0.f;
-                            vexp = e;
-                            vup = pa::exp2_int(e);
-                        }
 #pragma unroll
                         for (int g = 0; g < NG; ++g) {
                             kv[2 * g] *= qsc;
                             vv[2 * g + 1] += 8.f * vv[2 * g];   // the value of code 8
-                            vv[2 * g] *= vup;
+                            vv[2 * g] *= pa::exp2_int(kUp);
                         }
                         store_row<NG>(krows + lane * NG * 8, kv);
                         store_row<NG>(vrows + lane * NG * 8, vv);
@@ -676,7 +685,7 @@ __global__ void __launch_bounds__(max_warps(NT) * 32, 1) decode_int4_kernel(cons
                                         if (16 * mt + cr + 8 * r >= valid) x[mt][nt][r][j] = -INFINITY;
                     // ---- online softmax per head
                     float top[NT][NJ];
-                    bool above = fresh || rs != 1.f;
+                    bool above = fresh;
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -697,7 +706,7 @@ __global__ void __launch_bounds__(max_warps(NT) * 32, 1) decode_int4_kernel(cons
                                 v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
                                 v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
                                 const float up = fresh ? v : fmaxf(v, 0.f);
-                                const float a = fresh ? 0.f : pa::fast_exp2(-up), f = a * rs;
+                                const float a = fresh ? 0.f : pa::fast_exp2(-up);
                                 bias[nt][j] -= up;
 #pragma unroll
                                 for (int mt = 0; mt < kTiles; ++mt)
@@ -707,11 +716,14 @@ __global__ void __launch_bounds__(max_warps(NT) * 32, 1) decode_int4_kernel(cons
 #pragma unroll
                                 for (int g = 0; g < NG; ++g) {
                                     lowv[nt][g][j] *= a;
-                                    mid[nt][2 * g + j] *= f;
 #pragma unroll
-                                    for (int u = 0; u < 4; ++u) {
-                                        o[g][u][nt][j] *= f;
-                                        o[g][u][nt][2 + j] *= f;
+                                    for (int i = j; i <= (kOne ? 1 : j); ++i) {
+                                        mid[nt][2 * g + i] *= a;
+#pragma unroll
+                                        for (int u = 0; u < 4; ++u) {
+                                            o[g][u][nt][i] *= a;
+                                            o[g][u][nt][2 + i] *= a;
+                                        }
                                     }
                                 }
                             }
@@ -720,7 +732,7 @@ __global__ void __launch_bounds__(max_warps(NT) * 32, 1) decode_int4_kernel(cons
                     // ---- P, and O^T += V^T P^T
 #pragma unroll
                     for (int mt = 0; mt < kTiles; ++mt) {
-                        uint32_t pb[NG][NT][2];
+                        uint32_t pb[NG][NT][2], pl[NG][NT][2];   // the two parts of P times V's step
 #pragma unroll
                         for (int r = 0; r < 2; ++r) {
                             float vv[2 * NG];
@@ -735,9 +747,18 @@ __global__ void __launch_bounds__(max_warps(NT) * 32, 1) decode_int4_kernel(cons
                                 }
 #pragma unroll
                                 for (int g = 0; g < NG; ++g) {
-                                    // rounded to f16: P's only rounding
-                                    pb[g][nt][r] = pa::movmatrix_trans(
-                                        pa::pack2<false>(e[0] * vv[2 * g], e[1] * vv[2 * g]));
+                                    const float y0 = e[0] * vv[2 * g], y1 = e[1] * vv[2 * g];
+                                    const float h0 = upper_half(y0), h1 = upper_half(y1);
+                                    if constexpr (kOne) {
+                                        pb[g][nt][r] = pa::movmatrix_trans(pa::pack2<true>(h0, y0 - h0));
+                                    } else if constexpr (kDup) {
+                                        pb[g][nt][r] = pa::movmatrix_trans(
+                                            pa::pack2<true>(fmaf(dup, y0, -h0), fmaf(dup, y1, -h1)));
+                                    } else {
+                                        pb[g][nt][r] = pa::movmatrix_trans(__byte_perm(
+                                            __float_as_uint(y0), __float_as_uint(y1), 0x7632));
+                                        pl[g][nt][r] = pa::movmatrix_trans(pa::pack2<true>(y0 - h0, y1 - h1));
+                                    }
 #pragma unroll
                                     for (int j = 0; j < NJ; ++j) lowv[nt][g][j] += e[j] * vv[2 * g + 1];
                                 }
@@ -756,24 +777,34 @@ __global__ void __launch_bounds__(max_warps(NT) * 32, 1) decode_int4_kernel(cons
                                 z[r][0] = __byte_perm(w0, w1, perm0);
                                 z[r][1] = __byte_perm(w0, w1, perm1);
                             }
-#pragma unroll
-                            for (int nt = 0; nt < NT; ++nt)
-                                pa::mma_16816<false>(mid[nt], eights[g], pb[g][nt][0], pb[g][nt][1]);
+                            // One product behind, the second parts: no two in a row into one
+                            // accumulator.
+                            constexpr bool kTwo = !kOne && !kDup;
+                            uint32_t a[4], was[4];
 #pragma unroll
                             for (int u = 0; u < 4; ++u) {
                                 // u even: the byte's lower code; u odd: the whole byte, lower
                                 // code plus 16 times the upper one, which the end takes apart
                                 const uint32_t mask = u & 1 ? kBytes : kLowNibbles;
-                                uint32_t a[4];
 #pragma unroll
                                 for (int q = 0; q < 4; ++q) {
                                     const uint32_t w = z[q >> 1][q & 1];
+                                    was[q] = a[q];
                                     // bytes 1 and 3 to the low half of each half
                                     a[q] = (u < 2 ? w : __byte_perm(w, 0, 0x4341)) & mask;
                                 }
 #pragma unroll
-                                for (int nt = 0; nt < NT; ++nt)
-                                    pa::mma_16816<false>(o[g][u][nt], a, pb[g][nt][0], pb[g][nt][1]);
+                                for (int nt = 0; nt < NT; ++nt) {
+                                    pa::mma_16816<true>(o[g][u][nt], a, pb[g][nt][0], pb[g][nt][1]);
+                                    if (u == 0) pa::mma_16816<true>(mid[nt], eights[g], pb[g][nt][0], pb[g][nt][1]);
+                                }
+                                if constexpr (kTwo)
+#pragma unroll
+                                    for (int nt = 0; nt < NT; ++nt) {
+                                        if (u > 0) pa::mma_16816<true>(o[g][u - 1][nt], was, pl[g][nt][0], pl[g][nt][1]);
+                                        if (u == 3) pa::mma_16816<true>(mid[nt], eights[g], pl[g][nt][0], pl[g][nt][1]);
+                                        if (u == 3) pa::mma_16816<true>(o[g][u][nt], a, pl[g][nt][0], pl[g][nt][1]);
+                                    }
                             }
                         }
                     }
@@ -804,15 +835,16 @@ __global__ void __launch_bounds__(max_warps(NT) * 32, 1) decode_int4_kernel(cons
             const uint32_t at = segn == 0 ? L.slots + (uint32_t)warp * slot_floats(G, D) * 4
                                           : (uint32_t)warp * S * kStage;
             float* slot = reinterpret_cast<float*>(smem + at);
-            const float low = pa::exp2_int(min(24 - vexp, 127));
+            // Both parts of P in one lane; in kG4 the lanes with the second part have the others'.
+            auto both = [&](const float (&acc)[4], int i) { return kOne ? acc[i] + acc[i + 1] : acc[i]; };
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int j = 0; j < NJ; ++j) {
                     const int h = 8 * nt + 2 * c4 + j;
-                    if (h >= G) continue;
+                    if (!kDup && h >= G) continue;
                     const float inv = whole ? 1.f / l_run[nt][j] : 1.f;
-                    if (!whole && cr == 0) {
+                    if (!whole && cr == 0 && h < G) {
                         slot[h] = -bias[nt][j];
                         slot[G + h] = l_run[nt][j];
                     }
@@ -822,12 +854,18 @@ __global__ void __launch_bounds__(max_warps(NT) * 32, 1) decode_int4_kernel(cons
 #pragma unroll
                         for (int u = 0; u < 8; ++u) {
                             const int e = 2 * (u >> 2) + j;
-                            const float code = u & 1 ? (o[g][u & 3][nt][e] - o[g][(u & 3) - 1][nt][e]) * 0.0625f
-                                                     : o[g][u & 3][nt][e];
-                            const float sum = (code - mid[nt][2 * g + j]) * low;
-                            v[u] = (sum + lowv[nt][g][j]) * inv;
+                            const float even = both(o[g][u & 2][nt], e);
+                            const float code = u & 1 ? (both(o[g][u & 3][nt], e) - even) * 0.0625f : even;
+                            const float sum = (code - both(mid[nt], 2 * g + j)) * pa::exp2_int(133 - kUp);
+                            if constexpr (kDup) {
+                                const float part = c4 < 2 ? lowv[nt][g][j] - sum : sum;
+                                v[u] = (part + __shfl_xor_sync(0xffffffffu, part, 2)) * inv;
+                            } else {
+                                v[u] = (sum + lowv[nt][g][j]) * inv;
+                            }
                         }
                         const int at_d = 64 * g + 8 * cr;
+                        if (kDup && (h >= G || c4 >= 2)) continue;
                         if (whole) {
                             *reinterpret_cast<uint4*>(p.out + ((int64_t)s.i * p.H + s.g * G + h) * D + at_d) =
                                 make_uint4(pa::pack2<kBF16>(v[0], v[1]), pa::pack2<kBF16>(v[2], v[3]),
@@ -1065,14 +1103,14 @@ __global__ void __launch_bounds__(max_warps(NT) * 32, 1) decode_int4_kernel(cons
 
 // As many warps as shared memory holds rings and slots for; 0: not even four.
 int choose_warps(int D, int G, int B) {
-    for (int w = max_warps(G <= 8 ? 1 : 2); w >= 4; --w)
+    for (int w = max_warps(form_of(G)); w >= 4; --w)
         if (make_layout(D, G, B, w).total <= kSmemBudget) return w;
     return 0;
 }
 
-template <int D, bool kBF16, int NT, bool kOne, int kShift>
+template <int D, bool kBF16, int kForm, int kShift>
 pa_status launch(const Int4Params& p, cudaStream_t stream) {
-    auto kern = decode_int4_kernel<D, kBF16, NT, kOne, kShift>;
+    auto kern = decode_int4_kernel<D, kBF16, kForm, kShift>;
     // The shared-memory limit is set once per device.
     static std::atomic<uint64_t> done{0};
     int dev = 0;
@@ -1101,17 +1139,21 @@ pa_status launch(const Int4Params& p, cudaStream_t stream) {
     return pa::cuda_status(cudaLaunchKernelEx(&cfg, kern, p));
 }
 
-template <int D, bool kBF16, int NT, bool kOne>
+template <int D, bool kBF16, int kForm>
 pa_status launch_b(const Int4Params& p, cudaStream_t stream) {
-    if (p.bs_shift == 3) return launch<D, kBF16, NT, kOne, 3>(p, stream);
-    if (p.bs_shift == 4) return launch<D, kBF16, NT, kOne, 4>(p, stream);
-    return launch<D, kBF16, NT, kOne, 5>(p, stream);
+    if (p.bs_shift == 3) return launch<D, kBF16, kForm, 3>(p, stream);
+    if (p.bs_shift == 4) return launch<D, kBF16, kForm, 4>(p, stream);
+    return launch<D, kBF16, kForm, 5>(p, stream);
 }
 
 template <int D, bool kBF16>
 pa_status launch_g(const Int4Params& p, cudaStream_t stream) {
-    if (p.G == 1) return launch_b<D, kBF16, 1, true>(p, stream);
-    return p.G <= 8 ? launch_b<D, kBF16, 1, false>(p, stream) : launch_b<D, kBF16, 2, false>(p, stream);
+    switch (form_of(p.G)) {
+        case kG1: return launch_b<D, kBF16, kG1>(p, stream);
+        case kG4: return launch_b<D, kBF16, kG4>(p, stream);
+        case kG8: return launch_b<D, kBF16, kG8>(p, stream);
+        default: return launch_b<D, kBF16, kG16>(p, stream);
+    }
 }
 
 }  // namespace
