@@ -9,9 +9,12 @@
 // so the tensor cores multiply bare codes, K's step and minimum meet each score
 // once per key and group, V's step is folded into P, and the values of code 8 are one
 // number per (head, group).  The 8 that the codes are taken from is a product of its
-// own, P times a tile of eights, subtracted at the end: what the tensor cores' truncating
-// sums do to the codes' mean (2.5 times their spread, and 100 times the result of a long
-// flat context) they do to the eights as well.
+// own, P times a tile of eights, subtracted every eight chunks: what the tensor cores'
+// truncating sums do to the codes' mean (2.5 times their spread, and 100 times the result of
+// a long flat context) they do to the eights as well, and between two subtractions the sums
+// stay small.  (Subtracted once, at the end of a run, an f16 result of 32768 flat tokens was off
+// 1.6 times as far as an fp32 computation's, in 110 us for 16 contexts of 8 KV heads, G = 4;
+// so it is 1.002 times in 111, every four chunks 1.0005 in 111.5.)
 //
 // P times V's step goes to the tensor cores as two bf16 numbers, its upper half and what
 // that leaves, rounded: 16 bits of it (off by 2^-16 of it at most) at every size that fp32
@@ -20,7 +23,7 @@
 // times theirs, and gave an f16 result 1.4 times an fp32 computation's error.)  Up to four
 // query heads the second part takes columns of the products that are free, above that
 // products of its own.  Against the single number 16 x 32768 tokens of 8 KV heads take 109.5
-// instead of 106 us with G = 4, 125 instead of 108 with G = 8, 195 instead of 159 with G = 16.
+// instead of 106 us with G = 4, 125 instead of 108 with G = 8, 196 instead of 159 with G = 16.
 //
 // A code needs no conversion.  As the low bits of an f16 whose other bits are zero
 // it is the subnormal c 2^-24 (c 2^-20 in the nibble above), exactly, and as a bf16's a
@@ -267,6 +270,7 @@ constexpr uint32_t kBytes = 0x00FF00FFu;         // of a bf16: (c + 16 c') 2^-13
 // (base 2): probabilities reach 2^8, which fp32 sums bear, and most chunks need neither the
 // maximum across lanes nor a rescale.
 constexpr float kLazy = 8.f;
+constexpr int kSettle = 8;   // chunks between two subtractions of the codes' middle
 // V's steps are held 2^64 times as large, so that what they and P are multiplied by, codes
 // 2^-133 times theirs, leaves normal numbers down to a P of 2^-33 at f16's smallest step, and
 // sums over any context stay far below fp32's largest.
@@ -606,213 +610,231 @@ __global__ void __launch_bounds__(max_warps(kForm) * 32, 1) decode_int4_kernel(c
             bool fresh = true;   // no maximum yet
             int32_t valid = n - c0 * kChunk;   // tokens of the context from the chunk on
 #pragma unroll 1
-            for (int32_t c = c0; c < c_end; ++c, valid -= kChunk) {
-                wait_group<S - 1>();
-                __syncwarp();   // every lane's copies have landed
-                {
-                    const uint32_t kt = stage + koff, vt0 = stage + voff0, vt1 = stage + voff1;
-                    const uint32_t st_at = stage + 2 * kCodes + lane * kSRow;
-                    // ---- S^T = K Q^T over the codes, per group
-                    float st[kTiles][NG][NT][4];
-#pragma unroll
-                    for (int mt = 0; mt < kTiles; ++mt)
-#pragma unroll
-                        for (int g = 0; g < NG; ++g) {
-#pragma unroll
-                            for (int nt = 0; nt < NT; ++nt)
-                                st[mt][g][nt][0] = st[mt][g][nt][1] = st[mt][g][nt][2] = st[mt][g][nt][3] = 0.f;
-                            const uint2 w0 = pa::lds64(kt + 16 * mt * kRow + 32 * g);
-                            const uint2 w1 = pa::lds64(kt + (16 * mt + 8) * kRow + 32 * g);
-#pragma unroll
-                            for (int ks = 0; ks < 4; ++ks) {
-                                const uint32_t y0 = (ks < 2 ? w0.x : w0.y) >> (8 * (ks & 1));
-                                const uint32_t y1 = (ks < 2 ? w1.x : w1.y) >> (8 * (ks & 1));
-                                const uint32_t a[4] = {y0 & kLowNibbles, y1 & kLowNibbles,
-                                                       y0 & kHighNibbles, y1 & kHighNibbles};
-#pragma unroll
-                                for (int nt = 0; nt < NT; ++nt)
-                                    pa::mma_16816<false>(st[mt][g][nt], a, qb[nt][g][ks][0], qb[nt][g][ks][1]);
-                            }
-                        }
-                    // ---- steps and minima: lane r takes row r of the chunk to fp32, K's
-                    // steps with the score's factor, for all lanes to read
+            for (int32_t c = c0; c < c_end;) {
+                const int32_t stop = min(c + kSettle, c_end);
+#pragma unroll 1
+                for (; c < stop; ++c, valid -= kChunk) {
+                    wait_group<S - 1>();
+                    __syncwarp();   // every lane's copies have landed
                     {
-                        float kv[2 * NG], vv[2 * NG];
-                        load_f16_scales<NG>(st_at, kv);
-                        load_f16_scales<NG>(st_at + kScales, vv);
-                        if (lane >= valid)   // a row past the context may hold anything
-#pragma unroll
-                            for (int g = 0; g < 2 * NG; ++g) vv[g] = 0.f;
-#pragma unroll
-                        for (int g = 0; g < NG; ++g) {
-                            kv[2 * g] *= qsc;
-                            vv[2 * g + 1] += 8.f * vv[2 * g];   // the value of code 8
-                            vv[2 * g] *= pa::exp2_int(kUp);
-                        }
-                        store_row<NG>(krows + lane * NG * 8, kv);
-                        store_row<NG>(vrows + lane * NG * 8, vv);
-                    }
-                    __syncwarp();
-                    // ---- base-2 logits, relative to the running maxima
-                    float x[kTiles][NT][2][NJ];   // [key half][head]
-#pragma unroll
-                    for (int mt = 0; mt < kTiles; ++mt)
-#pragma unroll
-                        for (int r = 0; r < 2; ++r) {
-                            float kv[2 * NG];
-                            load_row<NG>(krow + (16 * mt + 8 * r) * NG * 8, kv);
-#pragma unroll
-                            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                                for (int j = 0; j < NJ; ++j) {
-                                    float v = bias[nt][j];
-#pragma unroll
-                                    for (int g = 0; g < NG; ++g) v += kv[2 * g + 1] * qsum[nt][g][j];
-#pragma unroll
-                                    for (int g = 0; g < NG; ++g) v += kv[2 * g] * st[mt][g][nt][2 * r + j];
-                                    x[mt][nt][r][j] = v;
-                                }
-                        }
-                    if (valid < kChunk)   // the context's last chunk
+                        const uint32_t kt = stage + koff, vt0 = stage + voff0, vt1 = stage + voff1;
+                        const uint32_t st_at = stage + 2 * kCodes + lane * kSRow;
+                        // ---- S^T = K Q^T over the codes, per group
+                        float st[kTiles][NG][NT][4];
 #pragma unroll
                         for (int mt = 0; mt < kTiles; ++mt)
 #pragma unroll
-                            for (int r = 0; r < 2; ++r)
+                            for (int g = 0; g < NG; ++g) {
+#pragma unroll
+                                for (int nt = 0; nt < NT; ++nt)
+                                    st[mt][g][nt][0] = st[mt][g][nt][1] = st[mt][g][nt][2] = st[mt][g][nt][3] = 0.f;
+                                const uint2 w0 = pa::lds64(kt + 16 * mt * kRow + 32 * g);
+                                const uint2 w1 = pa::lds64(kt + (16 * mt + 8) * kRow + 32 * g);
+#pragma unroll
+                                for (int ks = 0; ks < 4; ++ks) {
+                                    const uint32_t y0 = (ks < 2 ? w0.x : w0.y) >> (8 * (ks & 1));
+                                    const uint32_t y1 = (ks < 2 ? w1.x : w1.y) >> (8 * (ks & 1));
+                                    const uint32_t a[4] = {y0 & kLowNibbles, y1 & kLowNibbles,
+                                                           y0 & kHighNibbles, y1 & kHighNibbles};
+#pragma unroll
+                                    for (int nt = 0; nt < NT; ++nt)
+                                        pa::mma_16816<false>(st[mt][g][nt], a, qb[nt][g][ks][0], qb[nt][g][ks][1]);
+                                }
+                            }
+                        // ---- steps and minima: lane r takes row r of the chunk to fp32, K's
+                        // steps with the score's factor, for all lanes to read
+                        {
+                            float kv[2 * NG], vv[2 * NG];
+                            load_f16_scales<NG>(st_at, kv);
+                            load_f16_scales<NG>(st_at + kScales, vv);
+                            if (lane >= valid)   // a row past the context may hold anything
+#pragma unroll
+                                for (int g = 0; g < 2 * NG; ++g) vv[g] = 0.f;
+#pragma unroll
+                            for (int g = 0; g < NG; ++g) {
+                                kv[2 * g] *= qsc;
+                                vv[2 * g + 1] += 8.f * vv[2 * g];   // the value of code 8
+                                vv[2 * g] *= pa::exp2_int(kUp);
+                            }
+                            store_row<NG>(krows + lane * NG * 8, kv);
+                            store_row<NG>(vrows + lane * NG * 8, vv);
+                        }
+                        __syncwarp();
+                        // ---- base-2 logits, relative to the running maxima
+                        float x[kTiles][NT][2][NJ];   // [key half][head]
+#pragma unroll
+                        for (int mt = 0; mt < kTiles; ++mt)
+#pragma unroll
+                            for (int r = 0; r < 2; ++r) {
+                                float kv[2 * NG];
+                                load_row<NG>(krow + (16 * mt + 8 * r) * NG * 8, kv);
 #pragma unroll
                                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                                    for (int j = 0; j < NJ; ++j)
-                                        if (16 * mt + cr + 8 * r >= valid) x[mt][nt][r][j] = -INFINITY;
-                    // ---- online softmax per head
-                    float top[NT][NJ];
-                    bool above = fresh;
+                                    for (int j = 0; j < NJ; ++j) {
+                                        float v = bias[nt][j];
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
+                                        for (int g = 0; g < NG; ++g) v += kv[2 * g + 1] * qsum[nt][g][j];
 #pragma unroll
-                        for (int j = 0; j < NJ; ++j) {
-                            top[nt][j] = x[0][nt][0][j];
+                                        for (int g = 0; g < NG; ++g) v += kv[2 * g] * st[mt][g][nt][2 * r + j];
+                                        x[mt][nt][r][j] = v;
+                                    }
+                            }
+                        if (valid < kChunk)   // the context's last chunk
 #pragma unroll
                             for (int mt = 0; mt < kTiles; ++mt)
-                                top[nt][j] = fmaxf(top[nt][j], fmaxf(x[mt][nt][0][j], x[mt][nt][1][j]));
-                            above |= top[nt][j] > kLazy;
-                        }
-                    if (__any_sync(0xffffffffu, above)) {
+#pragma unroll
+                                for (int r = 0; r < 2; ++r)
+#pragma unroll
+                                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                                        for (int j = 0; j < NJ; ++j)
+                                            if (16 * mt + cr + 8 * r >= valid) x[mt][nt][r][j] = -INFINITY;
+                        // ---- online softmax per head
+                        float top[NT][NJ];
+                        bool above = fresh;
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                             for (int j = 0; j < NJ; ++j) {
-                                float v = top[nt][j];
-                                v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
-                                v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
-                                v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
-                                const float up = fresh ? v : fmaxf(v, 0.f);
-                                const float a = fresh ? 0.f : pa::fast_exp2(-up);
-                                bias[nt][j] -= up;
+                                top[nt][j] = x[0][nt][0][j];
 #pragma unroll
                                 for (int mt = 0; mt < kTiles; ++mt)
+                                    top[nt][j] = fmaxf(top[nt][j], fmaxf(x[mt][nt][0][j], x[mt][nt][1][j]));
+                                above |= top[nt][j] > kLazy;
+                            }
+                        if (__any_sync(0xffffffffu, above)) {
 #pragma unroll
-                                    for (int r = 0; r < 2; ++r) x[mt][nt][r][j] -= up;
-                                l_run[nt][j] *= a;
+                            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                                for (int g = 0; g < NG; ++g) {
-                                    lowv[nt][g][j] *= a;
+                                for (int j = 0; j < NJ; ++j) {
+                                    float v = top[nt][j];
+                                    v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
+                                    v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
+                                    v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
+                                    const float up = fresh ? v : fmaxf(v, 0.f);
+                                    const float a = fresh ? 0.f : pa::fast_exp2(-up);
+                                    bias[nt][j] -= up;
 #pragma unroll
-                                    for (int i = j; i <= (kOne ? 1 : j); ++i) {
-                                        mid[nt][2 * g + i] *= a;
+                                    for (int mt = 0; mt < kTiles; ++mt)
 #pragma unroll
-                                        for (int u = 0; u < 4; ++u) {
-                                            o[g][u][nt][i] *= a;
-                                            o[g][u][nt][2 + i] *= a;
+                                        for (int r = 0; r < 2; ++r) x[mt][nt][r][j] -= up;
+                                    l_run[nt][j] *= a;
+#pragma unroll
+                                    for (int g = 0; g < NG; ++g) {
+                                        lowv[nt][g][j] *= a;
+#pragma unroll
+                                        for (int i = j; i <= (kOne ? 1 : j); ++i) {
+                                            mid[nt][2 * g + i] *= a;
+#pragma unroll
+                                            for (int u = 0; u < 4; ++u) {
+                                                o[g][u][nt][i] *= a;
+                                                o[g][u][nt][2 + i] *= a;
+                                            }
                                         }
                                     }
                                 }
-                            }
-                    }
-                    fresh = false;
-                    // ---- P, and O^T += V^T P^T
-#pragma unroll
-                    for (int mt = 0; mt < kTiles; ++mt) {
-                        uint32_t pb[NG][NT][2], pl[NG][NT][2];   // the two parts of P times V's step
-#pragma unroll
-                        for (int r = 0; r < 2; ++r) {
-                            float vv[2 * NG];
-                            load_row<NG>(vrow + (16 * mt + 8 * r) * NG * 8, vv);
-#pragma unroll
-                            for (int nt = 0; nt < NT; ++nt) {
-                                float e[2] = {0.f, 0.f};
-#pragma unroll
-                                for (int j = 0; j < NJ; ++j) {
-                                    e[j] = pa::fast_exp2(x[mt][nt][r][j]);
-                                    l_run[nt][j] += e[j];
-                                }
-#pragma unroll
-                                for (int g = 0; g < NG; ++g) {
-                                    const float y0 = e[0] * vv[2 * g], y1 = e[1] * vv[2 * g];
-                                    const float h0 = upper_half(y0), h1 = upper_half(y1);
-                                    if constexpr (kOne) {
-                                        pb[g][nt][r] = pa::movmatrix_trans(pa::pack2<true>(h0, y0 - h0));
-                                    } else if constexpr (kDup) {
-                                        pb[g][nt][r] = pa::movmatrix_trans(
-                                            pa::pack2<true>(fmaf(dup, y0, -h0), fmaf(dup, y1, -h1)));
-                                    } else {
-                                        pb[g][nt][r] = pa::movmatrix_trans(__byte_perm(
-                                            __float_as_uint(y0), __float_as_uint(y1), 0x7632));
-                                        pl[g][nt][r] = pa::movmatrix_trans(pa::pack2<true>(y0 - h0, y1 - h1));
-                                    }
-#pragma unroll
-                                    for (int j = 0; j < NJ; ++j) lowv[nt][g][j] += e[j] * vv[2 * g + 1];
-                                }
-                            }
                         }
-                        // The fragment's key pairs: 16 mt + 8 r + 2 c4 + {0, 1}; odd c4 read
-                        // the pair's second row first, so that the four rows of a load lie in
-                        // both halves of the 128 bytes, and swap in the byte permutation.
+                        fresh = false;
+                        // ---- P, and O^T += V^T P^T
 #pragma unroll
-                        for (int g = 0; g < NG; ++g) {
-                            uint32_t z[2][2];   // [key half][values 0..3 | 4..7]
+                        for (int mt = 0; mt < kTiles; ++mt) {
+                            uint32_t pb[NG][NT][2], pl[NG][NT][2];   // the two parts of P times V's step
 #pragma unroll
                             for (int r = 0; r < 2; ++r) {
-                                const uint32_t w0 = lds32(vt0 + (16 * mt + 8 * r) * kRow + 32 * g);
-                                const uint32_t w1 = lds32(vt1 + (16 * mt + 8 * r) * kRow + 32 * g);
-                                z[r][0] = __byte_perm(w0, w1, perm0);
-                                z[r][1] = __byte_perm(w0, w1, perm1);
-                            }
-                            // One product behind, the second parts: no two in a row into one
-                            // accumulator.
-                            constexpr bool kTwo = !kOne && !kDup;
-                            uint32_t a[4], was[4];
-#pragma unroll
-                            for (int u = 0; u < 4; ++u) {
-                                // u even: the byte's lower code; u odd: the whole byte, lower
-                                // code plus 16 times the upper one, which the end takes apart
-                                const uint32_t mask = u & 1 ? kBytes : kLowNibbles;
-#pragma unroll
-                                for (int q = 0; q < 4; ++q) {
-                                    const uint32_t w = z[q >> 1][q & 1];
-                                    was[q] = a[q];
-                                    // bytes 1 and 3 to the low half of each half
-                                    a[q] = (u < 2 ? w : __byte_perm(w, 0, 0x4341)) & mask;
-                                }
+                                float vv[2 * NG];
+                                load_row<NG>(vrow + (16 * mt + 8 * r) * NG * 8, vv);
 #pragma unroll
                                 for (int nt = 0; nt < NT; ++nt) {
-                                    pa::mma_16816<true>(o[g][u][nt], a, pb[g][nt][0], pb[g][nt][1]);
-                                    if (u == 0) pa::mma_16816<true>(mid[nt], eights[g], pb[g][nt][0], pb[g][nt][1]);
+                                    float e[2] = {0.f, 0.f};
+#pragma unroll
+                                    for (int j = 0; j < NJ; ++j) {
+                                        e[j] = pa::fast_exp2(x[mt][nt][r][j]);
+                                        l_run[nt][j] += e[j];
+                                    }
+#pragma unroll
+                                    for (int g = 0; g < NG; ++g) {
+                                        const float y0 = e[0] * vv[2 * g], y1 = e[1] * vv[2 * g];
+                                        const float h0 = upper_half(y0), h1 = upper_half(y1);
+                                        if constexpr (kOne) {
+                                            pb[g][nt][r] = pa::movmatrix_trans(pa::pack2<true>(h0, y0 - h0));
+                                        } else if constexpr (kDup) {
+                                            pb[g][nt][r] = pa::movmatrix_trans(
+                                                pa::pack2<true>(fmaf(dup, y0, -h0), fmaf(dup, y1, -h1)));
+                                        } else {
+                                            pb[g][nt][r] = pa::movmatrix_trans(__byte_perm(
+                                                __float_as_uint(y0), __float_as_uint(y1), 0x7632));
+                                            pl[g][nt][r] = pa::movmatrix_trans(pa::pack2<true>(y0 - h0, y1 - h1));
+                                        }
+#pragma unroll
+                                        for (int j = 0; j < NJ; ++j) lowv[nt][g][j] += e[j] * vv[2 * g + 1];
+                                    }
                                 }
-                                if constexpr (kTwo)
+                            }
+                            // The fragment's key pairs: 16 mt + 8 r + 2 c4 + {0, 1}; odd c4 read
+                            // the pair's second row first, so that the four rows of a load lie in
+                            // both halves of the 128 bytes, and swap in the byte permutation.
+#pragma unroll
+                            for (int g = 0; g < NG; ++g) {
+                                uint32_t z[2][2];   // [key half][values 0..3 | 4..7]
+#pragma unroll
+                                for (int r = 0; r < 2; ++r) {
+                                    const uint32_t w0 = lds32(vt0 + (16 * mt + 8 * r) * kRow + 32 * g);
+                                    const uint32_t w1 = lds32(vt1 + (16 * mt + 8 * r) * kRow + 32 * g);
+                                    z[r][0] = __byte_perm(w0, w1, perm0);
+                                    z[r][1] = __byte_perm(w0, w1, perm1);
+                                }
+                                // One product behind, the second parts: no two in a row into one
+                                // accumulator.
+                                constexpr bool kTwo = !kOne && !kDup;
+                                uint32_t a[4], was[4];
+#pragma unroll
+                                for (int u = 0; u < 4; ++u) {
+                                    // u even: the byte's lower code; u odd: the whole byte, lower
+                                    // code plus 16 times the upper one, which the end takes apart
+                                    const uint32_t mask = u & 1 ? kBytes : kLowNibbles;
+#pragma unroll
+                                    for (int q = 0; q < 4; ++q) {
+                                        const uint32_t w = z[q >> 1][q & 1];
+                                        was[q] = a[q];
+                                        // bytes 1 and 3 to the low half of each half
+                                        a[q] = (u < 2 ? w : __byte_perm(w, 0, 0x4341)) & mask;
+                                    }
 #pragma unroll
                                     for (int nt = 0; nt < NT; ++nt) {
-                                        if (u > 0) pa::mma_16816<true>(o[g][u - 1][nt], was, pl[g][nt][0], pl[g][nt][1]);
-                                        if (u == 3) pa::mma_16816<true>(mid[nt], eights[g], pl[g][nt][0], pl[g][nt][1]);
-                                        if (u == 3) pa::mma_16816<true>(o[g][u][nt], a, pl[g][nt][0], pl[g][nt][1]);
+                                        pa::mma_16816<true>(o[g][u][nt], a, pb[g][nt][0], pb[g][nt][1]);
+                                        if (u == 0) pa::mma_16816<true>(mid[nt], eights[g], pb[g][nt][0], pb[g][nt][1]);
                                     }
+                                    if constexpr (kTwo)
+#pragma unroll
+                                        for (int nt = 0; nt < NT; ++nt) {
+                                            if (u > 0) pa::mma_16816<true>(o[g][u - 1][nt], was, pl[g][nt][0], pl[g][nt][1]);
+                                            if (u == 3) pa::mma_16816<true>(mid[nt], eights[g], pl[g][nt][0], pl[g][nt][1]);
+                                            if (u == 3) pa::mma_16816<true>(o[g][u][nt], a, pl[g][nt][0], pl[g][nt][1]);
+                                        }
+                                }
                             }
                         }
                     }
+                    __syncwarp();   // every lane has read the stage: it may be filled again
+                    stage = stage + kStage == ring + S * kStage ? ring : stage + kStage;
+                    if (ipos < hi) issue();
+                    commit_group();
                 }
-                __syncwarp();   // every lane has read the stage: it may be filled again
-                stage = stage + kStage == ring + S * kStage ? ring : stage + kStage;
-                if (ipos < hi) issue();
-                commit_group();
+                // The codes' middle leaves o, while it is small.
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int g = 0; g < NG; ++g)
+#pragma unroll
+                        for (int j = 0; j < (kOne ? 2 : NJ); ++j) {
+#pragma unroll
+                            for (int u = 0; u < 4; ++u)
+#pragma unroll
+                                for (int e = j; e < 4; e += 2)
+                                    o[g][u][nt][e] -= (u & 1 ? 17.f : 1.f) * mid[nt][2 * g + j];
+                            mid[nt][2 * g + j] = 0.f;
+                        }
             }
             pos += c_end - c0 + (c_end == s.nc ? kPairCost : 0);
 
@@ -856,7 +878,7 @@ __global__ void __launch_bounds__(max_warps(kForm) * 32, 1) decode_int4_kernel(c
                             const int e = 2 * (u >> 2) + j;
                             const float even = both(o[g][u & 2][nt], e);
                             const float code = u & 1 ? (both(o[g][u & 3][nt], e) - even) * 0.0625f : even;
-                            const float sum = (code - both(mid[nt], 2 * g + j)) * pa::exp2_int(133 - kUp);
+                            const float sum = code * pa::exp2_int(133 - kUp);
                             if constexpr (kDup) {
                                 const float part = c4 < 2 ? lowv[nt][g][j] - sum : sum;
                                 v[u] = (part + __shfl_xor_sync(0xffffffffu, part, 2)) * inv;

@@ -63,9 +63,11 @@ def group_bound(q, cache, tbl, n, scale, dtype, ref):
       ln 2, both in w and in the sum that divides), exp2 (2^-22) and three fp32 products: below
       2^-19 + 2^-20 |x|;
     * the sums over the keys, on the tensor cores (16 keys at a time, the two parts one after the
-      other, each sum cut off 2^-23 of the largest partial sum at worst, for P's codes and for the
-      eights): n / 4 of them; the minima in fp32, each lane every eighth key, n / 8 roundings of
-      2^-24; the joins, 64 of 2^-24: (n / 4 + n / 16 + 32) 2^-23 of sum_j w_j a_j.
+      other, each sum cut off 2^-23 of the largest partial sum at worst, which the weight of the
+      eight chunks between two subtractions of the codes' middle bounds): 32 of them for P's
+      codes and 32 for the eights, and one rounding of what is left per subtraction; the
+      minima in fp32, each lane every eighth key, n / 8 roundings of 2^-24; the joins, 64 of 2^-24:
+      (64 + 32 + n / 16) 2^-23 of sum_j w_j a_j.
     """
     kc, vc, ks, vs = cache
     _, H, d = q.shape
@@ -84,7 +86,7 @@ def group_bound(q, cache, tbl, n, scale, dtype, ref):
         w = np.exp(x - x.max())
         w /= w.sum()
         size = np.abs(x / np.log(2)).max()
-        rel = 2.0 ** -19 + 2.0 ** -20 * size + (n / 4 + n / 16 + 32) * 2.0 ** -23
+        rel = 2.0 ** -19 + 2.0 ** -20 * size + (96 + n / 16) * 2.0 ** -23
         bound[0, h] += 2.0 ** -16 * (w @ off) + rel * (w @ amp)
     return bound
 
@@ -161,13 +163,18 @@ def rms(x):
 
 
 @pytest.mark.parametrize("H,Hkv,d", [(1, 1, 128), (3, 1, 128), (7, 1, 64), (8, 1, 128), (13, 1, 128)])
-@pytest.mark.parametrize("n,B,limit", [(60, 40, 1.05)])
+@pytest.mark.parametrize("n,B,limit", [(60, 40, 1.05), (32769, 2500, 1.25)])
 def test_an_f16_result_is_off_by_little_but_its_own_rounding(n, B, limit, H, Hkv, d):
-    """Weights that f16 does not hold; root mean squares, r that of
+    """Weights that f16 does not hold, and runs of 1000 chunks a warp.  Root mean squares, r that of
     the output's rounding (known from the reference; some 2^-12.3 of the result):
     * short contexts: with x = sum_j (w_j s_j (c_j - 8))^2 the result is of size sqrt(x), and P's
       second part is off by 2^-17.8 of each product, together 2^-17.8 sqrt(x): r / 45, and the
       fp32 steps less: 5% is ample;
+    * long ones: with a = sum_j w_j 8 s_j, the result is some a / 300 and r 2^-20.5 a; of the 32 sums
+      between two subtractions, of the codes and of the eights, each cuts half a unit of 2^-23 on
+      average, alike but where one of the two lies beyond a power of two: (1/2) 32 / 2 of 2^-24 a
+      = 2^-21 a where it does, and its deviation, 2^-23 a, averages out over the subtractions:
+      at most sqrt(1 + (3/4)^2) = 1.25 r.
     """
     rng = np.random.default_rng(n + H)
     logits = -rng.integers(0, 24, (n, 1)) / 32 if n < 100 else np.zeros((n, 1))
