@@ -216,11 +216,10 @@ __device__ __forceinline__ uint4 dequantise8(uint2 codes, uint32_t sm) {
 // Piece v is values 8 v .. 8 v + 7 of k_out and of v_out.
 template <bool kBF16, Format F, int D, int kUnroll>
 __global__ void __launch_bounds__(kThreads)
-gather_cache_kernel(const void* __restrict__ k_cache, const void* __restrict__ v_cache,
-                    const uint32_t* __restrict__ k_scale, const uint32_t* __restrict__ v_scale,
-                    const int64_t* __restrict__ slot_mapping, uint32_t vecs, FastDiv by_heads,
-                    uint32_t Hkv, int bs_shift, int64_t num_slots, uint4* __restrict__ k_out,
-                    uint4* __restrict__ v_out, unsigned int* __restrict__ err) {
+gather_cache_kernel(const void* k_cache, const void* v_cache, const uint32_t* k_scale,
+                    const uint32_t* v_scale, const int64_t* slot_mapping, uint32_t vecs, FastDiv by_heads,
+                    uint32_t Hkv, int bs_shift, int64_t num_slots, uint4* k_out, uint4* v_out,
+                    unsigned int* err) {
     constexpr uint32_t kRow = D / kVec;
     asm volatile("griddepcontrol.wait;" ::: "memory");   // launched while an append may run
     int64_t slot[kUnroll];
@@ -231,7 +230,7 @@ gather_cache_kernel(const void* __restrict__ k_cache, const void* __restrict__ v
     for (int u = 0; u < kUnroll; ++u) {
         const uint32_t v = piece<kUnroll>(u), row = v / kRow, t = by_heads(row);
         h[u] = row - t * Hkv;
-        slot[u] = v < vecs ? __ldg(slot_mapping + t) : -1;
+        slot[u] = v < vecs ? pa::ld_behind_wait(slot_mapping + t) : -1;
     }
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
@@ -246,16 +245,16 @@ gather_cache_kernel(const void* __restrict__ k_cache, const void* __restrict__ v
         const int64_t at = ((((slot[u] >> bs_shift) * Hkv) + h[u]) << bs_shift) +
                            (slot[u] & ((1 << bs_shift) - 1));
         if constexpr (F == kInt4) {
-            kc[u] = make_uint2(__ldg(static_cast<const uint32_t*>(k_cache) + at * kRow + l), 0);
-            vc[u] = make_uint2(__ldg(static_cast<const uint32_t*>(v_cache) + at * kRow + l), 0);
-            ks[u] = __ldg(k_scale + at * (D / 64) + l / kGroupLanes);
-            vs[u] = __ldg(v_scale + at * (D / 64) + l / kGroupLanes);
+            kc[u] = make_uint2(pa::ld_behind_wait(static_cast<const uint32_t*>(k_cache) + at * kRow + l), 0);
+            vc[u] = make_uint2(pa::ld_behind_wait(static_cast<const uint32_t*>(v_cache) + at * kRow + l), 0);
+            ks[u] = pa::ld_behind_wait(k_scale + at * (D / 64) + l / kGroupLanes);
+            vs[u] = pa::ld_behind_wait(v_scale + at * (D / 64) + l / kGroupLanes);
         } else {
             const int64_t c = (slot[u] * Hkv + h[u]) * kRow + l;
-            kc[u] = __ldg(static_cast<const uint2*>(k_cache) + c);
-            vc[u] = __ldg(static_cast<const uint2*>(v_cache) + c);
-            ks[u] = __ldg(k_scale + at);
-            vs[u] = __ldg(v_scale + at);
+            kc[u] = pa::ld_behind_wait(static_cast<const uint2*>(k_cache) + c);
+            vc[u] = pa::ld_behind_wait(static_cast<const uint2*>(v_cache) + c);
+            ks[u] = pa::ld_behind_wait(k_scale + at);
+            vs[u] = pa::ld_behind_wait(v_scale + at);
         }
     }
 #pragma unroll

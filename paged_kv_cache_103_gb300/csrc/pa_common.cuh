@@ -24,6 +24,15 @@ __device__ __forceinline__ void raise_error(unsigned int* word, unsigned int bit
     atomicOr(word, bits);
 }
 
+// A read for a kernel that was launched while the one before it ran, behind its
+// griddepcontrol.wait: what that one wrote is there, for ordinary loads that stay behind the
+// wait (it names memory as changed).  __ldg is neither: the read-only path is for memory that
+// nothing writes during the kernel's life, which began before the wait.
+template <typename T>
+__device__ __forceinline__ T ld_behind_wait(const T* p) {
+    return *p;
+}
+
 // Atomic add at GPU scope with acquire-release semantics; returns the old value.
 __device__ __forceinline__ int atomic_add_acq_rel_gpu(int* addr, int v) {
     int old;

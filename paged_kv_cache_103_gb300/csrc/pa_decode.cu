@@ -194,8 +194,15 @@ __device__ __forceinline__ uint32_t u4_word(const uint4& v, int i) {
     return i == 0 ? v.x : (i == 1 ? v.y : (i == 2 ? v.z : v.w));
 }
 
+// A call's lengths, tables and queries; kLate: of a kernel that starts before its predecessor ends.
+template <bool kLate, typename T>
+__device__ __forceinline__ T ld_in(const T* p) {
+    if constexpr (kLate) return pa::ld_behind_wait(p);
+    return __ldg(p);
+}
+template <bool kLate>
 __device__ __forceinline__ uint32_t ld_u32(const uint16_t* p) {
-    return __ldg(reinterpret_cast<const unsigned int*>(p));
+    return ld_in<kLate>(reinterpret_cast<const unsigned int*>(p));
 }
 
 // A stage holds one chunk of K then one of V, each laid out [block][64-column
@@ -278,8 +285,8 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap kmap,
             g_wbase = (c0 * kChunk) >> (31 - __clz(bs));
             const int32_t* trow = p.block_tables + (int64_t)g_i * p.max_blocks;
             const int32_t j = g_wbase + lane;
-            g_went = j < p.max_blocks ? __ldg(trow + j) : -1;
-            g_wnext = j + 32 < p.max_blocks ? __ldg(trow + j + 32) : -1;
+            g_went = j < p.max_blocks ? ld_in<kPair>(trow + j) : -1;
+            g_wnext = j + 32 < p.max_blocks ? ld_in<kPair>(trow + j + 32) : -1;
             // ... and the K / V blocks of this producer's first chunk (chunk
             // c0 + prod of the guessed pair) are prefetched into L2, so that
             // the real loads after the scan find them there; a wrong guess only
@@ -310,7 +317,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap kmap,
         const int beg = min(tid * per, B), end = min(beg + per, B);
         int32_t local = 0;
         for (int i = beg; i < end; ++i) {
-            const int32_t raw = __ldg(p.context_lens + i);
+            const int32_t raw = ld_in<kPair>(p.context_lens + i);
             if (blockIdx.x == 0) {
                 if (raw < 0) pa::raise_error(p.err, PA_DEVERR_CONTEXT);
                 if (raw > max_len) pa::raise_error(p.err, PA_DEVERR_TABLE_WIDTH);
@@ -339,7 +346,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap kmap,
         for (int w = 0; w < warp; ++w) run += scan[w];
         for (int i = beg; i < end; ++i) {
             prefix[i] = run * Hkv;
-            run += (clamp_len(__ldg(p.context_lens + i), max_len) + kChunk - 1) / kChunk;
+            run += (clamp_len(ld_in<kPair>(p.context_lens + i), max_len) + kChunk - 1) / kChunk;
         }
         if (tid == 0) {
             int32_t total = 0;
@@ -400,7 +407,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap kmap,
             Walk w;
             w.s = find_segment(prefix, B, Hkv, at, hi);
             w.kvh = kPair ? w.s.i % p.pair_heads : w.s.g / p.subs;
-            w.n_raw = __ldg(p.context_lens + w.s.i);
+            w.n_raw = ld_in<kPair>(p.context_lens + w.s.i);
             w.trow = p.block_tables + (int64_t)w.s.i * p.max_blocks;
             w.wbase = (w.s.c0 * kChunk) >> bs_shift;
             if (w.s.i == g_i && w.wbase == g_wbase) {   // the window loaded at entry
@@ -410,8 +417,8 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap kmap,
                 return w;
             }
             const int32_t j = w.wbase + lane;
-            w.went = j < p.max_blocks ? __ldg(w.trow + j) : -1;
-            w.wnext = j + 32 < p.max_blocks ? __ldg(w.trow + j + 32) : -1;
+            w.went = j < p.max_blocks ? ld_in<kPair>(w.trow + j) : -1;
+            w.wnext = j + 32 < p.max_blocks ? ld_in<kPair>(w.trow + j + 32) : -1;
             return w;
         };
         int32_t k = 0;      // chunks of this CTA walked so far
@@ -434,7 +441,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap kmap,
                         cur.wbase += 32;
                         cur.went = cur.wnext;
                         const int32_t j = cur.wbase + 32 + lane;
-                        cur.wnext = j < p.max_blocks ? __ldg(cur.trow + j) : -1;
+                        cur.wnext = j < p.max_blocks ? ld_in<kPair>(cur.trow + j) : -1;
                     }
                     if (k >= S && !__all_sync(0xffffffffu,
                                               pa::mbar_wait(&empty[stage], use ^ 1u, kWaitLimitNs))) {
@@ -515,8 +522,8 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap kmap,
                 const uint16_t* qrow = p.q + ((int64_t)sg.i * p.H + sg.g * G + hq) * D + cc;
 #pragma unroll
                 for (int ks = 0; ks < D / 16; ++ks) {
-                    qb[nt][ks][0] = hq < G ? ld_u32(qrow + ks * 16) : 0u;
-                    qb[nt][ks][1] = hq < G ? ld_u32(qrow + ks * 16 + 8) : 0u;
+                    qb[nt][ks][0] = hq < G ? ld_u32<kPair>(qrow + ks * 16) : 0u;
+                    qb[nt][ks][1] = hq < G ? ld_u32<kPair>(qrow + ks * 16 + 8) : 0u;
                 }
             }
         } else {
@@ -533,8 +540,8 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap kmap,
                 const uint16_t* qrow = p.q + ((int64_t)sg.i * p.H + sg.g * G + hq) * D + 32 * c4;
 #pragma unroll
                 for (int ks = 0; ks < D / 16; ++ks) {
-                    qb[nt][ks][0] = hq < G ? ld_u32(qrow + 4 * ks) : 0u;
-                    qb[nt][ks][1] = hq < G ? ld_u32(qrow + 4 * ks + 2) : 0u;
+                    qb[nt][ks][0] = hq < G ? ld_u32<kPair>(qrow + 4 * ks) : 0u;
+                    qb[nt][ks][1] = hq < G ? ld_u32<kPair>(qrow + 4 * ks + 2) : 0u;
                     if constexpr (kBF16)
 #pragma unroll
                         for (int j = 0; j < 2; ++j)
@@ -701,7 +708,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap kmap,
     int32_t segn = 0;  // pairs this CTA has walked (selects the merge slot)
     if (lo < hi) {
         s = find_segment(prefix, B, Hkv, lo, hi);
-        n = clamp_len(__ldg(p.context_lens + s.i), max_len);
+        n = clamp_len(ld_in<kPair>(p.context_lens + s.i), max_len);
         load_q(s);
     }
     for (int32_t pos = lo; pos < hi;) {
@@ -1084,7 +1091,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap kmap,
         int32_t n_next = n;
         if (npos < hi) {
             sn = find_segment(prefix, B, Hkv, npos, hi);
-            n_next = clamp_len(__ldg(p.context_lens + sn.i), max_len);
+            n_next = clamp_len(ld_in<kPair>(p.context_lens + sn.i), max_len);
             load_q(sn);
         }
 

@@ -323,7 +323,7 @@ __global__ void __launch_bounds__(max_warps(kForm) * 32, 1) decode_int4_kernel(c
         int32_t local = 0, held = 0;   // cost; sequences that are not empty
 #pragma unroll 1
         for (int i = beg; i < end; ++i) {
-            const int32_t raw = __ldg(p.context_lens + i);
+            const int32_t raw = pa::ld_behind_wait(p.context_lens + i);
             if (blockIdx.x == 0) {
                 if (raw < 0) pa::raise_error(p.err, PA_DEVERR_CONTEXT);
                 if (raw > max_len) pa::raise_error(p.err, PA_DEVERR_TABLE_WIDTH);
@@ -351,7 +351,7 @@ __global__ void __launch_bounds__(max_warps(kForm) * 32, 1) decode_int4_kernel(c
 #pragma unroll 1
         for (int i = beg; i < end; ++i) {
             prefix[i] = run * Hkv;
-            const int32_t chunks = (clamp_len(__ldg(p.context_lens + i), max_len) + kChunk - 1) / kChunk;
+            const int32_t chunks = (clamp_len(pa::ld_behind_wait(p.context_lens + i), max_len) + kChunk - 1) / kChunk;
             run += chunks ? chunks + kPairCost : 0;
         }
         if (tid == 0) {
@@ -426,7 +426,7 @@ __global__ void __launch_bounds__(max_warps(kForm) * 32, 1) decode_int4_kernel(c
         };
         auto entry = [&](int32_t i, int32_t j, int32_t nb) {
             if (j >= nb) return -1;
-            const int32_t blk = __ldg(p.block_tables + (int64_t)i * p.max_blocks + j);
+            const int32_t blk = pa::ld_behind_wait(p.block_tables + (int64_t)i * p.max_blocks + j);
             if ((uint32_t)blk < (uint32_t)p.num_blocks) return blk;
             pa::raise_error(p.err, PA_DEVERR_BLOCK_ID);
             return -1;
@@ -435,7 +435,7 @@ __global__ void __launch_bounds__(max_warps(kForm) * 32, 1) decode_int4_kernel(c
             Walk w;
             w.s = s;
             const int32_t j0 = (s.c * kChunk) >> bs_shift, j = j0 + lane;
-            const int32_t n = clamp_len(__ldg(p.context_lens + s.i), max_len);
+            const int32_t n = clamp_len(pa::ld_behind_wait(p.context_lens + s.i), max_len);
             const uint32_t head = (uint32_t)(s.g / p.subs);
             w.at = 0;
             w.nb = (n + bmask) >> bs_shift;
@@ -515,8 +515,8 @@ __global__ void __launch_bounds__(max_warps(kForm) * 32, 1) decode_int4_kernel(c
 #pragma unroll
                 for (int g = 0; g < NG; ++g) {
                     const uint4 z = make_uint4(0, 0, 0, 0);
-                    const uint4 a = h < G ? __ldg(row + 8 * g) : z;
-                    const uint4 b = h < G ? __ldg(row + 8 * g + 1) : z;
+                    const uint4 a = h < G ? pa::ld_behind_wait(row + 8 * g) : z;
+                    const uint4 b = h < G ? pa::ld_behind_wait(row + 8 * g + 1) : z;
                     raw[nt][g][0] = a.x, raw[nt][g][1] = a.y, raw[nt][g][2] = a.z, raw[nt][g][3] = a.w;
                     raw[nt][g][4] = b.x, raw[nt][g][5] = b.y, raw[nt][g][6] = b.z, raw[nt][g][7] = b.w;
                 }
@@ -586,7 +586,7 @@ __global__ void __launch_bounds__(max_warps(kForm) * 32, 1) decode_int4_kernel(c
             }
             if (segn) convert_q();
             const int32_t c0 = s.c, c_end = min(s.nc, s.c + hi - pos);
-            const int32_t n = clamp_len(__ldg(p.context_lens + s.i), max_len);
+            const int32_t n = clamp_len(pa::ld_behind_wait(p.context_lens + s.i), max_len);
             // Running state for heads 8 nt + 2 c4 + {0, 1} (kG4: of that modulo 4): the negative
             // of the maximum (bias; the logits below are relative to it), sum, sums of P times
             // V's minima; o: rows are values 64 g + 8 cr + u (e < 2) and + 4 + u.
