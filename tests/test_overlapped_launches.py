@@ -1,7 +1,9 @@
 """Kernels that are launched before their predecessor in the stream has ended.
 
-On the CPU: what such a kernel reads behind its wait goes through coherent reads.  On the GPU: rows
-read on one stream while their neighbours are written and read back on another."""
+On the CPU: what such a kernel reads behind its wait goes through coherent reads.  On the GPU: whole
+chains of calls enqueued behind a delay, so that every call is there before the first one starts and
+each of them is launched early, against the same calls waited for one by one; the pairs of calls that
+may overlap stand next to each other, in a stream and in a captured graph."""
 import os
 import re
 
@@ -87,6 +89,117 @@ class Chain:
     def selected(self, q, out):
         binding.pa_decode_selected(q, self.k16, self.k16, self.sel, self.sel_n, self.keep * self.bs, self.scale, out,
                                    self.ws)
+
+
+def append_gather(c, n, wait):
+    """Every append overwrites the rows that the read back before it read."""
+    outs = [torch.zeros(2, *c.rows[0][0].shape, dtype=c.x.dtype, device="cuda") for _ in range(n)]
+    yield outs
+    for i in range(n):
+        c.append(i)
+        wait()
+        c.gather(i, outs[i])
+        wait()
+
+
+def append_decode(c, n, wait):
+    outs = [torch.zeros_like(c.x) for _ in range(n)]
+    yield outs
+    for i in range(n):
+        c.append(i)
+        wait()
+        c.decode(c.qs[i % 3], outs[i])
+        wait()
+
+
+def decode_decode(c, n, wait):
+    """A decode's output is the next one's query; one workspace."""
+    outs = [torch.zeros_like(c.x) for _ in range(n)]
+    c.append(0)
+    yield outs
+    for i in range(n):
+        c.decode(outs[i - 1] if i else c.qs[0], outs[i])
+        wait()
+
+
+def decode_gather(c, n, wait):
+    outs = [torch.zeros(2, *c.rows[0][0].shape, dtype=c.x.dtype, device="cuda") for _ in range(n)]
+    mid = [torch.zeros_like(c.x) for _ in range(n)]
+    c.append(0)
+    yield outs + mid
+    for i in range(n):
+        c.decode(c.qs[i % 3], mid[i])
+        wait()
+        c.gather(i, outs[i])
+        wait()
+
+
+def select_decode(c, n, wait):
+    """The lists are overwritten by the next selection, whose query is this decode's output."""
+    outs = [torch.zeros_like(c.x) for _ in range(n)]
+    yield outs
+    for i in range(n):
+        q = outs[i - 1] if i % 3 else c.qs[i % 2]
+        c.select(q)
+        wait()
+        c.selected(q, outs[i])
+        wait()
+
+
+def decode_then_selected(c, n, wait):
+    """A 4-bit decode's output is the query of the decode behind it, over lists made before."""
+    outs = [torch.zeros_like(c.x) for _ in range(2 * n)]
+    c.append(0)
+    c.select(c.qs[0])
+    yield outs
+    for i in range(n):
+        c.decode(outs[2 * i - 1] if i else c.qs[0], outs[2 * i])
+        wait()
+        c.selected(outs[2 * i], outs[2 * i + 1])
+        wait()
+
+
+CHAINS = [append_gather, append_decode, decode_decode, decode_gather, select_decode, decode_then_selected]
+
+
+@gpu
+@pytest.mark.parametrize("captured", [False, True])
+@pytest.mark.parametrize("T,Hkv,G", [(5, 1, 2), (700, 8, 4), (6000, 4, 1)])
+@pytest.mark.parametrize("chain", CHAINS)
+def test_chains_behind_a_delay(lib, chain, T, Hkv, G, captured):
+    n = 24
+    c = Chain(T, Hkv, G)
+
+    def calls(wait):
+        gen = chain(c, n, wait)
+        outs = next(gen)
+        return outs, lambda: next(gen, None)
+    want, go = calls(torch.cuda.synchronize)
+    go()
+    torch.cuda.synchronize()
+    if captured:
+        got, go = calls(lambda: None)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            go()
+        for _ in range(3):
+            for x in got:
+                x.zero_()
+            torch.cuda.synchronize()
+            graph.replay()
+            torch.cuda.synchronize()
+            assert all(torch.equal(a, b) for a, b in zip(got, want))
+    else:
+        for _ in range(3):
+            got, go = calls(lambda: None)
+            torch.cuda.synchronize()
+            torch.cuda._sleep(4_000_000)      # two milliseconds, in which all calls are enqueued
+            go()
+            torch.cuda.synchronize()
+            assert all(torch.equal(a, b) for a, b in zip(got, want))
+    assert binding.pa_check_device_errors() == 0
+    assert want[0].abs().amax() > 0
 
 
 @gpu
