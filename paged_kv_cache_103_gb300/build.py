@@ -23,7 +23,7 @@ CUDA_SOURCES = ["pa_decode.cu", "pa_cache.cu", "pa_runtime.cu", "pa_noalloc.cu",
                 "pa_multi_query_tc.cu", "pa_step.cu", "pa_cache_int4.cu", "pa_decode_int4.cu",
                 "pa_select.cu"]
 CXX_SOURCES = ["pa_allocator.cpp"]
-HEADERS = ["pa_common.cuh"]
+HEADERS = ["pa_common.cuh", "pa_device_once.h"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

@@ -8,6 +8,7 @@
 #include <stdint.h>
 
 #include "pa.h"
+#include "pa_device_once.h"
 
 namespace pa {
 
@@ -16,6 +17,16 @@ namespace pa {
 unsigned int* device_error_word();
 // Number of SMs of the current device (cached per device); 0 on error.
 int device_sm_count();
+// Raises a kernel's limit of dynamic shared memory on the current device; `once` is the
+// kernel's own.  False on error.
+template <typename K>
+bool allow_smem(DeviceOnce& once, K kern, size_t bytes) {
+    int dev = 0;
+    return cudaGetDevice(&dev) == cudaSuccess && once(dev, [&] {
+               return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                           (int)bytes) == cudaSuccess;
+           });
+}
 // Maps a CUDA error to a status (and remembers nothing else).
 inline pa_status cuda_status(cudaError_t e) { return e == cudaSuccess ? PA_OK : PA_ERR_CUDA; }
 

@@ -1242,20 +1242,17 @@ pa_status launch(const CUtensorMap& km, const CUtensorMap& vm, const CUtensorMap
                  const CUtensorMap& vsm, const DecodeParams& prm, size_t smem,
                  cudaStream_t stream) {
     auto kern = paged_decode_kernel<D, kBF16, NT, kAsync, kFp8, kInt8, kPair>;
-    static std::once_flag once;
-    static cudaError_t attr_err = cudaSuccess;
-    static int regs = 0;
-    std::call_once(once, [&] {
-        attr_err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                        (int)kSmemBudget);
-        cudaFuncAttributes fa{};
-        if (attr_err == cudaSuccess) attr_err = cudaFuncGetAttributes(&fa, kern);
-        regs = fa.numRegs;
-    });
-    if (attr_err != cudaSuccess) return PA_ERR_CUDA;
+    static pa::DeviceOnce once;
+    if (!pa::allow_smem(once, kern, kSmemBudget)) return PA_ERR_CUDA;
     // The 8-bit register split adds up only against this launch allocation: a
     // kernel built with another count would wait forever in setmaxnreg.
-    if (kFp8 && regs != kQ8LaunchRegs) return PA_ERR_UNSUPPORTED;
+    if constexpr (kFp8) {
+        static const int regs = [&] {
+            cudaFuncAttributes fa{};
+            return cudaFuncGetAttributes(&fa, kern) == cudaSuccess ? fa.numRegs : 0;
+        }();
+        if (regs != kQ8LaunchRegs) return PA_ERR_UNSUPPORTED;
+    }
     if constexpr (kPair) {
         // Started early, so that its launch hides behind the selection's last barriers.
         cudaLaunchAttribute attr{};

@@ -56,7 +56,6 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
-#include <atomic>
 #include <cmath>
 #include <cstring>
 
@@ -1133,16 +1132,8 @@ int choose_warps(int D, int G, int B) {
 template <int D, bool kBF16, int kForm, int kShift>
 pa_status launch(const Int4Params& p, cudaStream_t stream) {
     auto kern = decode_int4_kernel<D, kBF16, kForm, kShift>;
-    // The shared-memory limit is set once per device.
-    static std::atomic<uint64_t> done{0};
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev >= 64) return PA_ERR_CUDA;
-    if (!(done.load() >> dev & 1)) {
-        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 (int)kSmemBudget) != cudaSuccess)
-            return PA_ERR_CUDA;
-        done.fetch_or(1ull << dev);
-    }
+    static pa::DeviceOnce once;
+    if (!pa::allow_smem(once, kern, kSmemBudget)) return PA_ERR_CUDA;
     int ctas = pa::device_sm_count();
     if (ctas <= 0) return PA_ERR_CUDA;
     if (ctas > kMaxCtas) ctas = kMaxCtas;

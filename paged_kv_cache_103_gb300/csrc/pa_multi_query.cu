@@ -750,16 +750,16 @@ template <int D, bool kBF16, int NW>
 pa_status launch(const CUtensorMap& km, const CUtensorMap& vm, const Params& prm, size_t smem,
                  int grid, cudaStream_t stream) {
     auto kern = multi_query_kernel<D, kBF16, NW>;
-    static std::once_flag once;
-    static cudaError_t attr_err = cudaSuccess;
-    std::call_once(once, [&] {
-        attr_err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                        (int)Shape<NW>::kSmemBudget);
-        if (attr_err == cudaSuccess)   // the largest shared-memory carve-out
-            attr_err = cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout,
-                                            100);
+    static pa::DeviceOnce once;
+    int dev = 0;
+    const bool ok = cudaGetDevice(&dev) == cudaSuccess && once(dev, [&] {
+        return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    (int)Shape<NW>::kSmemBudget) == cudaSuccess &&
+               // the largest shared-memory carve-out
+               cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, 100) ==
+                   cudaSuccess;
     });
-    if (attr_err != cudaSuccess) return PA_ERR_CUDA;
+    if (!ok) return PA_ERR_CUDA;
     kern<<<grid, Shape<NW>::kThreads, smem, stream>>>(km, vm, prm);
     return pa::cuda_status(cudaGetLastError());
 }

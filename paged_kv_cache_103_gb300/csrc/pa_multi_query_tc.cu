@@ -1505,13 +1505,8 @@ template <bool kBF16>
 pa_status launch(const CUtensorMap& qm, const CUtensorMap& km, const CUtensorMap& vm,
                  const Params& prm, size_t smem, int grid, cudaStream_t stream) {
     auto kern = multi_query_tc_kernel<kBF16>;
-    static std::once_flag once;
-    static cudaError_t attr_err = cudaSuccess;
-    std::call_once(once, [&] {
-        attr_err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                        (int)smem_total(kMaxBatch));
-    });
-    if (attr_err != cudaSuccess) return PA_ERR_CUDA;
+    static pa::DeviceOnce once;
+    if (!pa::allow_smem(once, kern, smem_total(kMaxBatch))) return PA_ERR_CUDA;
     kern<<<grid, kThreads, smem, stream>>>(qm, km, vm, prm);
     return pa::cuda_status(cudaGetLastError());
 }
@@ -1524,13 +1519,8 @@ template <bool kBF16>
 pa_status launch_split(const CUtensorMap& qm, const CUtensorMap& km, const CUtensorMap& vm,
                        const SParams& prm, size_t smem, int grid, cudaStream_t stream) {
     auto kern = multi_query_tc_split_kernel<kBF16>;
-    static std::once_flag once;
-    static cudaError_t attr_err = cudaSuccess;
-    std::call_once(once, [&] {
-        attr_err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                        (int)split_smem_total(kMaxBatch));
-    });
-    if (attr_err != cudaSuccess) return PA_ERR_CUDA;
+    static pa::DeviceOnce once;
+    if (!pa::allow_smem(once, kern, split_smem_total(kMaxBatch))) return PA_ERR_CUDA;
     kern<<<grid, kThreads, smem, stream>>>(qm, km, vm, prm);
     return pa::cuda_status(cudaGetLastError());
 }

@@ -16,7 +16,6 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
-#include <atomic>
 #include <cstring>
 
 #include "pa.h"
@@ -456,15 +455,8 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams 
 template <bool kBF16, int D>
 pa_status launch_score(const SelectParams& p, dim3 grid, size_t smem, cudaStream_t stream) {
     auto kern = score_kernel<kBF16, D>;
-    // The shared-memory limit is set once per device.
-    static std::atomic<uint64_t> done{0};
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev >= 64) return PA_ERR_CUDA;
-    if (!(done.load() >> dev & 1)) {
-        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kScoreSmem) != cudaSuccess)
-            return PA_ERR_CUDA;
-        done.fetch_or(1ull << dev);
-    }
+    static pa::DeviceOnce once;
+    if (!pa::allow_smem(once, kern, kScoreSmem)) return PA_ERR_CUDA;
     kern<<<grid, kThreads, smem, stream>>>(p);
     return pa::cuda_status(cudaGetLastError());
 }
