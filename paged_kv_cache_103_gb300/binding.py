@@ -597,11 +597,15 @@ def pa_select_blocks(q, boxes, box_scale, block_tables, context_lens, block_size
         _ptr(workspace, workspace.dtype, dev), workspace.nbytes, st), "pa_select_blocks")
 
 
+MAX_PAIRS = 4096      # (sequence, KV head) pairs of one pa_decode_selected call of the library
+
+
 def pa_decode_selected(q, k_cache, v_cache, sel_blocks, sel_lens, max_sel_len: int, scale: float,
                        out, workspace, stream=None) -> None:
     """``pa_decode`` over a block list per (sequence, KV head): ``q/out [B, H, d]``, caches
     ``[N, bs, Hkv, d]``, ``sel_blocks [B, Hkv, keep]`` and ``sel_lens [B, Hkv]`` int32
-    (from ``pa_select_blocks``), ``workspace`` as ``pa_decode``'s."""
+    (from ``pa_select_blocks``), ``workspace`` as ``pa_decode``'s.  A batch of more than 4096
+    (sequence, KV head) pairs takes one launch per 4096 of them, in whole sequences."""
     import torch
     B, H, d = q.shape
     N, bs, Hkv, _ = k_cache.shape
@@ -612,6 +616,13 @@ def pa_decode_selected(q, k_cache, v_cache, sel_blocks, sel_lens, max_sel_len: i
         _misfit(k_cache=(k_cache, (N, bs, Hkv, d)), v_cache=(v_cache, tuple(k_cache.shape)),
                 sel_blocks=(sel_blocks, (B, Hkv, keep)), sel_lens=(sel_lens, (B, Hkv)),
                 out=(out, (B, H, d)))
+    most = max(1, MAX_PAIRS // max(1, Hkv))     # sequences of a launch
+    if B > most:
+        for i in range(0, B, most):
+            part = slice(i, i + most)
+            pa_decode_selected(q[part], k_cache, v_cache, sel_blocks[part], sel_lens[part], max_sel_len,
+                               scale, out[part], workspace, stream)
+        return
     dev, st = _where(q, stream)
     dt, i32 = q.dtype, torch.int32
     _check(load().pa_decode_selected(

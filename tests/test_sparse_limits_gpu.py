@@ -1,0 +1,42 @@
+"""Block-sparse decode at the sizes where its calls change form or meet their limits."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import cache4 as o
+from paged_kv_cache_103_gb300 import binding
+
+from _cache4 import workspace
+from _harness import assert_close
+from test_sparse_gpu import _case, _select
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from paged_kv_cache_103_gb300 import build
+    build.build()
+    binding.load()
+
+
+@pytest.mark.parametrize("B,H,Hkv,d", [(128, 40, 40, 128), (103, 80, 40, 64), (4096, 4, 2, 64)])
+def test_what_is_selected_can_be_decoded(B, H, Hkv, d):
+    """Batches of more than 4096 (sequence, KV head) pairs, ragged last part among them."""
+    rng = np.random.default_rng(B)
+    bs, keep = 8, 3
+    lens = rng.integers(0, 60, B).tolist()
+    q, k, v, tbl, hb, hs = _case(lens, bs, H, Hkv, d, torch.float16, 3)
+    sel, n = _select(q, hb, hs, tbl, lens, bs, keep, 0, 1)
+    want, wn = o.select_blocks(q.float().numpy(), hb, hs, tbl, lens, bs, keep, 0, 1)
+    assert np.array_equal(sel.cpu().numpy(), want) and np.array_equal(n.cpu().numpy(), wn)
+    out = torch.full_like(q, float("nan"), device="cuda")
+    ws = workspace(B, H, d)
+    for _ in range(2):
+        binding.pa_decode_selected(q.cuda(), k.cuda(), v.cuda(), sel, n, keep * bs, d ** -0.5, out, ws)
+    assert binding.pa_check_device_errors() == 0
+    ref = o.decode_selected(q.double().numpy(), k.double().numpy(), v.double().numpy(), want, wn, d ** -0.5)
+    assert_close(out.cpu(), ref)
+    assert int(ws[: B * H * 4].view(torch.int32).abs().sum()) == 0
