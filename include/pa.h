@@ -599,7 +599,7 @@ PA_API pa_status pa_summarize_blocks(const void* k_cache, const int32_t* block_i
  * chooses every block and reads no box.  A negative context counts as 0 and sets
  * PA_DEVERR_CONTEXT, one longer than its table row is cut to it and sets
  * PA_DEVERR_TABLE_WIDTH; an id outside the pool scores lowest, sets
- * PA_DEVERR_BLOCK_ID and is passed on if chosen all the same.
+ * PA_DEVERR_BLOCK_ID where it is scored or chosen and is passed on if chosen.
  *   q            (device) [B][H][d] fp16/bf16 (dtype), 16-byte aligned
  *   keep         >= first + last, first >= 0, last >= 1;  H / Hkv <= 128,
  *                Hkv <= 65535

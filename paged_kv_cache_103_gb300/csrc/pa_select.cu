@@ -329,10 +329,14 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams 
     for (int32_t j = count + tid; j < p.keep; j += kSelThreads) sel[j] = -1;
     const int32_t k = p.keep - p.first - p.last, m = nb - p.first - p.last;   // k < m below
     const int32_t head = nb <= p.keep ? nb : p.first;
-    for (int32_t j = tid; j < head; j += kSelThreads) sel[j] = __ldg(table + j);
+    auto keep_always = [&](int32_t to, int32_t from) {   // no score looks at these ids
+        const int32_t id = __ldg(table + from);
+        if (g == 0 && (uint32_t)id >= (uint32_t)p.num_blocks) pa::raise_error(p.err, PA_DEVERR_BLOCK_ID);
+        sel[to] = id;
+    };
+    for (int32_t j = tid; j < head; j += kSelThreads) keep_always(j, j);
     if (nb > p.keep)
-        for (int32_t j = tid; j < p.last; j += kSelThreads)
-            sel[p.keep - p.last + j] = __ldg(table + nb - p.last + j);
+        for (int32_t j = tid; j < p.last; j += kSelThreads) keep_always(p.keep - p.last + j, nb - p.last + j);
     for (int b = tid; b < kBins; b += kSelThreads) hist[b] = 0;
     const int32_t per = kPer ? kPer : (m + kSelThreads - 1) / kSelThreads;
     const int32_t beg = min(max(m, 0), tid * per), end = min(max(m, 0), beg + per);

@@ -40,3 +40,21 @@ def test_what_is_selected_can_be_decoded(B, H, Hkv, d):
     ref = o.decode_selected(q.double().numpy(), k.double().numpy(), v.double().numpy(), want, wn, d ** -0.5)
     assert_close(out.cpu(), ref)
     assert int(ws[: B * H * 4].view(torch.int32).abs().sum()) == 0
+
+
+@pytest.mark.parametrize("at,keep,last", [(0, 4, 1), (12, 4, 1), (11, 4, 2), (5, 13, 1), (5, 40, 1)])
+@pytest.mark.parametrize("bad_id", [-1, 1 << 20])
+def test_a_bad_id_is_flagged_where_it_is_kept_unscored(at, keep, last, bad_id):
+    """The first and last blocks, and all of them where nothing is left out, are listed without a
+    score; an id outside the pool among them is passed on and flagged like any other."""
+    lens, bs = [100, 30], 8
+    q, k, v, tbl, hb, hs = _case(lens, bs, 6, 3, 64, torch.float16, 3)
+    good = tbl.copy()
+    tbl[0, at] = bad_id
+    sel, n = _select(q, hb, hs, tbl, lens, bs, keep, 1, last)
+    assert binding.pa_check_device_errors() == binding.DEVERR["BLOCK_ID"]
+    want, wn = o.select_blocks(q.float().numpy(), hb, hs, good, lens, bs, keep, 1, last)
+    assert np.array_equal(sel.cpu().numpy(), np.where(want == good[0, at], bad_id, want))
+    assert np.array_equal(n.cpu().numpy(), wn)
+    _select(q, hb, hs, good, lens, bs, keep, 1, last)
+    assert binding.pa_check_device_errors() == 0
