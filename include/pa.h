@@ -511,7 +511,9 @@ PA_API pa_status pa_multi_query_tc(const void* q, const int32_t* q_start, int32_
  * for d = 128 only.  q and out are fp16/bf16 (dtype).  Both products run on
  * f16 tensor-core MMAs with fp32 accumulation: the codes widen exactly; a bf16
  * q is scaled by a power of two into f16 range first (exact for its elements
- * down to 2^-29 of its largest).  A table entry outside the pool reads zero
+ * down to 2^-29 of its largest); a probability times its V row's scale is rounded to
+ * f16 under a power of two that follows the largest V scale read, with fewer bits
+ * where the product is below 2^-28 of that scale.  A table entry outside the pool reads zero
  * codes and scales and sets PA_DEVERR_BLOCK_ID.  Other arguments, the
  * workspace and the errors are those of pa_decode.
  *   k_cache, v_cache (device) [num_blocks][block_size][Hkv][128] uint8
@@ -541,7 +543,8 @@ PA_API pa_status pa_decode_int8(const void* q, const void* k_cache, const void* 
  * bf16 q is scaled by a power of two into f16 range first (exact for elements
  * down to 2^-25 of the KV head's largest), and a probability times its row's step is
  * held to 16 bits (off by 2^-16 of itself at most) at any size.  A table entry outside the pool reads rows of
- * zeros and sets PA_DEVERR_BLOCK_ID.  Other arguments, the workspace
+ * zeros and sets PA_DEVERR_BLOCK_ID.  max_context_len must not be negative and is
+ * not used beyond that: the work is cut by context_lens.  Other arguments, the workspace
  * (pa_decode_workspace_size, here 16-byte aligned) and the errors are those of
  * pa_decode.
  *   q, out           (device) 16-byte aligned
@@ -572,7 +575,9 @@ PA_API pa_status pa_decode_int4(const void* q, const void* k_cache, const void* 
  *   boxes[b][h][1][c] = the same of hi_c;  box_scale[b][h] = S
  * (IEEE fp32 division); codes are 0 where S == 0, as for fill 0.  A block is
  * summarised when it has been filled (and again after it was written anew); the
- * blocks that pa_select_blocks always keeps need no box.  The same id may be
+ * blocks that pa_select_blocks always keeps need no box.  Boxes belong to a pool's
+ * block ids: a block that pa_copy_blocks, pa_swap_blocks or an append has written
+ * anew is summarised again, from its keys, before it is selected from.  The same id may be
  * listed more than once if its fill is the same.  An id outside the pool is
  * skipped and sets PA_DEVERR_BLOCK_ID; a fill outside [0, block_size] is cut to it
  * and sets PA_DEVERR_CONTEXT.  Rows holding NaN or infinity are outside this
@@ -596,7 +601,9 @@ PA_API pa_status pa_summarize_blocks(const void* k_cache, const int32_t* block_i
  * sel_blocks[i][g] receives the chosen blocks' physical ids in context order, then
  * -1; sel_lens[i][g] the tokens they hold (the context's last block is always
  * chosen and always last, so the lists read like block tables).  nb <= keep
- * chooses every block and reads no box.  A negative context counts as 0 and sets
+ * chooses every block and reads no box.  The boxes' codes and the query's are the
+ * nearest ones, so a score is a block's largest possible q . k to within their
+ * roundings.  A negative context counts as 0 and sets
  * PA_DEVERR_CONTEXT, one longer than its table row is cut to it and sets
  * PA_DEVERR_TABLE_WIDTH; an id outside the pool scores lowest, sets
  * PA_DEVERR_BLOCK_ID where it is scored or chosen and is passed on if chosen.

@@ -6,9 +6,12 @@
 // largest key value of each head-dim channel, lo_c and hi_c, as INT8 codes with
 // one fp32 scale.  For a query q the block's largest possible score is at most
 //     sum_c max(q_c lo_c, q_c hi_c) = sum_c q_c (q_c > 0 ? hi_c : lo_c),
-// so a block whose bound is low holds no key that matters.  The query is coded
+// so a block where that is low holds no key that matters.  The query is coded
 // in INT8 too, which makes the sum an integer: the score, and with it the
-// selection, does not depend on the order of summation.
+// selection, does not depend on the order of summation.  Codes are the nearest, so
+// what is ranked is the bound to within half a step of both codes and not the
+// bound itself: a key's score may pass it by
+//     sum_c ((|q_c| S + max(|lo_c|, |hi_c|) sq) / 2 + sq S / 4).
 //     sq = max |q_c| / 127,  c_c = rint(q_c / sq),  dot = sum_c c_c (..) ,
 //     score = max over the group's query heads of (dot sq) S
 // with every operation rounded to fp32 once.
