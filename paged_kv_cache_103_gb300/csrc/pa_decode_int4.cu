@@ -90,9 +90,15 @@ struct Int4Params {
 // The forms of the kernel by query heads of a KV head: one; up to 4; up to 8; up to 16.
 enum Form { kG1, kG4, kG8, kG16 };
 constexpr Form form_of(int G) { return G == 1 ? kG1 : G <= 4 ? kG4 : G <= 8 ? kG8 : kG16; }
-// One CTA per SM.  Sixteen warps, or eight where 9 .. 16 heads need two 8-wide MMA
-// tiles and twice the accumulators.
-__host__ __device__ constexpr int max_warps(int form) { return form == kG16 ? 8 : 16; }
+// One CTA per SM.  Warps by the registers a chunk takes: at d = 128 twelve of 168, which
+// keeps more than 128 in use (with sixteen of 128, which spill, 16 x 32768 tokens take 111.4 us
+// with G = 4 instead of 107.3, the 40-head batch 71.7 instead of 69.8, the long-tailed one of
+// G = 7 27.1 instead of 24.2; fourteen leave the four schedulers uneven: 120 us); at d = 64
+// sixteen (64.2 us against 65.7 with twelve); eight where 9 .. 16 heads need two 8-wide
+// MMA tiles and twice the accumulators.
+__host__ __device__ constexpr int max_warps(int D, int form) {
+    return form == kG16 ? 8 : D == 128 ? 12 : 16;
+}
 constexpr uint32_t kSmemBudget = 227 * 1024;
 
 // One partial result in shared memory: row maxima [G], row sums [G], padding to 16 bytes,
@@ -284,7 +290,7 @@ __device__ __forceinline__ float upper_half(float x) {
 // kG4: columns h and h + 4 are both head h, the latter with the second part of P and the
 // former with minus the first.
 template <int D, bool kBF16, int kForm, int kShift>
-__global__ void __launch_bounds__(max_warps(kForm) * 32, 1) decode_int4_kernel(const Int4Params p) {
+__global__ void __launch_bounds__(max_warps(D, kForm) * 32, 1) decode_int4_kernel(const Int4Params p) {
     constexpr bool kOne = kForm == kG1, kDup = kForm == kG4;
     constexpr int NG = D / 64, NT = kForm == kG16 ? 2 : 1, NJ = kOne ? 1 : 2;
     constexpr uint32_t kRow = D / 2, kSRow = NG * 4;         // bytes of a row's codes and scales
@@ -1124,7 +1130,7 @@ __global__ void __launch_bounds__(max_warps(kForm) * 32, 1) decode_int4_kernel(c
 
 // As many warps as shared memory holds rings and slots for; 0: not even four.
 int choose_warps(int D, int G, int B) {
-    for (int w = max_warps(form_of(G)); w >= 4; --w)
+    for (int w = max_warps(D, form_of(G)); w >= 4; --w)
         if (make_layout(D, G, B, w).total <= kSmemBudget) return w;
     return 0;
 }
