@@ -9,12 +9,12 @@
 // so the tensor cores multiply bare codes, K's step and minimum meet each score
 // once per key and group, V's step is folded into P, and the values of code 8 are one
 // number per (head, group).  The 8 that the codes are taken from is a product of its
-// own, P times a tile of eights, subtracted every eight chunks: what the tensor cores'
+// own, P times a tile of eights, subtracted every four chunks: what the tensor cores'
 // truncating sums do to the codes' mean (2.5 times their spread, and 100 times the result of
 // a long flat context) they do to the eights as well, and between two subtractions the sums
-// stay small.  (Subtracted once, at the end of a run, an f16 result of 32768 flat tokens was off
-// 1.6 times as far as an fp32 computation's, in 110 us for 16 contexts of 8 KV heads, G = 4;
-// so it is 1.002 times in 111, every four chunks 1.0005 in 111.5.)
+// stay small.  (Subtracted once, at the end of a run, an f16 result of 16 contexts of 32768
+// tokens, G = 4, was off 1.6 times as far as an fp32 computation's; every eight chunks it is
+// 1.002 times in 107.2 us, every four 1.0004 in 107.7, every two 1.0004 in 108.9.)
 //
 // P times V's step goes to the tensor cores as two bf16 numbers, its upper half and what
 // that leaves, rounded: 16 bits of it (off by 2^-16 of it at most) at every size that fp32
@@ -22,8 +22,8 @@
 // power of two for each warp, as it was, lost the codes of small steps beside a step 2^17
 // times theirs, and gave an f16 result 1.4 times an fp32 computation's error.)  Up to four
 // query heads the second part takes columns of the products that are free, above that
-// products of its own.  Against the single number 16 x 32768 tokens of 8 KV heads take 109.5
-// instead of 106 us with G = 4, 125 instead of 108 with G = 8, 196 instead of 159 with G = 16.
+// products of its own.  Against the single number 16 x 32768 tokens of 8 KV heads take 107.7
+// instead of 106 us with G = 4, 124 instead of 108 with G = 8, 197 instead of 159 with G = 16.
 //
 // A code needs no conversion.  As the low bits of an f16 whose other bits are zero
 // it is the subnormal c 2^-24 (c 2^-20 in the nibble above), exactly, and as a bf16's a
@@ -275,7 +275,7 @@ constexpr uint32_t kBytes = 0x00FF00FFu;         // of a bf16: (c + 16 c') 2^-13
 // (base 2): probabilities reach 2^8, which fp32 sums bear, and most chunks need neither the
 // maximum across lanes nor a rescale.
 constexpr float kLazy = 8.f;
-constexpr int kSettle = 8;   // chunks between two subtractions of the codes' middle
+constexpr int kSettle = 4;   // chunks between two subtractions of the codes' middle
 // V's steps are held 2^64 times as large, so that what they and P are multiplied by, codes
 // 2^-133 times theirs, leaves normal numbers down to a P of 2^-33 at f16's smallest step, and
 // sums over any context stay far below fp32's largest.

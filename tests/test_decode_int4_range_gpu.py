@@ -64,7 +64,7 @@ def group_bound(q, cache, tbl, n, scale, dtype, ref):
       2^-19 + 2^-20 |x|;
     * the sums over the keys, on the tensor cores (16 keys at a time, the two parts one after the
       other, each sum cut off 2^-23 of the largest partial sum at worst, which the weight of the
-      eight chunks between two subtractions of the codes' middle bounds): 32 of them for P's
+      chunks between two subtractions of the codes' middle bounds, eight at most): 32 of them for P's
       codes and 32 for the eights, and one rounding of what is left per subtraction; the
       minima in fp32, each lane every eighth key, n / 8 roundings of 2^-24; the joins, 64 of 2^-24:
       (64 + 32 + n / 16) 2^-23 of sum_j w_j a_j.
@@ -171,8 +171,8 @@ def test_an_f16_result_is_off_by_little_but_its_own_rounding(n, B, limit, H, Hkv
     * short contexts: with x = sum_j (w_j s_j (c_j - 8))^2 the result is of size sqrt(x), and P's
       second part is off by 2^-17.8 of each product, together 2^-17.8 sqrt(x): r / 45, and the
       fp32 steps less: 5% is ample;
-    * long ones: with a = sum_j w_j 8 s_j, the result is some a / 300 and r 2^-20.5 a; of the 32 sums
-      between two subtractions, of the codes and of the eights, each cuts half a unit of 2^-23 on
+    * long ones: with a = sum_j w_j 8 s_j, the result is some a / 300 and r 2^-20.5 a; of the 32 sums at
+      most between two subtractions, of the codes and of the eights, each cuts half a unit of 2^-23 on
       average, alike but where one of the two lies beyond a power of two: (1/2) 32 / 2 of 2^-24 a
       = 2^-21 a where it does, and its deviation, 2^-23 a, averages out over the subtractions:
       at most sqrt(1 + (3/4)^2) = 1.25 r.
