@@ -792,7 +792,7 @@ __global__ void __launch_bounds__(max_warps(D, kForm) * 32, 1) decode_int4_kerne
                                 // One product behind, the second parts: no two in a row into one
                                 // accumulator.
                                 constexpr bool kTwo = !kOne && !kDup;
-                                uint32_t a[4], was[4];
+                                uint32_t a[4] = {}, was[4];
 #pragma unroll
                                 for (int u = 0; u < 4; ++u) {
                                     // u even: the byte's lower code; u odd: the whole byte, lower
