@@ -416,8 +416,8 @@ PA_API pa_status pa_decode_workspace_init(void* workspace, size_t bytes, void* s
  * n = context_lens[i] and query head h:
  *   s_j = scale * q[i][h] . K_j,  K_j = k_cache[block_tables[i][j / bs]][j % bs][h / G]
  *   out[i][h] = sum_j softmax(s)_j V_j       over j in [0, n)
- * with fp32 accumulation, rounded once to the output dtype; n == 0 gives a
- * zero row.  The caller passes scale (1/sqrt(d) for the pages' formula).
+ * with fp32 accumulation, rounded once to the output dtype (a probability is held
+ * to 11 bits for fp16, to about 16 for bf16); n == 0 gives a zero row.  The caller passes scale (1/sqrt(d) for the pages' formula).
  *   q            (device) [B][H][d]
  *   k_cache, v_cache (device) [num_blocks][block_size][Hkv][d]
  *   block_tables (device) [B][max_blocks] int32

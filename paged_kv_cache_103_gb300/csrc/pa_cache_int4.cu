@@ -17,7 +17,7 @@
 // some ten instructions.  A thread takes K and V of the same place together, and the read
 // back four such places where there are enough, as independent chains of dependent loads
 // (slot, then codes) that hide each other's latency.
-// Measured at d = 128: append of 8192 x 8 rows 12.2 us (33.6 MB in, 9.4 out: 3.5 TB/s;
+// Measured at d = 128: append of 8192 x 8 rows 12.3 us (33.6 MB in, 9.4 out: 3.5 TB/s;
 // issue and its short grid), read back of 32768 x 8 rows 28.9 us (172 MB: 5.9 TB/s),
 // append and read back of 64 x 40 rows 4.5 us, all of it latency.
 #include <cuda_fp16.h>
@@ -322,7 +322,7 @@ pa_status gather(const void* k_cache, const void* v_cache, const void* k_scale,
     const FastDiv by_heads((uint32_t)Hkv);
     // Four pieces a thread once they fill the SMs' threads all the same, else one: the read
     // back of 32768 x 8 rows took 29.6 us with four and 34.1 us with one, that of 1001 x 4
-    // rows 2.4 us with four and 1.9 us with one.
+    // rows 2.4 us with four and 1.9 us with one (28.9 and 1.6 with what came after).
     const int64_t fill = 4ll * 2048 * pa::device_sm_count();
     for (int64_t t0 = 0; t0 < T_tokens; t0 += slab) {
         const int64_t n = T_tokens - t0 < slab ? T_tokens - t0 : slab;

@@ -44,14 +44,14 @@
 // through the workspace, by the CTA that arrives last:
 //     M = max m_p,  out = sum_p 2^(m_p - M) o_p / sum_p 2^(m_p - M) l_p.
 //
-// Measured (d = 128, device time): 16 x 32768 tokens of 8 KV heads, G = 4: 106 us, 5.7
-// TB/s, DRAM traffic 1.000 times the bytes above, 55 % of the ALU's and 29 % of the tensor
-// pipe's cycles, 59 % of the issue slots; 64 sequences of 128 .. 2048 tokens, 40 heads, G =
-// 1: 72 us, 5.6 TB/s; 32 long-tailed contexts, 4 heads of G = 7, 70 MB: 24 us, of which
+// Measured (d = 128, device time): 16 x 32768 tokens of 8 KV heads, G = 4: 107.8 us, 5.6
+// TB/s, DRAM traffic 1.000 times the bytes above, 53 % of the ALU's and 28 % of the tensor
+// pipe's cycles, 57 % of the issue slots; 64 sequences of 128 .. 2048 tokens, 40 heads, G =
+// 1: 70 us, 5.7 TB/s; 32 long-tailed contexts, 4 heads of G = 7, 70 MB: 24 us, of which
 // the start is some 4 (lengths, table, first copies) and the joining of pairs at the end as
-// much; 4 sequences of up to 64 tokens: 6 us, all latency.  Asynchronous copies took the
+// much; 4 sequences of up to 64 tokens: 6.6 us, all latency.  Asynchronous copies took the
 // place of bulk copies (one per tile, each a turn of a loop over the lanes), and one CTA
-// of 16 warps that of two CTAs of 8, whose pairs crossed CTAs twice as often.
+// that of two CTAs of 8 warps, whose pairs crossed CTAs twice as often.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>

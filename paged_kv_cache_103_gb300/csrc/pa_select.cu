@@ -45,7 +45,7 @@ __device__ __forceinline__ uint32_t code8(float x, float s) {
 
 // One warp per (listed block, KV head): lane l owns channels 8 (l % (D / 8)) .. + 7 of every
 // (32 / (D / 8))-th row, so a block's rows are in flight at once.  Bound by HBM: 2048
-// blocks of 16 x 8 x 128 values (71.4 MB) take 14.6 us, 4.9 TB/s (16.0 us before a lane
+// blocks of 16 x 8 x 128 values (71.4 MB) take 15.0 us, 4.8 TB/s (16.0 us before a lane
 // had four rows in flight).  Afterwards the first half of the warp has the smallest values
 // to code, the second the largest.
 template <bool kBF16, int D>
