@@ -627,7 +627,8 @@ PA_API pa_status pa_select_blocks(const void* q, const void* boxes, const float*
  * sequence: query head h of sequence i attends to the first sel_lens[i][h / G]
  * tokens of the blocks sel_blocks[i][h / G][:].  sel_blocks [B][Hkv][keep] and
  * sel_lens [B][Hkv] are those of pa_select_blocks (any lists will do); max_sel_len
- * is an upper bound of sel_lens.  B * Hkv is at most 4096; a larger batch, which
+ * is an upper bound of sel_lens.  A probability is held to 16 bits or more for
+ * either type.  B * Hkv is at most 4096; a larger batch, which
  * pa_select_blocks takes, is passed in slices of sequences (rows of q, sel_blocks,
  * sel_lens and out; the workspace may be the same).  Other arguments, the
  * workspace (pa_decode_workspace_size(B, H, d) bytes, here 16-byte aligned) and

@@ -273,6 +273,14 @@ __device__ __forceinline__ uint32_t bf16x2_residual(uint32_t packed, float lo, f
     return pack2<true>(lo - __uint_as_float(packed << 16), hi - __uint_as_float(packed & 0xFFFF0000u));
 }
 
+// The same of a pack2<false>(lo, hi) register: together about 22 bits.
+__device__ __forceinline__ uint32_t f16x2_residual(uint32_t packed, float lo, float hi) {
+    float a, b;
+    asm("{.reg .f16 x, y;\n mov.b32 {x, y}, %2;\n cvt.f32.f16 %0, x;\n cvt.f32.f16 %1, y;}"
+        : "=f"(a), "=f"(b) : "r"(packed));
+    return pack2<false>(lo - a, hi - b);
+}
+
 // 2^x with the hardware approximation (relative error about 2^-22).
 __device__ __forceinline__ float fast_exp2(float x) {
     float y;

@@ -911,8 +911,10 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap kmap,
                 // P^T as MMA B fragments: exp2, pack to 16 bits, transpose 8x8 tiles.
                 // A bf16 P keeps 8 bits; its rounding residual (pbl, a second
                 // B operand) restores about 16, so a short context whose V terms
-                // cancel stays within the tolerance (f16 and FP8 use f16 P).
-                constexpr bool kPbf16 = kBF16 && !kFp8;
+                // cancel stays within the tolerance.  An f16 P keeps 11 (f16 and FP8 caches);
+                // over chosen blocks, few keys as a rule, it has its residual too: without it
+                // an f16 result was off 1.2 times as far as an fp32 computation's.
+                constexpr bool kPbf16 = kBF16 && !kFp8, kTwoParts = kPbf16 || kPair;
                 uint32_t pb[kKeyTiles][NT][2];
                 uint32_t pbl[kKeyTiles][NT][2];
 #pragma unroll
@@ -937,11 +939,12 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap kmap,
                         const uint32_t h23 = pa::pack2<kPbf16>(e4[2], e4[3]);
                         pb[mt][nt][0] = pa::movmatrix_trans(h01);
                         pb[mt][nt][1] = pa::movmatrix_trans(h23);
-                        if constexpr (kPbf16) {
-                            pbl[mt][nt][0] =
-                                pa::movmatrix_trans(pa::bf16x2_residual(h01, e4[0], e4[1]));
-                            pbl[mt][nt][1] =
-                                pa::movmatrix_trans(pa::bf16x2_residual(h23, e4[2], e4[3]));
+                        if constexpr (kTwoParts) {
+                            auto left = [](uint32_t h, float lo, float hi) {
+                                return kPbf16 ? pa::bf16x2_residual(h, lo, hi) : pa::f16x2_residual(h, lo, hi);
+                            };
+                            pbl[mt][nt][0] = pa::movmatrix_trans(left(h01, e4[0], e4[1]));
+                            pbl[mt][nt][1] = pa::movmatrix_trans(left(h23, e4[2], e4[3]));
                         }
                     }
 
@@ -1003,7 +1006,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap kmap,
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt) {
                             pa::mma_16816<kBF16>(o[mt][nt], a, pb[ks2][nt][0], pb[ks2][nt][1]);
-                            if constexpr (kPbf16)
+                            if constexpr (kTwoParts)
                                 pa::mma_16816<kBF16>(o[mt][nt], a, pbl[ks2][nt][0],
                                                      pbl[ks2][nt][1]);
                         }

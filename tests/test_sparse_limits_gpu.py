@@ -109,3 +109,26 @@ def test_a_wide_table_costs_little():
             best = min(best, a.elapsed_time(b))
         times.append(best)
     assert times[1] < 3 * times[0], times
+
+
+@pytest.mark.parametrize("H,Hkv,d", [(2, 2, 128), (12, 3, 64), (8, 1, 128), (16, 1, 128), (32, 1, 64)])
+def test_an_f16_result_over_chosen_blocks_is_off_by_its_own_rounding(H, Hkv, d):
+    """Root mean squares, r that of the output's rounding (known from the reference; some 2^-12.3 of
+    the result): a probability in two f16 parts is off by 2^-22 of itself, or 2^-25 of the largest,
+    and the fp32 steps by less than 2^-18 together (logits of a few units: 2^-21 each, exp2 2^-22, sums
+    of at most 64 keys on the tensor cores 2^-21), 2% of r; a single f16 part gives 1.1 r and more."""
+    B, bs, n = 24, 16, 60
+    rng = np.random.default_rng(H)
+    N = 40
+    k, v = (torch.from_numpy(rng.standard_normal((N, bs, Hkv, d)).astype(np.float32)).half() for _ in "kv")
+    q = torch.from_numpy(rng.standard_normal((B, H, d)).astype(np.float32)).half()
+    sel = rng.integers(0, N, (B, Hkv, 4)).astype(np.int32)
+    lens = np.full((B, Hkv), n, np.int32)
+    out = torch.empty_like(q, device="cuda")
+    binding.pa_decode_selected(q.cuda(), k.cuda(), v.cuda(), torch.from_numpy(sel).cuda(), torch.from_numpy(lens).cuda(),
+                               64, d ** -0.5, out, workspace(B, H, d))
+    assert binding.pa_check_device_errors() == 0
+    ref = o.decode_selected(q.double().numpy(), k.double().numpy(), v.double().numpy(), sel, lens, d ** -0.5)
+    rms = lambda x: float(np.sqrt(np.mean(np.square(x))))  # noqa: E731
+    r = rms(ref.astype(np.float16).astype(np.float64) - ref)
+    assert rms(out.cpu().double().numpy() - ref) <= 1.02 * r, rms(out.cpu().double().numpy() - ref) / r
