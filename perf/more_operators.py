@@ -399,10 +399,10 @@ PLAIN = dict(write=_plain_write, read=_plain_read, decode=_plain_decode, weigh=_
 
 
 # ------------------------------------------------------------------------ the library's calls
-def _workspace(pa, st, size):
+def _workspace(st, size, *sizes):
     """A decode's workspace, which a program allocates and zeroes once."""
     if "ws" not in st:
-        st["ws"] = torch.zeros(size, dtype=torch.uint8, device="cuda")
+        st["ws"] = torch.zeros(size(*sizes), dtype=torch.uint8, device="cuda")
     return st["ws"]
 
 
@@ -421,12 +421,13 @@ def _own(st):
     if kind == "decode":
         decode = {"int8": pa.pa_decode_int8_block, "fp8": pa.pa_decode_fp8_block}[c["fmt"]]
         decode(st["q"], *cache, st["tables"], st["lens"], st["max_len"], st["scale"], st["out"],
-               _workspace(pa, st, pa.pa_decode_workspace_size(c["B"], c["H"], c["d"])))
+               _workspace(st, pa.pa_decode_workspace_size, c["B"], c["H"], c["d"]))
         return st["out"]
     if kind == "weigh":
-        size = pa.pa_decode_weights_workspace_size(c["B"], c["H"], c["Hkv"], c["d"], st["tokens"])
         pa.pa_decode_weights(st["q"], *cache, st["tables"], st["lens"], st["max_len"], st["scale"], st["out"],
-                             st["weights"], st["rows"], _workspace(pa, st, size))
+                             st["weights"], st["rows"],
+                             _workspace(st, pa.pa_decode_weights_workspace_size, c["B"], c["H"], c["Hkv"], c["d"],
+                                        st["tokens"]))
         return st["out"], st["weights"]
     pa.pa_select_tokens(st["weights"], st["rows"], st["lens"], c["first"], c["last"], st["kept"], st["kept_lens"],
                         st["new_weights"])
