@@ -63,7 +63,7 @@ typedef enum pa_dtype { PA_F16 = 0, PA_BF16 = 1 } pa_dtype;
 /* Bits of the device error word (pa_check_device_errors). */
 #define PA_DEVERR_BLOCK_ID 0x1u     /* table entry < 0 or >= num_blocks */
 #define PA_DEVERR_TABLE_WIDTH 0x2u  /* context_len needs more blocks than max_blocks */
-#define PA_DEVERR_SLOT 0x4u         /* slot >= num_blocks * block_size */
+#define PA_DEVERR_SLOT 0x4u         /* slot >= num_blocks * block_size, or an accumulator row >= num_rows */
 #define PA_DEVERR_TIMEOUT 0x8u      /* a bounded pipeline wait gave up */
 #define PA_DEVERR_PAIR 0x10u        /* copy pair outside the pool */
 #define PA_DEVERR_CONTEXT 0x20u     /* negative context length */
@@ -142,6 +142,20 @@ PA_API pa_status pa_fork(pa_allocator* a, int64_t parent, int64_t child);
  * table order. */
 PA_API pa_status pa_free(pa_allocator* a, int64_t seq_id);
 
+/* Cuts a sequence to num_tokens tokens (0 <= num_tokens <= its length) for an eviction
+ * that keeps as many of them (pa_select_tokens, pa_compact_tokens): the blocks behind the
+ * first ceil(num_tokens / block_size) are dropped as pa_free drops them, and of those
+ * that stay each that other sequences share is replaced by a block from the front of the free
+ * list (taken before any block is dropped), because the kept rows will be written there.
+ * The blocks that stay lose their prefix-cache entries and the sequence stops registering:
+ * their content is no longer a prefix's.  A length equal to num_tokens changes nothing.
+ * Export the table before the call (to read from) and after it (to write to), and compact
+ * on the device before anything else writes to the dropped blocks (the same stream will
+ * do).  Where the caller keeps several layers, it compacts each layer's cache.  All or
+ * nothing: PA_ERR_OOM leaves every state unchanged.  PA_ERR_INVALID for a swapped-out
+ * sequence or a num_tokens outside the range. */
+PA_API pa_status pa_alloc_evict(pa_allocator* a, int64_t seq_id, int32_t num_tokens);
+
 /* Fills block_tables (host, [B][max_blocks] int32, unused entries -1) and
  * context_lens (host, [B] int32) for seq_ids[0..B).  A table longer than
  * max_blocks returns PA_ERR_INVALID. */
@@ -181,7 +195,8 @@ typedef struct pa_prefix_stats {
     int64_t lookups;      /* prompt blocks looked up (each walk stops at its first miss) */
     int64_t hits;         /* of which found */
     int64_t registered;   /* blocks entered into the cache */
-    int64_t evicted;      /* entries dropped because their block was handed out again */
+    int64_t evicted;      /* entries dropped because their block was handed out again (or is
+                             written anew by an eviction, pa_alloc_evict) */
     int64_t entries;      /* entries now in the cache */
     int64_t cached_free;  /* free-list blocks that still hold an entry */
 } pa_prefix_stats;
@@ -340,6 +355,42 @@ PA_API pa_status pa_reshape_and_cache_int4(const void* k_new, const void* v_new,
                                            int32_t num_blocks, int32_t block_size, int32_t Hkv,
                                            int32_t d, pa_dtype dtype, void* stream);
 
+/* Block-scaled 8-bit KV append: codes as in the two 8-bit caches above, but one fp32
+ * scale per (block, KV head) instead of one per token, and KV heads outside the rows
+ * of a block as in the 4-bit cache, so that a (block, KV head) tile is one contiguous
+ * run.  For each block b that the call writes to and every KV head h, with R the rows
+ * of b that it writes and a = max |x| over them (widened to fp32):
+ *   base = 0 if row 0 is in R (the block begins anew), else k_scale[b][h]
+ *   s = max(base, fl32(a / TOP))                   TOP = 127 (INT8), 448 (E4M3)
+ *   rows in R:   code(fl32(x / s)), 0 where s == 0  (as the appends above round)
+ *   other rows, if 0 < base < s: code(fl32(c fl32(base / s))) for their codes c
+ *   k_scale[b][h] = s
+ * and the same for V (IEEE fp32 divisions).  So a block's scale grows with the tokens
+ * that fill it, at a rounding of its earlier codes each time.  Rows that a block which
+ * begins anew does not get are left as they are and mean nothing until they are written.
+ * Slots must be distinct, and the tokens of one block neighbours in the call, with
+ * nothing but padding (negative slots) between them -- the order of pa_seq_slots.  A
+ * slot >= num_blocks * block_size is skipped and sets PA_DEVERR_SLOT.  Rows holding NaN
+ * or infinity are outside this contract.  Blocks stay contiguous, so pa_copy_blocks and
+ * pa_swap_blocks move the codes; a block's scales, Hkv * 4 bytes, move with them where
+ * that is a multiple of 16, and by the caller's own copy where it is not.
+ *   k_new, v_new     (device) [T][Hkv][d] fp16/bf16 (dtype), d = 64 or 128, 16-byte aligned
+ *   slot_mapping     (device) [T] int64
+ *   k_cache, v_cache (device) [num_blocks][Hkv][block_size][d] uint8 codes, 16-byte aligned
+ *   k_scale, v_scale (device) [num_blocks][Hkv] fp32 */
+PA_API pa_status pa_reshape_and_cache_int8_block(const void* k_new, const void* v_new,
+                                                 const int64_t* slot_mapping, int32_t T,
+                                                 void* k_cache, void* v_cache, float* k_scale,
+                                                 float* v_scale, int32_t num_blocks,
+                                                 int32_t block_size, int32_t Hkv, int32_t d,
+                                                 pa_dtype dtype, void* stream);
+PA_API pa_status pa_reshape_and_cache_fp8_block(const void* k_new, const void* v_new,
+                                                const int64_t* slot_mapping, int32_t T,
+                                                void* k_cache, void* v_cache, float* k_scale,
+                                                float* v_scale, int32_t num_blocks,
+                                                int32_t block_size, int32_t Hkv, int32_t d,
+                                                pa_dtype dtype, void* stream);
+
 /* Reads tokens of a quantised cache back into 16 bits, the appends' inverse:
  * for t in [0, T) with slot = slot_mapping[t] >= 0 and every KV head h,
  * k_out[t][h][:] becomes the values that the row at that slot stands for --
@@ -367,6 +418,18 @@ PA_API pa_status pa_gather_cache_fp8(const void* k_cache, const void* v_cache,
                                      const int64_t* slot_mapping, int32_t T, void* k_out,
                                      void* v_out, int32_t num_blocks, int32_t block_size,
                                      int32_t Hkv, int32_t d, pa_dtype dtype, void* stream);
+
+/* The same for a block-scaled 8-bit cache (fl32(code scale), the scale that of the block). */
+PA_API pa_status pa_gather_cache_int8_block(const void* k_cache, const void* v_cache,
+                                            const float* k_scale, const float* v_scale,
+                                            const int64_t* slot_mapping, int32_t T, void* k_out,
+                                            void* v_out, int32_t num_blocks, int32_t block_size,
+                                            int32_t Hkv, int32_t d, pa_dtype dtype, void* stream);
+PA_API pa_status pa_gather_cache_fp8_block(const void* k_cache, const void* v_cache,
+                                           const float* k_scale, const float* v_scale,
+                                           const int64_t* slot_mapping, int32_t T, void* k_out,
+                                           void* v_out, int32_t num_blocks, int32_t block_size,
+                                           int32_t Hkv, int32_t d, pa_dtype dtype, void* stream);
 
 /* Copy-on-write block copies ([P3] section 3.3): for every layer l and pair p,
  * block pairs[p][1] of k_caches[l] and v_caches[l] becomes a bit copy of
@@ -559,6 +622,35 @@ PA_API pa_status pa_decode_int4(const void* q, const void* k_cache, const void* 
                                 int32_t num_blocks, float scale, pa_dtype dtype, void* out,
                                 void* workspace, size_t ws_bytes, void* stream);
 
+/* pa_decode over a block-scaled 8-bit cache written by pa_reshape_and_cache_int8_block /
+ * _fp8_block: computes what pa_decode computes with K_j = k_scale[b][h / G] * code,
+ * V_j likewise, for d = 64 or 128.  Both products take fp32 sums; a bf16 q is scaled by
+ * a power of two into f16 range first (exact for elements down to 2^-25 of the KV head's
+ * largest), and a probability times its block's V scale is held to 16 bits.  V scales of
+ * 2^-80 and more keep that precision.  A table entry outside the pool reads rows of
+ * zeros and sets PA_DEVERR_BLOCK_ID.  max_context_len must not be negative and is not
+ * used beyond that.  Other arguments, the workspace (pa_decode_workspace_size, here
+ * 16-byte aligned) and the errors are those of pa_decode.
+ *   q, out           (device) 16-byte aligned
+ *   k_cache, v_cache (device) [num_blocks][Hkv][block_size][d] uint8, 16-byte aligned
+ *   k_scale, v_scale (device) [num_blocks][Hkv] fp32 */
+PA_API pa_status pa_decode_int8_block(const void* q, const void* k_cache, const void* v_cache,
+                                      const float* k_scale, const float* v_scale,
+                                      const int32_t* block_tables, int32_t max_blocks,
+                                      const int32_t* context_lens, int32_t max_context_len,
+                                      int32_t B, int32_t H, int32_t Hkv, int32_t d,
+                                      int32_t block_size, int32_t num_blocks, float scale,
+                                      pa_dtype dtype, void* out, void* workspace,
+                                      size_t ws_bytes, void* stream);
+PA_API pa_status pa_decode_fp8_block(const void* q, const void* k_cache, const void* v_cache,
+                                     const float* k_scale, const float* v_scale,
+                                     const int32_t* block_tables, int32_t max_blocks,
+                                     const int32_t* context_lens, int32_t max_context_len,
+                                     int32_t B, int32_t H, int32_t Hkv, int32_t d,
+                                     int32_t block_size, int32_t num_blocks, float scale,
+                                     pa_dtype dtype, void* out, void* workspace,
+                                     size_t ws_bytes, void* stream);
+
 /* ------------------------------------------------------------------------
  * Block-sparse decode: a long context's query reads only the blocks whose keys
  * can score high.  The pages have no counterpart; it is the paged cache's own
@@ -639,6 +731,91 @@ PA_API pa_status pa_decode_selected(const void* q, const void* k_cache, const vo
                                     int32_t H, int32_t Hkv, int32_t d, int32_t block_size,
                                     int32_t num_blocks, float scale, pa_dtype dtype, void* out,
                                     void* workspace, size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Eviction by accumulated attention weight: a context that has outgrown its budget
+ * keeps its first tokens, its last ones and those that the queries so far have
+ * weighted most, chosen per (sequence, KV head).  The pages have no counterpart (their
+ * answer to a full pool is swap or preemption, [P1] section 3.2).  pa_decode_weights
+ * accumulates the weights step by step, pa_select_tokens chooses, pa_alloc_evict takes
+ * the blocks that fall free, pa_compact_tokens moves the kept rows together.  Keys keep
+ * the position encoding that they were written with; the sequence goes on at its new
+ * length as far as the cache is concerned.
+ *
+ * An accumulator row belongs to a sequence: weights [num_rows][Hkv][width] fp32, with
+ * rows[i] the row of the batch's sequence i and its entry j the token at position j.  The
+ * caller zeroes a row when a sequence takes it.  Rows of one call must be distinct; a
+ * negative row marks a sequence that takes no part (padding, or one without an
+ * accumulator); one >= num_rows takes no part either and sets PA_DEVERR_SLOT.
+ * ---------------------------------------------------------------------- */
+
+/* pa_decode that also adds every token's softmax weight to its accumulator:
+ *   out as pa_decode's;
+ *   weights[rows[i]][g][j] += sum over the query heads h of g of softmax_j(s of h)
+ * for j < min(context_lens[i], width); a context longer than width sets
+ * PA_DEVERR_TABLE_WIDTH.  A bf16 or fp16 P is held to 16 bits or more in out; the
+ * weights are fp32 throughout, the heads added in order, so that equal calls give equal
+ * results.
+ *   weights   (device) [num_rows][Hkv][width] fp32, updated in place
+ *   rows      (device) [B] int32
+ *   workspace (device, 16-byte aligned) >= pa_decode_weights_workspace_size(B, H, Hkv, d,
+ *             tokens) bytes, zeroed once by pa_decode_workspace_init, where tokens
+ *             is the sum of the call's context lengths or more (B * max_context_len always
+ *             will do): the logits of a call, 4 bytes a (token, query head), lie there.  A call
+ *             whose contexts need more computes out, adds nothing and sets PA_DEVERR_CONTEXT.
+ *   other arguments and errors as pa_decode's */
+PA_API size_t pa_decode_weights_workspace_size(int32_t B, int32_t H, int32_t Hkv, int32_t d,
+                                               int64_t tokens);
+PA_API pa_status pa_decode_weights(const void* q, const void* k_cache, const void* v_cache,
+                                   const int32_t* block_tables, int32_t max_blocks,
+                                   const int32_t* context_lens, int32_t max_context_len,
+                                   int32_t B, int32_t H, int32_t Hkv, int32_t d,
+                                   int32_t block_size, int32_t num_blocks, float scale,
+                                   pa_dtype dtype, void* out, float* weights,
+                                   const int32_t* rows, int32_t num_rows, int32_t width,
+                                   void* workspace, size_t ws_bytes, void* stream);
+
+/* Chooses, for each sequence i and KV head g, which of its n = context_lens[i] tokens
+ * stay: all of them if n <= keep; else the first `first`, the last `last` and, of those
+ * between, the ones with the largest weights[rows[i]][g][j] until there are `keep`,
+ * ties to the lower position (-0 equals 0; a NaN ranks below every number).
+ *   kept[i][g]    the chosen positions in ascending order, then -1
+ *   kept_lens[i]  min(n, keep): the same for every KV head
+ *   new_weights[rows[i]][g] the chosen tokens' weights in that order, then zeros to width
+ * A sequence that takes no part (see rows) gets kept_lens[i] = 0 and -1s.  A negative
+ * context counts as 0 and sets PA_DEVERR_CONTEXT, one longer than width is cut to it and
+ * sets PA_DEVERR_TABLE_WIDTH.
+ *   keep         >= first + last and >= 1; first, last >= 0
+ *   kept         (device) [B][Hkv][keep] int32;  kept_lens (device) [B] int32
+ *   new_weights  (device, nullable: not written) [num_rows][Hkv][width] fp32; may be
+ *                weights itself */
+PA_API pa_status pa_select_tokens(const float* weights, int32_t num_rows, int32_t width,
+                                  const int32_t* rows, const int32_t* context_lens, int32_t B,
+                                  int32_t Hkv, int32_t keep, int32_t first, int32_t last,
+                                  int32_t* kept, int32_t* kept_lens, float* new_weights,
+                                  void* stream);
+
+/* Moves the kept tokens of a 16-bit cache together: for each sequence i, KV head g and
+ * r < kept_lens[i], with p = kept[i][g][r],
+ *   K of (new_tables[i][r / bs], row r % bs, g) = K of (block_tables[i][p / bs], p % bs, g)
+ * as the cache was before the call, and the same for V; bit-exact.  A sequence's lists
+ * ascend strictly (p >= r then), as pa_select_tokens writes them.  A block of new_tables[i] is either
+ * the one at the same place of block_tables[i] (moved in place) or one that no block_tables
+ * row of the call holds; sequences that move in place do not share the blocks that they
+ * write (pa_alloc_evict sees to all of this).  Slots behind the kept tokens are left as
+ * they are.  A position whose block lies beyond its table or outside the pool, on either
+ * side, is not moved and sets PA_DEVERR_TABLE_WIDTH or PA_DEVERR_BLOCK_ID; a kept_lens
+ * outside [0, keep] is cut to it and sets PA_DEVERR_CONTEXT.
+ *   k_cache, v_cache (device) [num_blocks][block_size][Hkv][d], 16-byte aligned
+ *   kept         (device) [B][Hkv][keep] int32;  kept_lens (device) [B] int32
+ *   block_tables (device) [B][max_blocks] int32: the tables before the eviction
+ *   new_tables   (device) [B][new_max_blocks] int32: those after it (may be the same tensor) */
+PA_API pa_status pa_compact_tokens(void* k_cache, void* v_cache, const int32_t* kept,
+                                   int32_t keep, const int32_t* kept_lens,
+                                   const int32_t* block_tables, int32_t max_blocks,
+                                   const int32_t* new_tables, int32_t new_max_blocks, int32_t B,
+                                   int32_t Hkv, int32_t d, int32_t block_size,
+                                   int32_t num_blocks, pa_dtype dtype, void* stream);
 
 /* pa_decode without a caller-supplied workspace, for callers that cannot
  * allocate device memory: code running inside an allocator's own hooks, or in

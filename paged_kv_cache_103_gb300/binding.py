@@ -115,6 +115,26 @@ SIGNATURES = {
                                   _P]),
     "pa_decode_int4": (_ST, [_P, _P, _P, _P, _P, _P, _I32, _P, _I32, _I32, _I32, _I32, _I32, _I32,
                              _I32, _F32, _ST, _P, _P, _SZ, _P]),
+    "pa_reshape_and_cache_int8_block": (_ST, [_P, _P, _P, _I32, _P, _P, _P, _P, _I32, _I32, _I32,
+                                              _I32, _ST, _P]),
+    "pa_reshape_and_cache_fp8_block": (_ST, [_P, _P, _P, _I32, _P, _P, _P, _P, _I32, _I32, _I32,
+                                             _I32, _ST, _P]),
+    "pa_gather_cache_int8_block": (_ST, [_P, _P, _P, _P, _P, _I32, _P, _P, _I32, _I32, _I32, _I32,
+                                         _ST, _P]),
+    "pa_gather_cache_fp8_block": (_ST, [_P, _P, _P, _P, _P, _I32, _P, _P, _I32, _I32, _I32, _I32,
+                                        _ST, _P]),
+    "pa_decode_int8_block": (_ST, [_P, _P, _P, _P, _P, _P, _I32, _P, _I32, _I32, _I32, _I32, _I32,
+                                   _I32, _I32, _F32, _ST, _P, _P, _SZ, _P]),
+    "pa_decode_fp8_block": (_ST, [_P, _P, _P, _P, _P, _P, _I32, _P, _I32, _I32, _I32, _I32, _I32,
+                                  _I32, _I32, _F32, _ST, _P, _P, _SZ, _P]),
+    "pa_alloc_evict": (_ST, [_P, _I64, _I32]),
+    "pa_decode_weights_workspace_size": (_SZ, [_I32, _I32, _I32, _I32, _I64]),
+    "pa_decode_weights": (_ST, [_P, _P, _P, _P, _I32, _P, _I32, _I32, _I32, _I32, _I32, _I32, _I32,
+                                _F32, _ST, _P, _P, _P, _I32, _I32, _P, _SZ, _P]),
+    "pa_select_tokens": (_ST, [_P, _I32, _I32, _P, _P, _I32, _I32, _I32, _I32, _I32, _P, _P, _P,
+                               _P]),
+    "pa_compact_tokens": (_ST, [_P, _P, _P, _I32, _P, _P, _I32, _P, _I32, _I32, _I32, _I32, _I32,
+                                _I32, _ST, _P]),
     "pa_summarize_blocks": (_ST, [_P, _P, _P, _I32, _P, _P, _I32, _I32, _I32, _I32, _ST, _P]),
     "pa_select_blocks_workspace_size": (_SZ, [_I32, _I32, _I32]),
     "pa_select_blocks": (_ST, [_P, _P, _P, _P, _I32, _P, _I32, _I32, _I32, _I32, _I32, _I32, _I32,
@@ -546,6 +566,187 @@ def pa_decode_int4(q, k_cache, v_cache, k_scale, v_scale, block_tables, context_
         workspace.nbytes, st), "pa_decode_int4")
 
 
+def _block8_cache(k_cache, v_cache, k_scale, v_scale, Hkv: int, d: int):
+    """(num_blocks, block_size) of a block-scaled 8-bit cache whose four tensors fit each other."""
+    if k_cache.dim() != 4:
+        raise ValueError("block-scaled 8-bit caches are [num_blocks, Hkv, block_size, d]")
+    N, _, bs, _ = k_cache.shape
+    codes, scales = (N, Hkv, bs, d), (N, Hkv)
+    if (k_cache.shape != codes or v_cache.shape != codes or k_scale.shape != scales
+            or v_scale.shape != scales):
+        _misfit(k_cache=(k_cache, codes), v_cache=(v_cache, codes), k_scale=(k_scale, scales),
+                v_scale=(v_scale, scales))
+    return N, bs
+
+
+def _append_block8(name, k_new, v_new, slot_mapping, k_cache, v_cache, k_scale, v_scale, stream):
+    import torch
+    T, Hkv, d = k_new.shape
+    N, bs = _block8_cache(k_cache, v_cache, k_scale, v_scale, Hkv, d)
+    if v_new.shape != k_new.shape or slot_mapping.shape != (T,):
+        _misfit(v_new=(v_new, (T, Hkv, d)), slot_mapping=(slot_mapping, (T,)))
+    dev, st = _where(k_new, stream)
+    dt, u8, f32 = k_new.dtype, torch.uint8, torch.float32
+    _check(getattr(load(), name)(
+        _ptr(k_new, dt, dev), _ptr(v_new, dt, dev), _ptr(slot_mapping, torch.int64, dev), T,
+        _ptr(k_cache, u8, dev), _ptr(v_cache, u8, dev), _ptr(k_scale, f32, dev),
+        _ptr(v_scale, f32, dev), N, bs, Hkv, d, _dtype_code(k_new), st), name)
+
+
+def pa_reshape_and_cache_int8_block(k_new, v_new, slot_mapping, k_cache, v_cache, k_scale, v_scale,
+                                    stream=None) -> None:
+    """Quantising append into a block-scaled INT8 cache: ``k_new/v_new [T, Hkv, d]``
+    fp16/bf16, ``slot_mapping [T]`` int64 (distinct slots, the tokens of a block neighbours,
+    negative = padding), caches ``[N, Hkv, bs, d]`` uint8, scales ``[N, Hkv]`` float32.  A block
+    whose row 0 is written begins anew; else its scale grows with what is written, and its
+    other rows are coded again for the new scale."""
+    _append_block8("pa_reshape_and_cache_int8_block", k_new, v_new, slot_mapping, k_cache, v_cache,
+                   k_scale, v_scale, stream)
+
+
+def pa_reshape_and_cache_fp8_block(k_new, v_new, slot_mapping, k_cache, v_cache, k_scale, v_scale,
+                                   stream=None) -> None:
+    """``pa_reshape_and_cache_int8_block`` for a cache of E4M3 codes."""
+    _append_block8("pa_reshape_and_cache_fp8_block", k_new, v_new, slot_mapping, k_cache, v_cache,
+                   k_scale, v_scale, stream)
+
+
+def pa_gather_cache_int8_block(k_cache, v_cache, k_scale, v_scale, slot_mapping, k_out, v_out,
+                               stream=None) -> None:
+    """``pa_gather_cache_int4`` for a block-scaled INT8 cache (``[N, Hkv, bs, d]`` uint8
+    codes, ``[N, Hkv]`` float32 scales)."""
+    import torch
+    _, Hkv, d = k_out.shape
+    N, bs = _block8_cache(k_cache, v_cache, k_scale, v_scale, Hkv, d)
+    _gather("pa_gather_cache_int8_block", torch.float32, k_cache, v_cache, k_scale, v_scale,
+            slot_mapping, k_out, v_out, N, bs, stream)
+
+
+def pa_gather_cache_fp8_block(k_cache, v_cache, k_scale, v_scale, slot_mapping, k_out, v_out,
+                              stream=None) -> None:
+    """``pa_gather_cache_int8_block`` for a cache of E4M3 codes."""
+    import torch
+    _, Hkv, d = k_out.shape
+    N, bs = _block8_cache(k_cache, v_cache, k_scale, v_scale, Hkv, d)
+    _gather("pa_gather_cache_fp8_block", torch.float32, k_cache, v_cache, k_scale, v_scale,
+            slot_mapping, k_out, v_out, N, bs, stream)
+
+
+def _decode_block8(name, q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens,
+                   max_context_len, scale, out, workspace, stream):
+    import torch
+    B, H, d = q.shape
+    Hkv = k_cache.shape[1]
+    N, bs = _block8_cache(k_cache, v_cache, k_scale, v_scale, Hkv, d)
+    if (block_tables.dim() != 2 or block_tables.shape[0] != B or context_lens.shape != (B,)
+            or out.shape != q.shape):
+        _misfit(block_tables=(block_tables, (B, block_tables.shape[-1])),
+                context_lens=(context_lens, (B,)), out=(out, (B, H, d)))
+    dev, st = _where(q, stream)
+    dt, u8, f32, i32 = q.dtype, torch.uint8, torch.float32, torch.int32
+    _check(getattr(load(), name)(
+        _ptr(q, dt, dev), _ptr(k_cache, u8, dev), _ptr(v_cache, u8, dev), _ptr(k_scale, f32, dev),
+        _ptr(v_scale, f32, dev), _ptr(block_tables, i32, dev), block_tables.shape[1],
+        _ptr(context_lens, i32, dev), int(max_context_len), B, H, Hkv, d, bs, N, float(scale),
+        _dtype_code(q), _ptr(out, dt, dev), _ptr(workspace, workspace.dtype, dev),
+        workspace.nbytes, st), name)
+
+
+def pa_decode_int8_block(q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens,
+                         max_context_len: int, scale: float, out, workspace, stream=None) -> None:
+    """``pa_decode`` over a block-scaled INT8 cache (from ``pa_reshape_and_cache_int8_block``):
+    ``q/out [B, H, d]``, caches ``[N, Hkv, bs, d]`` uint8, scales ``[N, Hkv]`` float32."""
+    _decode_block8("pa_decode_int8_block", q, k_cache, v_cache, k_scale, v_scale, block_tables,
+                   context_lens, max_context_len, scale, out, workspace, stream)
+
+
+def pa_decode_fp8_block(q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens,
+                        max_context_len: int, scale: float, out, workspace, stream=None) -> None:
+    """``pa_decode_int8_block`` over a cache of E4M3 codes."""
+    _decode_block8("pa_decode_fp8_block", q, k_cache, v_cache, k_scale, v_scale, block_tables,
+                   context_lens, max_context_len, scale, out, workspace, stream)
+
+
+def pa_decode_weights_workspace_size(B: int, H: int, Hkv: int, d: int, tokens: int) -> int:
+    return int(load().pa_decode_weights_workspace_size(B, H, Hkv, d, tokens))
+
+
+def pa_decode_weights(q, k_cache, v_cache, block_tables, context_lens, max_context_len: int,
+                      scale: float, out, weights, rows, workspace, stream=None) -> None:
+    """``pa_decode`` that also adds each token's softmax weight, summed over the query heads of
+    its KV head, to ``weights[rows[i], g, position]``: ``weights [R, Hkv, W]`` float32,
+    ``rows [B]`` int32 (distinct; negative: not accumulated).  ``workspace``:
+    ``pa_decode_weights_workspace_size(B, H, Hkv, d, tokens)`` bytes, ``tokens`` the sum of
+    the context lengths or more."""
+    import torch
+    B, H, d = q.shape
+    N, bs, Hkv, _ = k_cache.shape
+    R, W = weights.shape[0], weights.shape[-1]
+    if (k_cache.shape != (N, bs, Hkv, d) or v_cache.shape != k_cache.shape
+            or block_tables.dim() != 2 or block_tables.shape[0] != B
+            or context_lens.shape != (B,) or out.shape != q.shape
+            or weights.shape != (R, Hkv, W) or rows.shape != (B,)):
+        _misfit(k_cache=(k_cache, (N, bs, Hkv, d)), v_cache=(v_cache, tuple(k_cache.shape)),
+                block_tables=(block_tables, (B, block_tables.shape[-1])),
+                context_lens=(context_lens, (B,)), out=(out, (B, H, d)),
+                weights=(weights, (R, Hkv, W)), rows=(rows, (B,)))
+    dev, st = _where(q, stream)
+    dt, i32 = q.dtype, torch.int32
+    _check(load().pa_decode_weights(
+        _ptr(q, dt, dev), _ptr(k_cache, dt, dev), _ptr(v_cache, dt, dev),
+        _ptr(block_tables, i32, dev), block_tables.shape[1], _ptr(context_lens, i32, dev),
+        int(max_context_len), B, H, Hkv, d, bs, N, float(scale), _dtype_code(q),
+        _ptr(out, dt, dev), _ptr(weights, torch.float32, dev), _ptr(rows, i32, dev), R, W,
+        _ptr(workspace, workspace.dtype, dev), workspace.nbytes, st), "pa_decode_weights")
+
+
+def pa_select_tokens(weights, rows, context_lens, first: int, last: int, kept, kept_lens,
+                     new_weights=None, stream=None) -> None:
+    """Chooses the tokens that stay: ``kept [B, Hkv, keep]`` (int32) receives, per (sequence,
+    KV head), the positions of the ``first``, the ``last`` and the heaviest tokens between, in
+    order, ``kept_lens [B]`` (int32) their number; ``new_weights`` (may be ``weights``) the
+    accumulators ``[R, Hkv, W]`` moved the same way."""
+    import torch
+    B, Hkv, keep = kept.shape
+    R, W = weights.shape[0], weights.shape[-1]
+    if (weights.shape != (R, Hkv, W) or rows.shape != (B,) or context_lens.shape != (B,)
+            or kept_lens.shape != (B,)
+            or (new_weights is not None and new_weights.shape != weights.shape)):
+        _misfit(weights=(weights, (R, Hkv, W)), rows=(rows, (B,)),
+                context_lens=(context_lens, (B,)), kept_lens=(kept_lens, (B,)),
+                **({} if new_weights is None else {"new_weights": (new_weights, (R, Hkv, W))}))
+    dev, st = _where(weights, stream)
+    i32, f32 = torch.int32, torch.float32
+    _check(load().pa_select_tokens(
+        _ptr(weights, f32, dev), R, W, _ptr(rows, i32, dev), _ptr(context_lens, i32, dev), B, Hkv,
+        keep, int(first), int(last), _ptr(kept, i32, dev), _ptr(kept_lens, i32, dev),
+        None if new_weights is None else _ptr(new_weights, f32, dev), st), "pa_select_tokens")
+
+
+def pa_compact_tokens(k_cache, v_cache, kept, kept_lens, block_tables, new_tables,
+                      stream=None) -> None:
+    """Moves the rows ``kept [B, Hkv, keep]`` of a 16-bit cache ``[N, bs, Hkv, d]`` from
+    where ``block_tables [B, max_blocks]`` has them to positions ``0 .. kept_lens[i] - 1`` of
+    ``new_tables [B, new_max_blocks]`` (int32; in place where both name the same block)."""
+    import torch
+    N, bs, Hkv, d = k_cache.shape
+    B, _, keep = kept.shape
+    if (v_cache.shape != k_cache.shape or kept.shape != (B, Hkv, keep) or kept_lens.shape != (B,)
+            or block_tables.dim() != 2 or block_tables.shape[0] != B or new_tables.dim() != 2
+            or new_tables.shape[0] != B):
+        _misfit(v_cache=(v_cache, (N, bs, Hkv, d)), kept=(kept, (B, Hkv, keep)),
+                kept_lens=(kept_lens, (B,)),
+                block_tables=(block_tables, (B, block_tables.shape[-1])),
+                new_tables=(new_tables, (B, new_tables.shape[-1])))
+    dev, st = _where(k_cache, stream)
+    dt, i32 = k_cache.dtype, torch.int32
+    _check(load().pa_compact_tokens(
+        _ptr(k_cache, dt, dev), _ptr(v_cache, dt, dev), _ptr(kept, i32, dev), keep,
+        _ptr(kept_lens, i32, dev), _ptr(block_tables, i32, dev), block_tables.shape[1],
+        _ptr(new_tables, i32, dev), new_tables.shape[1], B, Hkv, d, bs, N, _dtype_code(k_cache),
+        st), "pa_compact_tokens")
+
+
 def pa_summarize_blocks(k_cache, block_ids, boxes, box_scale, fills=None, stream=None) -> None:
     """Summarises blocks ``block_ids [n]`` (int32) of a 16-bit ``k_cache [N, bs, Hkv, d]``
     into ``boxes [N, Hkv, 2, d]`` int8 and ``box_scale [N, Hkv]`` float32; ``fills [n]``
@@ -775,6 +976,11 @@ class Allocator:
         s = PrefixStats()
         _check(self._lib.pa_prefix_stats_get(self._h, ctypes.byref(s)), "pa_prefix_stats_get")
         return {f: getattr(s, f) for f, _ in PrefixStats._fields_}
+
+    def evict(self, seq_id: int, num_tokens: int) -> None:
+        """Cuts the sequence to ``num_tokens`` tokens for an eviction: export its table before
+        (``block_tables`` of ``pa_compact_tokens``) and after (``new_tables``)."""
+        _check(self._lib.pa_alloc_evict(self._h, seq_id, num_tokens), "pa_alloc_evict")
 
     def fork(self, parent: int, child: int) -> None:
         _check(self._lib.pa_fork(self._h, parent, child), "pa_fork")

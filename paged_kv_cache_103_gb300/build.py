@@ -21,7 +21,7 @@ LIB = os.path.join(BUILD, "libpa.so")
 
 CUDA_SOURCES = ["pa_decode.cu", "pa_cache.cu", "pa_runtime.cu", "pa_noalloc.cu", "pa_multi_query.cu",
                 "pa_multi_query_tc.cu", "pa_step.cu", "pa_cache_int4.cu", "pa_decode_int4.cu",
-                "pa_select.cu"]
+                "pa_select.cu", "pa_cache_block8.cu", "pa_decode_block8.cu", "pa_evict.cu"]
 CXX_SOURCES = ["pa_allocator.cpp"]
 HEADERS = ["pa_common.cuh", "pa_device_once.h"]
 

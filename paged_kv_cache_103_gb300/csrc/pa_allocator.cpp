@@ -400,6 +400,34 @@ PA_API pa_status pa_prefix_stats_get(const pa_allocator* a, pa_prefix_stats* out
     return PA_OK;
 }
 
+PA_API pa_status pa_alloc_evict(pa_allocator* a, int64_t seq_id, int32_t num_tokens) {
+    if (!a || num_tokens < 0) return PA_ERR_INVALID;
+    auto it = a->seqs.find(seq_id);
+    if (it == a->seqs.end()) return PA_ERR_NOT_FOUND;
+    Sequence& s = it->second;
+    if (s.swapped || num_tokens > s.length) return PA_ERR_INVALID;
+    if (num_tokens == s.length) return PA_OK;
+    const size_t stay = (size_t)(((int64_t)num_tokens + a->block_size - 1) / a->block_size);
+    int32_t need = 0;
+    for (size_t j = 0; j < stay; ++j) need += a->ref[s.table[j]] > 1;
+    if (need > a->nfree) return PA_ERR_OOM;
+    for (size_t j = 0; j < stay; ++j) {
+        int32_t& b = s.table[j];
+        if (a->ref[b] > 1) {
+            a->ref[b] -= 1;
+            b = a->take_front();
+        } else {
+            a->evict(b);   // its content will no longer be the prefix's
+        }
+    }
+    for (size_t j = stay; j < s.table.size(); ++j)
+        if (--a->ref[s.table[j]] == 0) a->free_push_back(s.table[j]);
+    s.table.resize(stay);
+    s.length = num_tokens;
+    pa_allocator::untrack(s);
+    return PA_OK;
+}
+
 PA_API pa_status pa_fork(pa_allocator* a, int64_t parent, int64_t child) {
     if (!a) return PA_ERR_INVALID;
     auto p = a->seqs.find(parent);

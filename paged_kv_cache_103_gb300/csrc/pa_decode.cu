@@ -107,6 +107,12 @@ struct DecodeParams {
     int32_t len_hint;   // the caller's max_context_len: a guess of every context's length
     int32_t pair_heads; // kPair: the cache's KV heads (pair i reads KV head i mod pair_heads)
     float scale_log2;
+    // kScores: the logits of the call's chunks [chunk][G][kChunk] (as many chunks as score_chunks
+    // at most), the softmax's maximum and inverse sum of each query head [B * Hkv][G][2], and the
+    // list's prefix [B + 1].
+    float *scores, *stats;
+    int32_t* prefix_out;
+    int64_t score_chunks;
 };
 
 // Dynamic shared-memory carve-up; the same function runs on host and device.
@@ -230,7 +236,11 @@ __device__ __forceinline__ void q8x4_to_f16(uint32_t x, uint32_t& lo, uint32_t& 
 // a length of its own.  The kernel sees the pairs as sequences of one KV head
 // each (B Hkv of them, H / Hkv query heads); only the cache's KV head, i mod
 // the real Hkv, differs.
-template <int D, bool kBF16, int NT, bool kAsync, bool kFp8, bool kInt8, bool kPair>
+// kScores (pa_decode_weights): the base-2 logits go to memory as well, and with each query head's
+// maximum and sum add_weights_kernel makes them weights: a probability is known only when its
+// row's sum is.  Written once and read once, mostly in L2, they are 4 G bytes a (token, KV head)
+// beside the 4 d of K and V, where another pass over K would be 2 d.
+template <int D, bool kBF16, int NT, bool kAsync, bool kFp8, bool kInt8, bool kPair, bool kScores>
 __global__ void __launch_bounds__(cta_threads(kFp8), kCtasPerSm)
 paged_decode_kernel(const __grid_constant__ CUtensorMap kmap,
                     const __grid_constant__ CUtensorMap vmap,
@@ -364,6 +374,12 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap kmap,
     }
 
     const int64_t W = prefix[B];
+    if constexpr (kScores) {
+        if (blockIdx.x == 0) {
+            for (int32_t i = tid; i <= B; i += kThreads) p.prefix_out[i] = prefix[i];
+            if (tid == 0 && W > p.score_chunks) pa::raise_error(p.err, PA_DEVERR_CONTEXT);
+        }
+    }
     // CTAs in use: every one gets at least kMinChunksPerCta chunks, so short
     // batches are not cut into more partials than their size pays for.
     int64_t C = W / kMinChunksPerCta;
@@ -618,9 +634,16 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap kmap,
             packed.y = pa::pack2<kBF16>(v.z, v.w);
             *reinterpret_cast<uint2*>(p.out + ((int64_t)sg.i * p.H + h0 + r) * D + d4) = packed;
         };
+        auto store_stats = [&](int r, float M, float inv) {
+            float* to = p.stats + (((int64_t)sg.i * Hkv + sg.g) * G + r) * 2;
+            to[0] = M;
+            to[1] = inv;
+        };
         if (whole) {
             for (int e = t; e < G * D / 4; e += nthr)
                 store4(e / (D / 4), (e % (D / 4)) * 4, combined4(e));
+            if constexpr (kScores)
+                if (t < G) store_stats(t, rinfo[t], 1.f / rinfo[kMaxG + t]);
             return;
         }
         // Partial result of this CTA for a pair split between CTAs.
@@ -700,6 +723,8 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap kmap,
             }
             const float inv = 1.f / Ls;
             store4(r, d4, make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
+            if constexpr (kScores)
+                if (d4 == 0) store_stats(r, M, inv);
         }
     };
 
@@ -876,6 +901,20 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap kmap,
                             mx[nt][e & 1] = fmaxf(mx[nt][e & 1], x);
                         }
                 }
+                if constexpr (kScores) {
+                    if (W <= p.score_chunks) {
+                        float* to = p.scores + (int64_t)(s.a + s.c0 + t) * G * kChunk;
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                            for (int mt = 0; mt < kKeyTiles; ++mt)
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) {
+                                    const int h = 8 * nt + cc + (e & 1);
+                                    if (h < G) to[h * kChunk + mt * 16 + cr + 8 * (e >> 1)] = st[mt][nt][e];
+                                }
+                    }
+                }
                 bool grew = false;
                 float alpha[NT][2];
 #pragma unroll
@@ -914,7 +953,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap kmap,
                 // cancel stays within the tolerance.  An f16 P keeps 11 (f16 and FP8 caches);
                 // over chosen blocks, few keys as a rule, it has its residual too: without it
                 // an f16 result was off 1.2 times as far as an fp32 computation's.
-                constexpr bool kPbf16 = kBF16 && !kFp8, kTwoParts = kPbf16 || kPair;
+                constexpr bool kPbf16 = kBF16 && !kFp8, kTwoParts = kPbf16 || kPair || kScores;
                 uint32_t pb[kKeyTiles][NT][2];
                 uint32_t pbl[kKeyTiles][NT][2];
 #pragma unroll
@@ -1240,11 +1279,11 @@ int choose_stages(int D, int G, int B, bool fp8, int bs) {
     return s;
 }
 
-template <int D, bool kBF16, int NT, bool kAsync, bool kFp8, bool kInt8, bool kPair>
+template <int D, bool kBF16, int NT, bool kAsync, bool kFp8, bool kInt8, bool kPair, bool kScores>
 pa_status launch(const CUtensorMap& km, const CUtensorMap& vm, const CUtensorMap& ksm,
                  const CUtensorMap& vsm, const DecodeParams& prm, size_t smem,
                  cudaStream_t stream) {
-    auto kern = paged_decode_kernel<D, kBF16, NT, kAsync, kFp8, kInt8, kPair>;
+    auto kern = paged_decode_kernel<D, kBF16, NT, kAsync, kFp8, kInt8, kPair, kScores>;
     static pa::DeviceOnce once;
     if (!pa::allow_smem(once, kern, kSmemBudget)) return PA_ERR_CUDA;
     // The 8-bit register split adds up only against this launch allocation: a
@@ -1275,15 +1314,15 @@ pa_status launch(const CUtensorMap& km, const CUtensorMap& vm, const CUtensorMap
     }
 }
 
-template <int D, bool kBF16, bool kFp8, bool kInt8 = false, bool kPair = false>
+template <int D, bool kBF16, bool kFp8, bool kInt8 = false, bool kPair = false, bool kScores = false>
 pa_status launch_g(const CUtensorMap& km, const CUtensorMap& vm, const CUtensorMap& ksm,
                    const CUtensorMap& vsm, const DecodeParams& prm, size_t smem,
                    cudaStream_t stream) {
     if (async_merge(prm.G))
-        return launch<D, kBF16, 1, true, kFp8, kInt8, kPair>(km, vm, ksm, vsm, prm, smem, stream);
+        return launch<D, kBF16, 1, true, kFp8, kInt8, kPair, kScores>(km, vm, ksm, vsm, prm, smem, stream);
     return prm.G <= 8
-               ? launch<D, kBF16, 1, false, kFp8, kInt8, kPair>(km, vm, ksm, vsm, prm, smem, stream)
-               : launch<D, kBF16, 2, false, kFp8, kInt8, kPair>(km, vm, ksm, vsm, prm, smem, stream);
+               ? launch<D, kBF16, 1, false, kFp8, kInt8, kPair, kScores>(km, vm, ksm, vsm, prm, smem, stream)
+               : launch<D, kBF16, 2, false, kFp8, kInt8, kPair, kScores>(km, vm, ksm, vsm, prm, smem, stream);
 }
 
 // Checks shared by pa_decode and pa_decode_fp8; fills everything of prm but the
@@ -1523,6 +1562,151 @@ PA_API pa_status pa_decode_selected(const void* q, const void* k_cache, const vo
     return dtype == PA_BF16
                ? launch_g<64, true, false, false, true>(km, vm, km, vm, prm, smem, st)
                : launch_g<64, false, false, false, true>(km, vm, km, vm, prm, smem, st);
+}
+
+}  // extern "C"
+
+namespace {
+
+// ---- pa_decode_weights: from logits to weights ----------------------------------------
+struct WeightsParams {
+    const float *scores, *stats;
+    const int32_t *prefix, *context_lens, *rows;
+    float* weights;
+    unsigned int* err;
+    int64_t score_chunks;
+    int32_t B, Hkv, G, subs, num_rows, width;   // Hkv: the cache's
+};
+
+constexpr int kAddThreads = 256;
+
+// weights[row][g][j] += sum over the query heads h of g of 2^(s_hj - M_h) / L_h: a warp per
+// (sequence, KV head, chunk), a lane per token.  The heads are added in order, no two warps
+// touch the same weight.
+__global__ void __launch_bounds__(kAddThreads) add_weights_kernel(const WeightsParams p) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");   // launched while the decode may run
+    const int lane = threadIdx.x & 31;
+    if (blockIdx.x == 0)
+        for (int32_t i = threadIdx.x; i < p.B; i += kAddThreads) {
+            const int32_t row = pa::ld_behind_wait(p.rows + i);
+            if (row >= p.num_rows) pa::raise_error(p.err, PA_DEVERR_SLOT);
+            if (row >= 0 && row < p.num_rows && pa::ld_behind_wait(p.context_lens + i) > p.width)
+                pa::raise_error(p.err, PA_DEVERR_TABLE_WIDTH);
+        }
+    const int32_t W = pa::ld_behind_wait(p.prefix + p.B);
+    if (W > p.score_chunks) return;
+    const int32_t units = W / p.subs, warps = gridDim.x * (kAddThreads / 32);
+    for (int32_t u = blockIdx.x * (kAddThreads / 32) + (threadIdx.x >> 5); u < units; u += warps) {
+        int32_t lo = 0, hi = p.B;   // largest i with prefix[i] / subs <= u
+        while (hi - lo > 1) {
+            const int32_t mid = (lo + hi) >> 1;
+            if (pa::ld_behind_wait(p.prefix + mid) / p.subs <= u) lo = mid; else hi = mid;
+        }
+        const int32_t a = pa::ld_behind_wait(p.prefix + lo);
+        const int32_t nc = (pa::ld_behind_wait(p.prefix + lo + 1) - a) / (p.Hkv * p.subs);
+        const int32_t local = u - a / p.subs, g = local / nc, c = local - g * nc;
+        const int32_t row = pa::ld_behind_wait(p.rows + lo), j = c * kChunk + lane;
+        if (row < 0 || row >= p.num_rows) continue;
+        if (j >= min(pa::ld_behind_wait(p.context_lens + lo), p.width)) continue;
+        float sum = 0.f;
+        for (int32_t x = 0; x < p.subs; ++x) {
+            const float* s = p.scores + ((int64_t)a + (g * p.subs + x) * nc + c) * p.G * kChunk + lane;
+            const float* st = p.stats + ((int64_t)lo * p.Hkv * p.subs + g * p.subs + x) * p.G * 2;
+            for (int32_t h = 0; h < p.G; ++h)
+                sum += pa::fast_exp2(pa::ld_behind_wait(s + h * kChunk) - pa::ld_behind_wait(st + 2 * h)) *
+                       pa::ld_behind_wait(st + 2 * h + 1);
+        }
+        p.weights[((int64_t)row * p.Hkv + g) * p.width + j] += sum;
+    }
+}
+
+// A workspace of pa_decode_weights: pa_decode's, then stats, prefix, logits.
+size_t stats_bytes(int32_t B, int32_t H) { return ((size_t)B * H * 8 + 255) & ~size_t(255); }
+size_t prefix_bytes(int32_t B) { return (((size_t)B + 1) * 4 + 255) & ~size_t(255); }
+
+}  // namespace
+
+extern "C" {
+
+PA_API size_t pa_decode_weights_workspace_size(int32_t B, int32_t H, int32_t Hkv, int32_t d,
+                                               int64_t tokens) {
+    const size_t base = pa_decode_workspace_size(B, H, d);
+    if (!base || Hkv <= 0 || H % Hkv != 0 || tokens < 0 || tokens > ((int64_t)1 << 40)) return 0;
+    // a sequence's chunks hold fewer than kChunk tokens beside its own
+    return base + stats_bytes(B, H) + prefix_bytes(B) + ((size_t)tokens + (size_t)B * kChunk) * H * 4;
+}
+
+PA_API pa_status pa_decode_weights(const void* q, const void* k_cache, const void* v_cache,
+                                   const int32_t* block_tables, int32_t max_blocks,
+                                   const int32_t* context_lens, int32_t max_context_len,
+                                   int32_t B, int32_t H, int32_t Hkv, int32_t d,
+                                   int32_t block_size, int32_t num_blocks, float scale,
+                                   pa_dtype dtype, void* out, float* weights,
+                                   const int32_t* rows, int32_t num_rows, int32_t width,
+                                   void* workspace, size_t ws_bytes, void* stream) {
+    if (num_rows <= 0 || width <= 0) return PA_ERR_INVALID;
+    DecodeParams prm;
+    size_t smem = 0;
+    const pa_status st0 = prepare(max_blocks, max_context_len, B, H, Hkv, d, block_size,
+                                  num_blocks, scale, dtype, ws_bytes, false, &prm, &smem);
+    if (st0 != PA_OK || B == 0) return st0;
+    if (ws_bytes < pa_decode_weights_workspace_size(B, H, Hkv, d, 0)) return PA_ERR_INVALID;
+    if (!q || !k_cache || !v_cache || !block_tables || !context_lens || !out || !weights || !rows ||
+        !workspace)
+        return PA_ERR_INVALID;
+    if ((reinterpret_cast<uintptr_t>(k_cache) | reinterpret_cast<uintptr_t>(v_cache) |
+         reinterpret_cast<uintptr_t>(out) | reinterpret_cast<uintptr_t>(workspace)) & 15u)
+        return PA_ERR_INVALID;
+    if ((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(weights) |
+         reinterpret_cast<uintptr_t>(rows)) & 3u)
+        return PA_ERR_INVALID;
+
+    unsigned int* err = pa::device_error_word();
+    if (!err || pa_decode_grid_size() <= 0) return PA_ERR_CUDA;
+
+    CUtensorMap km, vm;
+    const int32_t pool_rows = num_blocks * block_size;
+    if (!encode_cache_map(&km, k_cache, pool_rows, Hkv, d, block_size, dtype) ||
+        !encode_cache_map(&vm, v_cache, pool_rows, Hkv, d, block_size, dtype))
+        return PA_ERR_CUDA;
+
+    unsigned char* ws = static_cast<unsigned char*>(workspace);
+    const size_t base = pa_decode_workspace_size(B, H, d);
+    const size_t fixed = base + stats_bytes(B, H) + prefix_bytes(B);
+    prm.q = static_cast<const uint16_t*>(q);
+    prm.out = static_cast<uint16_t*>(out);
+    prm.block_tables = block_tables;
+    prm.context_lens = context_lens;
+    prm.counters = reinterpret_cast<int32_t*>(ws);
+    prm.partials = reinterpret_cast<float*>(ws + counters_bytes(B, H));
+    prm.err = err;
+    prm.stats = reinterpret_cast<float*>(ws + base);
+    prm.prefix_out = reinterpret_cast<int32_t*>(ws + base + stats_bytes(B, H));
+    prm.scores = reinterpret_cast<float*>(ws + fixed);
+    prm.score_chunks = (int64_t)((ws_bytes - fixed) / ((size_t)prm.G * kChunk * 4));
+
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const pa_status done =
+        d == 128 ? (dtype == PA_BF16
+                        ? launch_g<128, true, false, false, false, true>(km, vm, km, vm, prm, smem, st)
+                        : launch_g<128, false, false, false, false, true>(km, vm, km, vm, prm, smem, st))
+                 : (dtype == PA_BF16
+                        ? launch_g<64, true, false, false, false, true>(km, vm, km, vm, prm, smem, st)
+                        : launch_g<64, false, false, false, false, true>(km, vm, km, vm, prm, smem, st));
+    if (done != PA_OK) return done;
+    WeightsParams wp{prm.scores, prm.stats, prm.prefix_out, context_lens, rows, weights, err,
+                     prm.score_chunks, B, Hkv, prm.G, prm.subs, num_rows, width};
+    // Started early, so that its launch hides behind the decode's end.
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)(8 * pa::device_sm_count()));
+    cfg.blockDim = dim3(kAddThreads);
+    cfg.stream = st;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return pa::cuda_status(cudaLaunchKernelEx(&cfg, add_weights_kernel, wp));
 }
 
 }  // extern "C"
