@@ -21,9 +21,10 @@ LIB = os.path.join(BUILD, "libpa.so")
 
 CUDA_SOURCES = ["pa_decode.cu", "pa_cache.cu", "pa_runtime.cu", "pa_noalloc.cu", "pa_multi_query.cu",
                 "pa_multi_query_tc.cu", "pa_step.cu", "pa_cache_int4.cu", "pa_decode_int4.cu",
-                "pa_select.cu", "pa_cache_block8.cu", "pa_decode_block8.cu", "pa_evict.cu"]
+                "pa_select.cu", "pa_cache_block8.cu", "pa_decode_int8_block.cu",
+                "pa_decode_fp8_block.cu", "pa_evict.cu"]
 CXX_SOURCES = ["pa_allocator.cpp"]
-HEADERS = ["pa_common.cuh", "pa_device_once.h"]
+HEADERS = ["pa_common.cuh", "pa_device_once.h", "pa_runs.cuh", "pa_decode_block8.cuh"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
