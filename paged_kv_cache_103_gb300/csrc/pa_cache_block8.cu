@@ -1,5 +1,5 @@
-// The block-scaled 8-bit KV cache's append (pa_reshape_and_cache_int8_block / _fp8_block)
-// and its read back (pa_gather_cache_int8_block / _fp8_block).
+// The block-scaled 8-bit KV cache's append (pa_reshape_and_cache_int8_block / _fp8_block).
+// Its read back is with those of the other quantised caches (pa_cache_int4.cu).
 //
 // Format ("LLM推理优化技术地图：从KV Cache到量化与投机解码", section 4.3, KV cache
 // quantisation; the page fixes none).  A code is an INT8 integer or an E4M3 number and
@@ -59,186 +59,256 @@ __device__ __forceinline__ float4 number4(uint32_t codes) {
     return make_float4(a.x, a.y, b.x, b.y);
 }
 
-constexpr int kThreads = 128;
-constexpr int kVec = 4;      // values a lane takes at a time
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr int kVec = 4;      // values of a lane
+constexpr int kWindow = 8;   // tokens of a CTA
 
-// A warp per (token, KV head, K or V).  The first token of a block in the call has the block's
-// work; the other tokens' warps leave it to that one.
-template <bool kBF16, bool kInt8, int D>
-__global__ void __launch_bounds__(kThreads)
-append_kernel(const uint2* __restrict__ k_new, const uint2* __restrict__ v_new,
-              const int64_t* __restrict__ slots, int32_t T, int32_t Hkv, int bs_shift,
-              uint32_t* k_cache, uint32_t* v_cache, float* k_scale, float* v_scale,
-              int64_t num_slots, unsigned int* err) {
-    constexpr int kRow = D / kVec;       // lanes' places of a row
-    constexpr float kTop = kInt8 ? 127.f : 448.f;
-    const int lane = threadIdx.x & 31;
-    const int64_t w = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
-    const int32_t t = (int32_t)(w / (2 * Hkv)), hv = (int32_t)(w - (int64_t)t * 2 * Hkv);
-    if (t >= T) return;
-    const int32_t h = hv >> 1;
-    const int64_t slot = slots[t];
-    if (slot < 0) return;
-    if (slot >= num_slots) {
-        if (hv == 0 && lane == 0) pa::raise_error(err, PA_DEVERR_SLOT);
-        return;
-    }
-    const int64_t block = slot >> bs_shift;
-    // Is there an earlier token of this block?  The nearest one that is written tells.
-    for (int32_t j = t - 1 - lane, first = t - 1; first >= 0; first -= 32, j -= 32) {
-        const int64_t s = j >= 0 ? slots[j] : -1;
-        const uint32_t some = __ballot_sync(0xffffffffu, s >= 0 && s < num_slots);
-        if (!some) continue;
-        if (__shfl_sync(0xffffffffu, s, __ffs(some) - 1) >> bs_shift == block) return;
-        break;
-    }
-    const uint2* x = hv & 1 ? v_new : k_new;
-    uint32_t* cache = (hv & 1 ? v_cache : k_cache) + ((block * Hkv + h) << bs_shift) * kRow;
-    float* scale = (hv & 1 ? v_scale : k_scale) + block * Hkv + h;
-    // f(row of the block, token) for each token of the block
-    auto each = [&](auto f) {
-        for (int32_t first = t; first < T; first += 32) {
-            const int64_t s = first + lane < T ? slots[first + lane] : -1;
-            const uint32_t some = __ballot_sync(0xffffffffu, s >= 0 && s < num_slots);
-            const uint32_t same = __ballot_sync(0xffffffffu, s >= 0 && s >> bs_shift == block);
-            const uint32_t other = some & ~same;
-            const uint32_t mine = other ? same & ((other & -other) - 1) : same;
-            for (uint32_t m = mine; m; m &= m - 1) {
-                const int l = __ffs(m) - 1;
-                f((int32_t)(__shfl_sync(0xffffffffu, s, l) & ((1 << bs_shift) - 1)), first + l);
-            }
-            if (other) break;
-        }
-    };
-    float a = 0.f;
-    uint32_t written = 0;
-    each([&](int32_t r, int32_t j) {
-        written |= 1u << r;
-        for (int l = lane; l < kRow; l += 32) {
-            const uint2 y = x[((int64_t)j * Hkv + h) * kRow + l];
-            const float2 p = widen2<kBF16>(y.x), q = widen2<kBF16>(y.y);
-            a = fmaxf(a, fmaxf(fmaxf(fabsf(p.x), fabsf(p.y)), fmaxf(fabsf(q.x), fabsf(q.y))));
-        }
-    });
-    a = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(a)));
-    const float base = written & 1 ? 0.f : *scale;
-    const float s = fmaxf(base, __fdiv_rn(a, kTop));
-    if (base > 0.f && base < s) {
-        const float ratio = __fdiv_rn(base, s);
-        for (int r = 0; r < 1 << bs_shift; ++r) {
-            if (written >> r & 1) continue;
-            for (int l = lane; l < kRow; l += 32) {
-                const float4 c = number4<kInt8>(cache[r * kRow + l]);
-                cache[r * kRow + l] = code4<kInt8>(__fmul_rn(c.x, ratio), __fmul_rn(c.y, ratio),
-                                                   __fmul_rn(c.z, ratio), __fmul_rn(c.w, ratio));
-            }
+// x / s for one s, correctly rounded without a division each: with y = 1 / s correctly rounded and q
+// = x y, q + (x - q s) y rounds to the quotient (Markstein, IBM J. Res. Dev. 34, 1990), unless
+// s's fraction is all ones or x - q s loses bits below the smallest float, which a quotient
+// of 2^-11 or more (smaller ones are codes of 0 either way) does not for s >= 2^-90.
+struct Divider {
+    float s, y;
+    bool fast;
+    __device__ explicit Divider(float s_) : s(s_), y(0.f), fast(false) {
+        if (s > 0.f) {
+            fast = s >= 8.0779356694631609e-28f && (__float_as_uint(s) & 0x7FFFFFu) != 0x7FFFFFu;   // 2^-90
+            if (fast) y = __frcp_rn(s);
         }
     }
-    each([&](int32_t r, int32_t j) {
-        for (int l = lane; l < kRow; l += 32) {
-            const uint2 y = x[((int64_t)j * Hkv + h) * kRow + l];
-            const float2 p = widen2<kBF16>(y.x), q = widen2<kBF16>(y.y);
-            cache[r * kRow + l] = s > 0.f ? code4<kInt8>(__fdiv_rn(p.x, s), __fdiv_rn(p.y, s),
-                                                         __fdiv_rn(q.x, s), __fdiv_rn(q.y, s))
-                                          : 0u;
-        }
-    });
-    __syncwarp();
-    if (lane == 0) *scale = s;
+    __device__ __forceinline__ float operator()(float x) const {
+        const float q = __fmul_rn(x, y);
+        return __fmaf_rn(__fmaf_rn(-q, s, x), y, q);
+    }
+};
+
+// Quotients of a row's values and their codes.  |x| <= TOP s (1 + 2^-24): INT8 codes need
+// no clamp where the quotient is not that of a scale below the smallest normal float.
+template <bool kBF16, bool kInt8>
+__device__ __forceinline__ uint32_t row_codes(uint2 w, const Divider& by) {
+    const float2 p = widen2<kBF16>(w.x), q = widen2<kBF16>(w.y);
+    if (!by.fast) {
+        if (!(by.s > 0.f)) return 0u;
+        return code4<kInt8>(__fdiv_rn(p.x, by.s), __fdiv_rn(p.y, by.s), __fdiv_rn(q.x, by.s), __fdiv_rn(q.y, by.s));
+    }
+    if constexpr (kInt8) {
+        // 1.5 2^23 more, an fp32 number's low byte is the nearest integer's (ties to even)
+        constexpr float kRound = 12582912.f;
+        auto one = [&](float x) { return __float_as_uint(__fadd_rn(by(x), kRound)); };
+        const uint32_t lo = __byte_perm(one(p.x), one(p.y), 0x0040), hi = __byte_perm(one(q.x), one(q.y), 0x0040);
+        return __byte_perm(lo, hi, 0x5410);
+    } else {
+        return code4<false>(by(p.x), by(p.y), by(q.x), by(q.y));
+    }
 }
 
-// A thread per four values of k_out and of v_out.
-template <bool kBF16, bool kInt8, int D>
-__global__ void __launch_bounds__(kThreads)
-gather_kernel(const uint32_t* k_cache, const uint32_t* v_cache, const float* k_scale,
-              const float* v_scale, const int64_t* slots, int64_t vecs, int32_t Hkv, int bs_shift,
-              int64_t num_slots, uint2* k_out, uint2* v_out, unsigned int* err) {
-    constexpr int kRow = D / kVec;
-    const int64_t v = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-    if (v >= vecs) return;
-    const int64_t row = v / kRow, l = v % kRow, t = row / Hkv, h = row - t * Hkv;
-    const int64_t slot = slots[t];
-    if (slot < 0) return;
-    if (slot >= num_slots) {
-        if (h == 0 && l == 0) pa::raise_error(err, PA_DEVERR_SLOT);
-        return;
-    }
-    const int64_t tile = (slot >> bs_shift) * Hkv + h;
-    const int64_t at = ((tile << bs_shift) + (slot & ((1 << bs_shift) - 1))) * kRow + l;
-    auto one = [&](const uint32_t* cache, const float* scale, uint2* out) {
-        const float4 c = number4<kInt8>(cache[at]);
-        const float s = scale[tile];
-        out[v] = make_uint2(pa::pack2<kBF16>(__fmul_rn(c.x, s), __fmul_rn(c.y, s)),
-                            pa::pack2<kBF16>(__fmul_rn(c.z, s), __fmul_rn(c.w, s)));
+struct AppendParams {
+    const uint2 *k_new, *v_new;
+    const int64_t* slots;
+    uint32_t *k_cache, *v_cache;
+    float *k_scale, *v_scale;
+    unsigned int* err;
+    int64_t num_slots;
+    int32_t T, Hkv, groups, per;   // a CTA takes `per` of the 2 Hkv (KV head, K or V) tiles, one of `groups`
+};
+
+// A CTA has kWindow tokens and some (KV head, K or V) pairs.  A token that is the first of its
+// block in the call leads the block's tokens, wherever they end; each (leader, pair) is a
+// warp's: a tile of at most kRows rows, read once into registers, 8 bytes a lane.
+template <bool kBF16, bool kInt8, int D, int kShift>
+__global__ void __launch_bounds__(kThreads) append_kernel(const AppendParams p) {
+    constexpr int kLanes = D / kVec, kPer = 32 / kLanes;   // lanes of a row, rows of an instruction
+    constexpr int kRows = 1 << kShift, kSteps = kRows / kPer;
+    constexpr float kTop = kInt8 ? 127.f : 448.f;
+    asm volatile("griddepcontrol.launch_dependents;");   // what reads the cache may be launched: it waits
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, l = lane % kLanes, sub = lane / kLanes;
+    const int32_t window = blockIdx.x / p.groups, group = blockIdx.x - window * p.groups;
+    const int32_t t0 = window * kWindow, T = p.T;
+    auto slot_at = [&](int32_t t) {   // -1: padding, or outside the pool
+        const int64_t s = t >= 0 && t < T ? __ldg(p.slots + t) : -1;
+        return s < p.num_slots ? s : -1;
     };
-    one(k_cache, k_scale, k_out);
-    one(v_cache, v_scale, v_out);
+    // ---- leaders: the nearest written token before has another block
+    const int64_t mine = lane < kWindow ? slot_at(t0 + lane) : -1;
+    const int64_t before = slot_at(t0 - 32 + lane);
+    if (group == 0 && warp == 0 && lane < kWindow && t0 + lane < T && __ldg(p.slots + t0 + lane) >= p.num_slots)
+        pa::raise_error(p.err, PA_DEVERR_SLOT);
+    const uint32_t live = __ballot_sync(0xffffffffu, mine >= 0);
+    if (!live) return;
+    uint32_t some = __ballot_sync(0xffffffffu, before >= 0);
+    int64_t last = some ? __shfl_sync(0xffffffffu, before, 31 - __clz(some)) : -1;
+    for (int32_t first = t0 - 64; !some && first > -32; first -= 32) {   // padding: further back
+        const int64_t s = slot_at(first + lane);
+        some = __ballot_sync(0xffffffffu, s >= 0);
+        if (some) last = __shfl_sync(0xffffffffu, s, 31 - __clz(some));
+    }
+    const uint32_t lower = live & ((1u << lane) - 1);
+    const int64_t prev = __shfl_sync(0xffffffffu, mine, lower ? 31 - __clz(lower) : 0);
+    const int64_t prev_block = (lower ? prev : last) >> kShift;   // -1: none
+    const uint32_t leaders = __ballot_sync(0xffffffffu, mine >= 0 && prev_block != mine >> kShift);
+    const int32_t hv0 = group * p.per, tiles = min(p.per, 2 * p.Hkv - hv0);
+    const int items = __popc(leaders) * tiles;
+#pragma unroll 1
+    for (int it = warp; it < items; it += kWarps) {
+        const int lead = it / tiles;
+        const int32_t hv = hv0 + it - lead * tiles, h = hv >> 1;
+        uint32_t m = leaders;
+        for (int x = 0; x < lead; ++x) m &= m - 1;
+        const int32_t t = t0 + __ffs(m) - 1;
+        const int64_t block = __shfl_sync(0xffffffffu, mine, __ffs(m) - 1) >> kShift;
+        const uint2* x = (hv & 1 ? p.v_new : p.k_new) + l;
+        uint32_t* cache = (hv & 1 ? p.v_cache : p.k_cache) + ((block * p.Hkv + h) << kShift) * kLanes + l;
+        float* scale = (hv & 1 ? p.v_scale : p.k_scale) + block * p.Hkv + h;
+        const float was = *scale;
+        // ---- the block's tokens among 32 from the leader on
+        const int64_t s = slot_at(t + lane);
+        const uint32_t any = __ballot_sync(0xffffffffu, s >= 0);
+        const uint32_t same = __ballot_sync(0xffffffffu, s >= 0 && s >> kShift == block);
+        const uint32_t other = any & ~same;
+        uint32_t run = other ? same & ((other & -other) - 1) : same;
+        const int32_t r_lane = (int32_t)(s & (kRows - 1));
+        if (other || t + 32 >= T || __popc(run) >= kRows) {
+            // These are all of them.  (A slot named twice would make more: those are left out.)
+            uint2 w[kSteps];
+            uint32_t written = __reduce_or_sync(0xffffffffu, run >> lane & 1 ? 1u << r_lane : 0u);
+            uint32_t todo = run, top2 = 0;
+#pragma unroll
+            for (int q = 0; q < kSteps; ++q) {
+                const int a = __ffs(todo) - 1;
+                todo &= todo - 1;
+                int from = a;
+                if constexpr (kPer == 2) {
+                    const int b = __ffs(todo) - 1;
+                    todo &= todo - 1;
+                    from = sub ? b : a;
+                }
+                w[q] = make_uint2(0, 0);
+                if (from >= 0) w[q] = __ldg(x + ((int64_t)(t + from) * p.Hkv + h) * kLanes);
+            }
+#pragma unroll
+            for (int q = 0; q < kSteps; ++q) {
+                top2 = pa::max_x2<kBF16>(top2, w[q].x & 0x7FFF7FFFu);
+                top2 = pa::max_x2<kBF16>(top2, w[q].y & 0x7FFF7FFFu);
+            }
+            const float2 top = widen2<kBF16>(top2);
+            const float a = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(top.x, top.y))));
+            const float base = written & 1 ? 0.f : was, now = fmaxf(base, __fdiv_rn(a, kTop));
+            if (base > 0.f && base < now) {
+                const float ratio = __fdiv_rn(base, now);
+#pragma unroll 4
+                for (int r = sub; r < kRows; r += kPer) {
+                    if (written >> r & 1) continue;
+                    const float4 c = number4<kInt8>(cache[r * kLanes]);
+                    cache[r * kLanes] = code4<kInt8>(__fmul_rn(c.x, ratio), __fmul_rn(c.y, ratio),
+                                                     __fmul_rn(c.z, ratio), __fmul_rn(c.w, ratio));
+                }
+            }
+            const Divider by(now);
+            todo = run;
+#pragma unroll
+            for (int q = 0; q < kSteps; ++q) {
+                const int a2 = __ffs(todo) - 1;
+                todo &= todo - 1;
+                int from = a2;
+                if constexpr (kPer == 2) {
+                    const int b = __ffs(todo) - 1;
+                    todo &= todo - 1;
+                    from = sub ? b : a2;
+                }
+                const int r = __shfl_sync(0xffffffffu, r_lane, from & 31);
+                if (from >= 0) cache[r * kLanes] = row_codes<kBF16, kInt8>(w[q], by);
+            }
+            if (lane == 0) *scale = now;
+            continue;
+        }
+        // ---- padding between them: row by row, twice
+        auto each = [&](auto f) {   // f(row of the block, token)
+            for (int32_t first = t; first < T; first += 32) {
+                const int64_t sl = slot_at(first + lane);
+                const uint32_t all = __ballot_sync(0xffffffffu, sl >= 0);
+                const uint32_t ours = __ballot_sync(0xffffffffu, sl >= 0 && sl >> kShift == block);
+                const uint32_t end = all & ~ours;
+                for (uint32_t y = end ? ours & ((end & -end) - 1) : ours; y; y &= y - 1) {
+                    const int at = __ffs(y) - 1;
+                    f((int32_t)(__shfl_sync(0xffffffffu, sl, at) & (kRows - 1)), first + at);
+                }
+                if (end) break;
+            }
+        };
+        auto row = [&](int32_t j) {
+            return sub == 0 ? __ldg(x + ((int64_t)j * p.Hkv + h) * kLanes) : make_uint2(0, 0);
+        };
+        uint32_t written = 0, top2 = 0;
+        each([&](int32_t r, int32_t j) {
+            const uint2 y = row(j);
+            written |= 1u << r;
+            top2 = pa::max_x2<kBF16>(top2, pa::max_x2<kBF16>(y.x & 0x7FFF7FFFu, y.y & 0x7FFF7FFFu));
+        });
+        const float2 top = widen2<kBF16>(top2);
+        const float a = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(top.x, top.y))));
+        const float base = written & 1 ? 0.f : was, now = fmaxf(base, __fdiv_rn(a, kTop));
+        if (base > 0.f && base < now) {
+            const float ratio = __fdiv_rn(base, now);
+            for (int r = sub; r < kRows; r += kPer) {
+                if (written >> r & 1) continue;
+                const float4 c = number4<kInt8>(cache[r * kLanes]);
+                cache[r * kLanes] = code4<kInt8>(__fmul_rn(c.x, ratio), __fmul_rn(c.y, ratio),
+                                                 __fmul_rn(c.z, ratio), __fmul_rn(c.w, ratio));
+            }
+        }
+        const Divider by(now);
+        each([&](int32_t r, int32_t j) {
+            if (sub == 0) cache[r * kLanes] = row_codes<kBF16, kInt8>(row(j), by);
+        });
+        if (lane == 0) *scale = now;
+    }
 }
 
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
-int shift_of(int32_t block_size) {
-    return block_size == 8 ? 3 : block_size == 16 ? 4 : block_size == 32 ? 5 : -1;
-}
-
-// Checks shared by the append and the read back.
-pa_status check(const void* k, const void* v, const int64_t* slots, int32_t T, const void* k_cache,
-                const void* v_cache, const void* k_scale, const void* v_scale, int32_t num_blocks,
-                int32_t block_size, int32_t Hkv, int32_t d, pa_dtype dtype) {
-    if (T < 0 || num_blocks < 0 || Hkv <= 0) return PA_ERR_INVALID;
-    if (dtype != PA_F16 && dtype != PA_BF16) return PA_ERR_UNSUPPORTED;
-    if (d != 64 && d != 128) return PA_ERR_UNSUPPORTED;
-    if (shift_of(block_size) < 0) return PA_ERR_UNSUPPORTED;
-    if (Hkv > (1 << 20)) return PA_ERR_UNSUPPORTED;
-    if (T == 0) return PA_OK;
-    if (!k || !v || !slots || !k_cache || !v_cache || !k_scale || !v_scale) return PA_ERR_INVALID;
-    if (!aligned(k, 16) || !aligned(v, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) ||
-        !aligned(k_scale, 4) || !aligned(v_scale, 4) || !aligned(slots, 8))
-        return PA_ERR_INVALID;
-    return PA_OK;
+template <bool kInt8, int D, int kShift>
+pa_status launch(const AppendParams& p, bool bf16, cudaStream_t stream) {
+    auto kern = bf16 ? append_kernel<true, kInt8, D, kShift> : append_kernel<false, kInt8, D, kShift>;
+    const int64_t ctas = ((int64_t)p.T + kWindow - 1) / kWindow * p.groups;
+    if (ctas > INT32_MAX) return PA_ERR_UNSUPPORTED;
+    kern<<<(unsigned)ctas, kThreads, 0, stream>>>(p);
+    return pa::cuda_status(cudaGetLastError());
 }
 
 template <bool kInt8>
 pa_status append(const void* k_new, const void* v_new, const int64_t* slots, int32_t T,
                  void* k_cache, void* v_cache, float* k_scale, float* v_scale, int32_t num_blocks,
                  int32_t block_size, int32_t Hkv, int32_t d, pa_dtype dtype, void* stream) {
-    const pa_status st = check(k_new, v_new, slots, T, k_cache, v_cache, k_scale, v_scale,
-                               num_blocks, block_size, Hkv, d, dtype);
-    if (st != PA_OK || T == 0) return st;
-    unsigned int* err = pa::device_error_word();
-    if (!err) return PA_ERR_CUDA;
-    const int64_t warps = (int64_t)T * Hkv * 2, ctas = (warps + kThreads / 32 - 1) / (kThreads / 32);
-    if (ctas > INT32_MAX) return PA_ERR_UNSUPPORTED;
+    if (T < 0 || num_blocks < 0 || Hkv <= 0) return PA_ERR_INVALID;
+    if (dtype != PA_F16 && dtype != PA_BF16) return PA_ERR_UNSUPPORTED;
+    if (d != 64 && d != 128) return PA_ERR_UNSUPPORTED;
+    if (block_size != 8 && block_size != 16 && block_size != 32) return PA_ERR_UNSUPPORTED;
+    if (Hkv > (1 << 20)) return PA_ERR_UNSUPPORTED;
+    if (T == 0) return PA_OK;
+    if (!k_new || !v_new || !slots || !k_cache || !v_cache || !k_scale || !v_scale) return PA_ERR_INVALID;
+    if (!aligned(k_new, 16) || !aligned(v_new, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) ||
+        !aligned(k_scale, 4) || !aligned(v_scale, 4) || !aligned(slots, 8))
+        return PA_ERR_INVALID;
+    AppendParams p{static_cast<const uint2*>(k_new), static_cast<const uint2*>(v_new), slots,
+                   static_cast<uint32_t*>(k_cache), static_cast<uint32_t*>(v_cache), k_scale, v_scale,
+                   pa::device_error_word(), (int64_t)num_blocks * block_size, T, Hkv, 0, 8};
+    const int sms = pa::device_sm_count();
+    if (!p.err || !sms) return PA_ERR_CUDA;
+    // A prompt's window has a leader or none, a decode step's eight: as many tiles as warps
+    // for the former where that leaves four CTAs an SM, fewer where it does not.
+    const int64_t windows = ((int64_t)T + kWindow - 1) / kWindow;
+    for (; p.per > 1 && windows * ((2 * Hkv + p.per - 1) / p.per) < 4 * sms; p.per /= 2) {}
+    p.groups = (2 * Hkv + p.per - 1) / p.per;
     const bool bf16 = dtype == PA_BF16;
-    auto kern = d == 128 ? (bf16 ? append_kernel<true, kInt8, 128> : append_kernel<false, kInt8, 128>)
-                         : (bf16 ? append_kernel<true, kInt8, 64> : append_kernel<false, kInt8, 64>);
-    kern<<<(unsigned)ctas, kThreads, 0, static_cast<cudaStream_t>(stream)>>>(
-        static_cast<const uint2*>(k_new), static_cast<const uint2*>(v_new), slots, T, Hkv,
-        shift_of(block_size), static_cast<uint32_t*>(k_cache), static_cast<uint32_t*>(v_cache),
-        k_scale, v_scale, (int64_t)num_blocks * block_size, err);
-    return pa::cuda_status(cudaGetLastError());
-}
-
-template <bool kInt8>
-pa_status gather(const void* k_cache, const void* v_cache, const float* k_scale,
-                 const float* v_scale, const int64_t* slots, int32_t T, void* k_out, void* v_out,
-                 int32_t num_blocks, int32_t block_size, int32_t Hkv, int32_t d, pa_dtype dtype,
-                 void* stream) {
-    const pa_status st = check(k_out, v_out, slots, T, k_cache, v_cache, k_scale, v_scale,
-                               num_blocks, block_size, Hkv, d, dtype);
-    if (st != PA_OK || T == 0) return st;
-    unsigned int* err = pa::device_error_word();
-    if (!err) return PA_ERR_CUDA;
-    const int64_t vecs = (int64_t)T * Hkv * (d / kVec), ctas = (vecs + kThreads - 1) / kThreads;
-    if (ctas > INT32_MAX) return PA_ERR_UNSUPPORTED;
-    const bool bf16 = dtype == PA_BF16;
-    auto kern = d == 128 ? (bf16 ? gather_kernel<true, kInt8, 128> : gather_kernel<false, kInt8, 128>)
-                         : (bf16 ? gather_kernel<true, kInt8, 64> : gather_kernel<false, kInt8, 64>);
-    kern<<<(unsigned)ctas, kThreads, 0, static_cast<cudaStream_t>(stream)>>>(
-        static_cast<const uint32_t*>(k_cache), static_cast<const uint32_t*>(v_cache), k_scale,
-        v_scale, slots, vecs, Hkv, shift_of(block_size), (int64_t)num_blocks * block_size,
-        static_cast<uint2*>(k_out), static_cast<uint2*>(v_out), err);
-    return pa::cuda_status(cudaGetLastError());
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (d == 128)
+        return block_size == 8    ? launch<kInt8, 128, 3>(p, bf16, st)
+               : block_size == 16 ? launch<kInt8, 128, 4>(p, bf16, st)
+                                  : launch<kInt8, 128, 5>(p, bf16, st);
+    return block_size == 8    ? launch<kInt8, 64, 3>(p, bf16, st)
+           : block_size == 16 ? launch<kInt8, 64, 4>(p, bf16, st)
+                              : launch<kInt8, 64, 5>(p, bf16, st);
 }
 
 }  // namespace
@@ -262,24 +332,6 @@ PA_API pa_status pa_reshape_and_cache_fp8_block(const void* k_new, const void* v
                                                 int32_t block_size, int32_t Hkv, int32_t d,
                                                 pa_dtype dtype, void* stream) {
     return append<false>(k_new, v_new, slot_mapping, T, k_cache, v_cache, k_scale, v_scale,
-                         num_blocks, block_size, Hkv, d, dtype, stream);
-}
-
-PA_API pa_status pa_gather_cache_int8_block(const void* k_cache, const void* v_cache,
-                                            const float* k_scale, const float* v_scale,
-                                            const int64_t* slot_mapping, int32_t T, void* k_out,
-                                            void* v_out, int32_t num_blocks, int32_t block_size,
-                                            int32_t Hkv, int32_t d, pa_dtype dtype, void* stream) {
-    return gather<true>(k_cache, v_cache, k_scale, v_scale, slot_mapping, T, k_out, v_out,
-                        num_blocks, block_size, Hkv, d, dtype, stream);
-}
-
-PA_API pa_status pa_gather_cache_fp8_block(const void* k_cache, const void* v_cache,
-                                           const float* k_scale, const float* v_scale,
-                                           const int64_t* slot_mapping, int32_t T, void* k_out,
-                                           void* v_out, int32_t num_blocks, int32_t block_size,
-                                           int32_t Hkv, int32_t d, pa_dtype dtype, void* stream) {
-    return gather<false>(k_cache, v_cache, k_scale, v_scale, slot_mapping, T, k_out, v_out,
                          num_blocks, block_size, Hkv, d, dtype, stream);
 }
 

@@ -1,5 +1,5 @@
 // The 4-bit KV cache's append (pa_reshape_and_cache_int4) and the read back of
-// the quantised caches (pa_gather_cache_int4 / _int8 / _fp8).
+// the quantised caches (pa_gather_cache_int4 / _int8 / _fp8 / _int8_block / _fp8_block).
 //
 // Format ("LLM推理优化技术地图：从KV Cache到量化与投机解码", section 4.3, KV cache
 // quantisation; the page fixes none).  A row is the d values of one (token, KV
@@ -181,7 +181,9 @@ __device__ __forceinline__ uint32_t piece(int u) {
     return (blockIdx.x * kUnroll * kThreads + (threadIdx.x & ~31u) * kUnroll) + 32 * u + (threadIdx.x & 31);
 }
 
-enum Format { kInt4, kInt8, kFp8 };
+enum Format { kInt4, kInt8, kFp8, kInt8Block, kFp8Block };
+template <Format F>
+constexpr bool kBlockScaled = F == kInt8Block || F == kFp8Block;
 
 // Eight codes -> the values they stand for, rounded once to 16 bits.
 template <bool kBF16, Format F>
@@ -198,7 +200,7 @@ __device__ __forceinline__ uint4 dequantise8(uint2 codes, uint32_t sm) {
         for (int i = 0; i < 2; ++i) {
             const uint32_t c = i ? codes.y : codes.x;
             uint32_t lo, hi;
-            if constexpr (F == kInt8)
+            if constexpr (F == kInt8 || F == kInt8Block)
                 pa::s8x4_to_f16(c, lo, hi);
             else
                 pa::e4m3x4_to_f16(c, lo, hi);
@@ -241,20 +243,22 @@ gather_cache_kernel(const void* k_cache, const void* v_cache, const uint32_t* k_
         }
         if (slot[u] < 0) continue;   // padding: the output row is left as it is
         // (block, head, row) of the scales and of the 4-bit codes; the 8-bit codes
-        // are in (slot, head) order.
-        const int64_t at = ((((slot[u] >> bs_shift) * Hkv) + h[u]) << bs_shift) +
-                           (slot[u] & ((1 << bs_shift) - 1));
+        // are in (slot, head) order, those of the block-scaled cache in (block, head, row) order with
+        // a scale per (block, head).
+        const int64_t tile = ((slot[u] >> bs_shift) * Hkv) + h[u];
+        const int64_t at = (tile << bs_shift) + (slot[u] & ((1 << bs_shift) - 1));
         if constexpr (F == kInt4) {
             kc[u] = make_uint2(pa::ld_behind_wait(static_cast<const uint32_t*>(k_cache) + at * kRow + l), 0);
             vc[u] = make_uint2(pa::ld_behind_wait(static_cast<const uint32_t*>(v_cache) + at * kRow + l), 0);
             ks[u] = pa::ld_behind_wait(k_scale + at * (D / 64) + l / kGroupLanes);
             vs[u] = pa::ld_behind_wait(v_scale + at * (D / 64) + l / kGroupLanes);
         } else {
-            const int64_t c = (slot[u] * Hkv + h[u]) * kRow + l;
+            const int64_t c = (kBlockScaled<F> ? at : slot[u] * Hkv + h[u]) * kRow + l;
+            const int64_t sc = kBlockScaled<F> ? tile : at;
             kc[u] = pa::ld_behind_wait(static_cast<const uint2*>(k_cache) + c);
             vc[u] = pa::ld_behind_wait(static_cast<const uint2*>(v_cache) + c);
-            ks[u] = pa::ld_behind_wait(k_scale + at);
-            vs[u] = pa::ld_behind_wait(v_scale + at);
+            ks[u] = pa::ld_behind_wait(k_scale + sc);
+            vs[u] = pa::ld_behind_wait(v_scale + sc);
         }
     }
 #pragma unroll
@@ -275,11 +279,11 @@ int shift_of(int32_t block_size) {
 // one launch (a launch counts its vectors in 32 bits).
 pa_status check(const void* k, const void* v, const int64_t* slot_mapping, int32_t T,
                 const void* k_cache, const void* v_cache, const void* k_scale, const void* v_scale,
-                int32_t num_blocks, int32_t block_size, int32_t Hkv, int32_t d, bool int4,
+                int32_t num_blocks, int32_t block_size, int32_t Hkv, int32_t d, bool d64,
                 pa_dtype dtype, int64_t* slab) {
     if (T < 0 || num_blocks < 0 || Hkv <= 0) return PA_ERR_INVALID;
     if (dtype != PA_F16 && dtype != PA_BF16) return PA_ERR_UNSUPPORTED;
-    if (d != 128 && (!int4 || d != 64)) return PA_ERR_UNSUPPORTED;
+    if (d != 128 && (!d64 || d != 64)) return PA_ERR_UNSUPPORTED;
     if (shift_of(block_size) < 0) return PA_ERR_UNSUPPORTED;
     if (Hkv > (1 << 20)) return PA_ERR_UNSUPPORTED;
     *slab = ((int64_t)1 << 30) / ((int64_t)Hkv * (d / kVec));
@@ -355,12 +359,13 @@ pa_status gather_any(const void* k_cache, const void* v_cache, const void* k_sca
                      pa_dtype dtype, void* stream) {
     int64_t slab = 0;
     const pa_status st = check(k_out, v_out, slots, T, k_cache, v_cache, k_scale, v_scale,
-                               num_blocks, block_size, Hkv, d, F == kInt4, dtype, &slab);
+                               num_blocks, block_size, Hkv, d, F == kInt4 || kBlockScaled<F>, dtype,
+                               &slab);
     if (st != PA_OK || T == 0) return st;
     unsigned int* err = pa::device_error_word();
     if (!err) return PA_ERR_CUDA;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if constexpr (F == kInt4)
+    if constexpr (F == kInt4 || kBlockScaled<F>)
         if (d == 64)
             return dtype == PA_BF16
                        ? gather<true, F, 64>(k_cache, v_cache, k_scale, v_scale, slots, T,
@@ -431,6 +436,24 @@ PA_API pa_status pa_gather_cache_fp8(const void* k_cache, const void* v_cache,
                                      int32_t Hkv, int32_t d, pa_dtype dtype, void* stream) {
     return gather_any<kFp8>(k_cache, v_cache, k_scale, v_scale, slot_mapping, T, k_out, v_out,
                             num_blocks, block_size, Hkv, d, dtype, stream);
+}
+
+PA_API pa_status pa_gather_cache_int8_block(const void* k_cache, const void* v_cache,
+                                            const float* k_scale, const float* v_scale,
+                                            const int64_t* slot_mapping, int32_t T, void* k_out,
+                                            void* v_out, int32_t num_blocks, int32_t block_size,
+                                            int32_t Hkv, int32_t d, pa_dtype dtype, void* stream) {
+    return gather_any<kInt8Block>(k_cache, v_cache, k_scale, v_scale, slot_mapping, T, k_out, v_out,
+                              num_blocks, block_size, Hkv, d, dtype, stream);
+}
+
+PA_API pa_status pa_gather_cache_fp8_block(const void* k_cache, const void* v_cache,
+                                           const float* k_scale, const float* v_scale,
+                                           const int64_t* slot_mapping, int32_t T, void* k_out,
+                                           void* v_out, int32_t num_blocks, int32_t block_size,
+                                           int32_t Hkv, int32_t d, pa_dtype dtype, void* stream) {
+    return gather_any<kFp8Block>(k_cache, v_cache, k_scale, v_scale, slot_mapping, T, k_out, v_out,
+                              num_blocks, block_size, Hkv, d, dtype, stream);
 }
 
 }  // extern "C"
