@@ -1580,9 +1580,11 @@ struct WeightsParams {
 
 constexpr int kAddThreads = 256;
 
-// weights[row][g][j] += sum over the query heads h of g of 2^(s_hj - M_h) / L_h: a warp per
-// (sequence, KV head, chunk), a lane per token.  The heads are added in order, no two warps
-// touch the same weight.
+constexpr int kAddChunks = 4;   // chunks of a warp at a time
+
+// weights[row][g][j] += sum over the query heads h of g of 2^(s_hj - M_h) / L_h: a warp has a
+// contiguous share of the (sequence, KV head, chunk) list, a lane a token of each of four chunks.
+// The heads are added in order, no two warps touch the same weight.
 __global__ void __launch_bounds__(kAddThreads) add_weights_kernel(const WeightsParams p) {
     asm volatile("griddepcontrol.wait;" ::: "memory");   // launched while the decode may run
     const int lane = threadIdx.x & 31;
@@ -1593,30 +1595,65 @@ __global__ void __launch_bounds__(kAddThreads) add_weights_kernel(const WeightsP
             if (row >= 0 && row < p.num_rows && pa::ld_behind_wait(p.context_lens + i) > p.width)
                 pa::raise_error(p.err, PA_DEVERR_TABLE_WIDTH);
         }
-    const int32_t W = pa::ld_behind_wait(p.prefix + p.B);
+    // the list's prefix, read once by all threads rather than again and again on the way
+    extern __shared__ int32_t prefix[];
+    for (int32_t i = threadIdx.x; i <= p.B; i += kAddThreads) prefix[i] = pa::ld_behind_wait(p.prefix + i);
+    __syncthreads();
+    const int32_t W = prefix[p.B];
     if (W > p.score_chunks) return;
     const int32_t units = W / p.subs, warps = gridDim.x * (kAddThreads / 32);
-    for (int32_t u = blockIdx.x * (kAddThreads / 32) + (threadIdx.x >> 5); u < units; u += warps) {
-        int32_t lo = 0, hi = p.B;   // largest i with prefix[i] / subs <= u
-        while (hi - lo > 1) {
-            const int32_t mid = (lo + hi) >> 1;
-            if (pa::ld_behind_wait(p.prefix + mid) / p.subs <= u) lo = mid; else hi = mid;
+    const int32_t me = blockIdx.x * (kAddThreads / 32) + (threadIdx.x >> 5);
+    int32_t u = (int32_t)((int64_t)me * units / warps);
+    const int32_t end = (int32_t)((int64_t)(me + 1) * units / warps);
+    if (u >= end) return;
+    int32_t i = 0, hi = p.B;   // largest i with prefix[i] / subs <= u
+    while (hi - i > 1) {
+        const int32_t mid = (i + hi) >> 1;
+        if (prefix[mid] <= u * p.subs) i = mid; else hi = mid;
+    }
+    while (u < end) {
+        // the chunks of sequence i that are this warp's
+        while (prefix[i + 1] <= u * p.subs) ++i;
+        const int32_t a = prefix[i], b = prefix[i + 1];
+        const int32_t nc = (b - a) / (p.Hkv * p.subs), stop = min(end, b / p.subs);
+        const int32_t row = pa::ld_behind_wait(p.rows + i);
+        const int32_t n = min(pa::ld_behind_wait(p.context_lens + i), p.width);
+        if (row < 0 || row >= p.num_rows) {
+            u = stop;
+            continue;
         }
-        const int32_t a = pa::ld_behind_wait(p.prefix + lo);
-        const int32_t nc = (pa::ld_behind_wait(p.prefix + lo + 1) - a) / (p.Hkv * p.subs);
-        const int32_t local = u - a / p.subs, g = local / nc, c = local - g * nc;
-        const int32_t row = pa::ld_behind_wait(p.rows + lo), j = c * kChunk + lane;
-        if (row < 0 || row >= p.num_rows) continue;
-        if (j >= min(pa::ld_behind_wait(p.context_lens + lo), p.width)) continue;
-        float sum = 0.f;
-        for (int32_t x = 0; x < p.subs; ++x) {
-            const float* s = p.scores + ((int64_t)a + (g * p.subs + x) * nc + c) * p.G * kChunk + lane;
-            const float* st = p.stats + ((int64_t)lo * p.Hkv * p.subs + g * p.subs + x) * p.G * 2;
-            for (int32_t h = 0; h < p.G; ++h)
-                sum += pa::fast_exp2(pa::ld_behind_wait(s + h * kChunk) - pa::ld_behind_wait(st + 2 * h)) *
-                       pa::ld_behind_wait(st + 2 * h + 1);
+        while (u < stop) {
+            const int32_t local = u - a / p.subs, g = local / nc, c0 = local - g * nc;
+            const int32_t c1 = min(nc, c0 + stop - u);     // of this KV head
+            float* to = p.weights + ((int64_t)row * p.Hkv + g) * p.width;
+            for (int32_t c = c0; c < c1; c += kAddChunks) {
+                float sum[kAddChunks] = {}, was[kAddChunks];
+                bool is[kAddChunks];
+#pragma unroll
+                for (int q = 0; q < kAddChunks; ++q) {
+                    const int32_t j = (c + q) * kChunk + lane;
+                    is[q] = c + q < c1 && j < n;
+                    was[q] = is[q] ? pa::ld_behind_wait(to + j) : 0.f;
+                }
+                for (int32_t x = 0; x < p.subs; ++x) {
+                    const int32_t pair = g * p.subs + x;
+                    const float* s = p.scores + ((int64_t)a + (int64_t)pair * nc + c) * p.G * kChunk + lane;
+                    const float* st = p.stats + ((int64_t)i * p.Hkv * p.subs + pair) * p.G * 2;
+#pragma unroll 4
+                    for (int32_t h = 0; h < p.G; ++h) {
+                        const float2 ml = pa::ld_behind_wait(reinterpret_cast<const float2*>(st) + h);
+#pragma unroll
+                        for (int q = 0; q < kAddChunks; ++q)
+                            if (is[q])
+                                sum[q] += pa::fast_exp2(pa::ld_behind_wait(s + (q * p.G + h) * kChunk) - ml.x) * ml.y;
+                    }
+                }
+#pragma unroll
+                for (int q = 0; q < kAddChunks; ++q)
+                    if (is[q]) to[(c + q) * kChunk + lane] = was[q] + sum[q];
+            }
+            u += c1 - c0;
         }
-        p.weights[((int64_t)row * p.Hkv + g) * p.width + j] += sum;
     }
 }
 
@@ -1703,6 +1740,7 @@ PA_API pa_status pa_decode_weights(const void* q, const void* k_cache, const voi
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)(8 * pa::device_sm_count()));
     cfg.blockDim = dim3(kAddThreads);
+    cfg.dynamicSmemBytes = (size_t)(B + 1) * 4;
     cfg.stream = st;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;

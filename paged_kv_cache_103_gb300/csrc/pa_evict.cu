@@ -32,18 +32,26 @@ __device__ __forceinline__ uint32_t ordered(float x) {
     return isnan(x) ? 0u : u ^ (u >> 31 ? 0xffffffffu : 0x80000000u);
 }
 
-constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
-constexpr int kBinBits = 10, kBins = 1 << kBinBits;   // four bins a thread
+constexpr int kBinBits = 10, kBins = 1 << kBinBits;
 
+// A warp has a contiguous stretch of the weights, 32 neighbours an instruction, so that ranks
+// inside it are counts of ballots: up to kPer instructions' in registers, or (0) any number, read
+// again from L2 by each pass.  Bound by latency: the length and row, the weights, two or three
+// passes of three barriers each, two scans.
+template <int kThreads, int kPer>
 __global__ void __launch_bounds__(kThreads) select_tokens_kernel(const ChooseParams p) {
+    constexpr int kWarps = kThreads / 32, kOwn = kBins / kThreads;   // bins of a thread
     __shared__ __align__(16) uint32_t hist[kBins];
     __shared__ uint32_t s_top[kWarps], s_low[kWarps], wsum[kWarps], wsum2[kWarps];
     __shared__ uint32_t s_bin, s_rank, s_count;
+    // What moves the rows may be launched: it waits for this grid's end.
+    asm volatile("griddepcontrol.launch_dependents;");
+    asm volatile("griddepcontrol.wait;" ::: "memory");   // launched while the kernel before may run
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t below = (1u << lane) - 1;
     const int32_t g = blockIdx.x, i = blockIdx.y;
     int32_t* kept = p.kept + ((int64_t)i * p.Hkv + g) * p.keep;
-    const int32_t row = p.rows[i], raw = p.context_lens[i];
+    const int32_t row = pa::ld_behind_wait(p.rows + i), raw = pa::ld_behind_wait(p.context_lens + i);
     const bool part = row >= 0 && row < p.num_rows;
     if (tid == 0 && g == 0) {
         if (row >= p.num_rows) pa::raise_error(p.err, PA_DEVERR_SLOT);
@@ -55,23 +63,40 @@ __global__ void __launch_bounds__(kThreads) select_tokens_kernel(const ChoosePar
     for (int32_t j = count + tid; j < p.keep; j += kThreads) kept[j] = -1;
     if (!part) return;
     const float* w = p.weights + ((int64_t)row * p.Hkv + g) * p.width;
+    float* to = p.new_weights ? p.new_weights + ((int64_t)row * p.Hkv + g) * p.width : nullptr;
     const int32_t k = p.keep - p.first - p.last, m = n - p.first - p.last;   // k < m where tokens go
+    const bool choose = n > p.keep && k > 0;
+    const int32_t per = kPer ? kPer : (m + kThreads - 1) / kThreads;
+    const int32_t beg = warp * per * 32 + lane;
+    float own[kPer ? kPer : 1];
+    if constexpr (kPer > 0)
+#pragma unroll
+        for (int q = 0; q < kPer; ++q)
+            own[q] = choose && beg + q * 32 < m ? pa::ld_behind_wait(w + p.first + beg + q * 32) : 0.f;
     const int32_t head = n <= p.keep ? n : p.first;
     for (int32_t j = tid; j < head; j += kThreads) kept[j] = j;
-    if (n > p.keep) {
+    if (n > p.keep)
         for (int32_t j = tid; j < p.last; j += kThreads) kept[p.keep - p.last + j] = n - p.last + j;
-        for (int b = tid; b < kBins; b += kThreads) hist[b] = 0;
-    }
-    if (n > p.keep && k > 0) {
-        const int32_t per = (m + kThreads - 1) / kThreads;
-        const int32_t beg = min(m, tid * per), end = min(m, beg + per);
-        auto each = [&](auto f) {   // f(key, place) for each key of this thread's stretch
-            for (int32_t j = beg; j < end; ++j) f(ordered(w[p.first + j]), j);
+    if (choose) {
+        // f(weight, place, whether there is one), for whole warps
+        auto each = [&](auto f) {
+            if constexpr (kPer > 0) {
+#pragma unroll
+                for (int q = 0; q < kPer; ++q) f(own[q], beg + q * 32, beg + q * 32 < m);
+            } else {
+#pragma unroll 4
+                for (int32_t q = 0; q < per; ++q) {
+                    const int32_t j = beg + q * 32;
+                    f(j < m ? pa::ld_behind_wait(w + p.first + j) : 0.f, j, j < m);
+                }
+            }
         };
         uint32_t top = 0, low = 0;    // the largest key, and the smallest's complement
-        each([&](uint32_t x, int) {
-            top = max(top, x);
-            low = max(low, ~x);
+        for (int b = tid; b < kBins; b += kThreads) hist[b] = 0;
+        each([&](float x, int32_t, bool is) {
+            if (!is) return;
+            top = max(top, ordered(x));
+            low = max(low, ~ordered(x));
         });
         top = __reduce_max_sync(0xffffffffu, top);
         low = __reduce_max_sync(0xffffffffu, low);
@@ -86,16 +111,20 @@ __global__ void __launch_bounds__(kThreads) select_tokens_kernel(const ChoosePar
         int shift = max(0, width - kBinBits);
         uint32_t rank = (uint32_t)k, limit, ties;      // chosen: keys above limit, and `ties` equal ones
         for (;;) {
-            each([&](uint32_t x, int) {
-                x -= base;                             // keys below base wrap to large numbers
-                if (width == 32 || (x >> width) == 0) atomicAdd(&hist[x >> shift], 1u);
+            each([&](float x, int32_t, bool is) {
+                const uint32_t y = ordered(x) - base;  // keys below base wrap to large numbers
+                if (is && (width == 32 || (y >> width) == 0)) atomicAdd(&hist[y >> shift], 1u);
             });
             __syncthreads();
-            // Counts from the top: thread t owns bins 4 t' .. 4 t' + 3 with t' = kThreads - 1 - t.
-            const int b0 = (kThreads - 1 - tid) * (kBins / kThreads);
-            const uint4 c4 = *reinterpret_cast<const uint4*>(hist + b0);
-            *reinterpret_cast<uint4*>(hist + b0) = make_uint4(0, 0, 0, 0);
-            const uint32_t mine = c4.x + c4.y + c4.z + c4.w;
+            // Counts from the top: thread t owns kOwn bins, those of thread 0 the highest.
+            const int b0 = (kThreads - 1 - tid) * kOwn;
+            uint32_t c[kOwn], mine = 0;
+#pragma unroll
+            for (int q = 0; q < kOwn; ++q) {
+                c[q] = hist[b0 + q];
+                hist[b0 + q] = 0;
+                mine += c[q];
+            }
             uint32_t upto = mine;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -106,14 +135,17 @@ __global__ void __launch_bounds__(kThreads) select_tokens_kernel(const ChoosePar
             __syncthreads();
             upto += __reduce_add_sync(0xffffffffu, lane < warp ? wsum[lane % kWarps] : 0u);
             if (upto >= rank && upto - mine < rank) {   // one thread
-                uint32_t want = rank - (upto - mine), c = c4.w;
-                int q = 3;
-                if (c < want) want -= c, c = c4.z, q = 2;
-                if (q == 2 && c < want) want -= c, c = c4.y, q = 1;
-                if (q == 1 && c < want) want -= c, c = c4.x, q = 0;
+                uint32_t want = rank - (upto - mine);
+                int q = kOwn - 1;
+#pragma unroll
+                for (int x = kOwn - 1; x > 0; --x)
+                    if (q == x && c[x] < want) want -= c[x], q = x - 1;
                 s_bin = b0 + q;
                 s_rank = want;
-                s_count = c;
+                s_count = c[0];
+#pragma unroll
+                for (int x = 1; x < kOwn; ++x)
+                    if (q == x) s_count = c[x];
             }
             __syncthreads();
             base += s_bin << shift;
@@ -133,41 +165,40 @@ __global__ void __launch_bounds__(kThreads) select_tokens_kernel(const ChoosePar
         }
         // ---- positions in order
         uint32_t above = 0, equal = 0;
-        each([&](uint32_t x, int) {
-            above += x > limit;
-            equal += x == limit;
+        each([&](float x, int32_t, bool is) {
+            above += __popc(__ballot_sync(0xffffffffu, is && ordered(x) > limit));
+            equal += __popc(__ballot_sync(0xffffffffu, is && ordered(x) == limit));
         });
-        uint32_t a = above, e = equal;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const uint32_t ya = __shfl_up_sync(0xffffffffu, a, o), ye = __shfl_up_sync(0xffffffffu, e, o);
-            if (lane >= o) {
-                a += ya;
-                e += ye;
-            }
-        }
-        if (lane == 31) {
-            wsum[warp] = a;
-            wsum2[warp] = e;
+        if (lane == 0) {
+            wsum[warp] = above;
+            wsum2[warp] = equal;
         }
         __syncthreads();
-        a += __reduce_add_sync(0xffffffffu, lane < warp ? wsum[lane % kWarps] : 0u) - above;
-        e += __reduce_add_sync(0xffffffffu, lane < warp ? wsum2[lane % kWarps] : 0u) - equal;
-        uint32_t at = a + min(e, ties);
-        each([&](uint32_t x, int32_t j) {
-            const bool take = x > limit || (x == limit && e < ties);
-            e += x == limit;
-            if (take) kept[p.first + at++] = p.first + j;
+        uint32_t a = __reduce_add_sync(0xffffffffu, lane < warp ? wsum[lane % kWarps] : 0u);
+        uint32_t e = __reduce_add_sync(0xffffffffu, lane < warp ? wsum2[lane % kWarps] : 0u);
+        each([&](float x, int32_t j, bool is) {
+            const uint32_t up = __ballot_sync(0xffffffffu, is && ordered(x) > limit);
+            const uint32_t eq = __ballot_sync(0xffffffffu, is && ordered(x) == limit);
+            const uint32_t my_e = e + __popc(eq & below);
+            if (up >> lane & 1 || (eq >> lane & 1 && my_e < ties)) {
+                const uint32_t at = p.first + a + __popc(up & below) + min(my_e, ties);
+                kept[at] = p.first + j;
+                if (kPer > 0 && to) to[at] = x;    // every weight between is in registers by now
+            }
+            a += __popc(up);
+            e += __popc(eq);
         });
     }
-    if (!p.new_weights) return;
-    // The kept weights move down, kept[r] >= r: a stretch is read before any of it is written.
-    float* to = p.new_weights + ((int64_t)row * p.Hkv + g) * p.width;
+    if (!to) return;
+    // The other kept weights move down, kept[r] >= r: a stretch is read before any of it is written.
+    const bool rest = !(kPer > 0 && choose);
     for (int32_t r = tid; r - tid < count; r += kThreads) {
+        if (!rest && r - tid >= p.first && r - tid + kThreads <= p.keep - p.last) continue;
+        const bool mine = r < count && (rest || r < p.first || r >= p.keep - p.last);
         __syncthreads();
-        const float x = r < count ? w[kept[r]] : 0.f;
+        const float x = mine ? pa::ld_behind_wait(w + kept[r]) : 0.f;
         __syncthreads();
-        if (r < count) to[r] = x;
+        if (mine) to[r] = x;
     }
     __syncthreads();
     for (int32_t r = count + tid; r < p.width; r += kThreads) to[r] = 0.f;
@@ -183,48 +214,88 @@ struct CompactParams {
 
 constexpr int kMove = 4;   // rows of a thread at a time, K and V each
 
-// One CTA per (sequence, KV head).  Row r comes from kept[r] >= r, and both ascend: once a
-// stretch of rows has been read, nothing that is still to be read lies in the stretch.
-__global__ void __launch_bounds__(kThreads) compact_kernel(const CompactParams p) {
-    const int32_t g = blockIdx.x, i = blockIdx.y, mask = (1 << p.bs_shift) - 1;
-    const int32_t raw = p.kept_lens[i];
-    if (threadIdx.x == 0 && g == 0 && (raw < 0 || raw > p.keep)) pa::raise_error(p.err, PA_DEVERR_CONTEXT);
+// A cluster of CTAs per (sequence, KV head).  Row r comes from kept[r] >= r, and both ascend:
+// once a stretch of rows has been read, nothing that is still to be read lies in the
+// stretch.  So the cluster reads a stretch into its registers, meets, writes it, and reads the
+// next one, without meeting again.
+template <int kThreads>
+__global__ void __launch_bounds__(kThreads, 1024 / kThreads) compact_kernel(const CompactParams p) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");   // launched while the choice may be made
+    uint32_t rank, ctas;
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+    asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(ctas));
+    const int32_t pair = blockIdx.x / ctas, i = pair / p.Hkv, g = pair - i * p.Hkv, mask = (1 << p.bs_shift) - 1;
+    const int32_t raw = pa::ld_behind_wait(p.kept_lens + i);
+    if (threadIdx.x == 0 && rank == 0 && g == 0 && (raw < 0 || raw > p.keep))
+        pa::raise_error(p.err, PA_DEVERR_CONTEXT);
     const int32_t n = max(0, min(raw, p.keep));
-    const int32_t* kept = p.kept + ((int64_t)i * p.Hkv + g) * p.keep;
+    const int32_t* kept = p.kept + (int64_t)pair * p.keep;
+    const int32_t* from_table = p.block_tables + (int64_t)i * p.max_blocks;
+    const int32_t* to_table = p.new_tables + (int64_t)i * p.new_max_blocks;
     const int rows = kThreads / p.vecs, r0 = threadIdx.x / p.vecs, c = threadIdx.x % p.vecs;
-    for (int32_t base = 0; base < n; base += rows * kMove) {
+    const int32_t stretch = rows * kMove * (int32_t)ctas;   // of the cluster
+    auto piece = [&](int32_t slot) { return ((int64_t)slot * p.Hkv + g) * p.vecs + c; };
+#pragma unroll 1
+    for (int32_t base = 0; base < n; base += min(stretch, n - base)) {
         uint4 k[kMove], v[kMove];
-        int64_t to[kMove];
+        int32_t to[kMove], from[kMove];   // slots; -1: not this row
+        const int32_t at = base + (int32_t)rank * rows * kMove + r0;   // < 2^31 + 2^13: as an unsigned number
 #pragma unroll
         for (int u = 0; u < kMove; ++u) {
-            const int32_t r = base + u * rows + r0;
-            to[u] = -1;
-            if (r >= n) continue;
-            const int32_t pos = kept[r], sb = pos >> p.bs_shift, db = r >> p.bs_shift;
+            const uint32_t r = (uint32_t)at + u * rows;
+            from[u] = to[u] = -1;
+            if (r < (uint32_t)n) from[u] = pa::ld_behind_wait(kept + r);
+        }
+#pragma unroll
+        for (int u = 0; u < kMove; ++u) {
+            const uint32_t r = (uint32_t)at + u * rows;
+            if (r >= (uint32_t)n) continue;
+            const int32_t pos = from[u], sb = pos >> p.bs_shift, db = (int32_t)(r >> p.bs_shift);
+            from[u] = -1;
             if (pos < 0 || sb >= p.max_blocks || db >= p.new_max_blocks) {
                 pa::raise_error(p.err, PA_DEVERR_TABLE_WIDTH);
                 continue;
             }
-            const int32_t src = p.block_tables[(int64_t)i * p.max_blocks + sb];
-            const int32_t dst = p.new_tables[(int64_t)i * p.new_max_blocks + db];
+            const int32_t src = pa::ld_behind_wait(from_table + sb), dst = pa::ld_behind_wait(to_table + db);
             if ((uint32_t)src >= (uint32_t)p.num_blocks || (uint32_t)dst >= (uint32_t)p.num_blocks) {
                 pa::raise_error(p.err, PA_DEVERR_BLOCK_ID);
                 continue;
             }
-            if (src == dst && pos == r) continue;
-            const int64_t from = ((((int64_t)src << p.bs_shift) + (pos & mask)) * p.Hkv + g) * p.vecs + c;
-            to[u] = ((((int64_t)dst << p.bs_shift) + (r & mask)) * p.Hkv + g) * p.vecs + c;
-            k[u] = p.k_cache[from];
-            v[u] = p.v_cache[from];
+            to[u] = (dst << p.bs_shift) + (int32_t)(r & mask);
+            from[u] = (src << p.bs_shift) + (pos & mask);
+            if (from[u] == to[u]) to[u] = -1;   // stays
         }
-        __syncthreads();
 #pragma unroll
-        for (int u = 0; u < kMove; ++u) {
-            if (to[u] < 0) continue;
-            p.k_cache[to[u]] = k[u];
-            p.v_cache[to[u]] = v[u];
-        }
+        for (int u = 0; u < kMove; ++u)
+            if (to[u] >= 0) k[u] = pa::ld_behind_wait(p.k_cache + piece(from[u]));
+#pragma unroll
+        for (int u = 0; u < kMove; ++u)
+            if (to[u] >= 0) v[u] = pa::ld_behind_wait(p.v_cache + piece(from[u]));
+        asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+#pragma unroll
+        for (int u = 0; u < kMove; ++u)
+            if (to[u] >= 0) {
+                p.k_cache[piece(to[u])] = k[u];
+                p.v_cache[piece(to[u])] = v[u];
+            }
     }
+}
+
+template <typename K, typename P>
+pa_status launch_early(K kern, dim3 grid, int threads, int cluster, cudaStream_t stream, const P& p) {
+    cudaLaunchAttribute attr[2] = {};
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 0 ? 2 : 1;
+    return pa::cuda_status(cudaLaunchKernelEx(&cfg, kern, p));
 }
 
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
@@ -250,8 +321,13 @@ PA_API pa_status pa_select_tokens(const float* weights, int32_t num_rows, int32_
     ChooseParams p{weights, new_weights, rows, context_lens, kept, kept_lens,
                    pa::device_error_word(), num_rows, width, Hkv, keep, first, last};
     if (!p.err) return PA_ERR_CUDA;
-    select_tokens_kernel<<<dim3((unsigned)Hkv, (unsigned)B), kThreads, 0, static_cast<cudaStream_t>(stream)>>>(p);
-    return pa::cuda_status(cudaGetLastError());
+    const dim3 grid((unsigned)Hkv, (unsigned)B);
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const int64_t most = (int64_t)width - first - last;   // weights to choose from, at most
+    if (most <= 4 * 256) return launch_early(select_tokens_kernel<256, 4>, grid, 256, 0, st, p);
+    if (most <= 8 * 1024) return launch_early(select_tokens_kernel<1024, 8>, grid, 1024, 0, st, p);
+    if (most <= 24 * 1024) return launch_early(select_tokens_kernel<1024, 24>, grid, 1024, 0, st, p);
+    return launch_early(select_tokens_kernel<1024, 0>, grid, 1024, 0, st, p);
 }
 
 PA_API pa_status pa_compact_tokens(void* k_cache, void* v_cache, const int32_t* kept,
@@ -276,8 +352,19 @@ PA_API pa_status pa_compact_tokens(void* k_cache, void* v_cache, const int32_t* 
                     block_tables, new_tables, pa::device_error_word(), keep, max_blocks,
                     new_max_blocks, Hkv, d / 8, block_size == 8 ? 3 : block_size == 16 ? 4 : 5, num_blocks};
     if (!p.err) return PA_ERR_CUDA;
-    compact_kernel<<<dim3((unsigned)Hkv, (unsigned)B), kThreads, 0, static_cast<cudaStream_t>(stream)>>>(p);
-    return pa::cuda_status(cudaGetLastError());
+    const int sms = pa::device_sm_count();
+    if (!sms) return PA_ERR_CUDA;
+    const int64_t pairs = (int64_t)B * Hkv;
+    if (pairs > INT32_MAX / 8) return PA_ERR_UNSUPPORTED;
+    // Up to eight CTAs a pair, as many as its rows fill; of 1024 threads where even so there is
+    // less than one for every SM.
+    int cluster = 1;
+    const int small = 256 / p.vecs * kMove;
+    while (cluster < 8 && (int64_t)cluster * small < keep) cluster *= 2;
+    const dim3 grid((unsigned)(pairs * cluster));
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (pairs * cluster <= sms) return launch_early(compact_kernel<1024>, grid, 1024, cluster, st, p);
+    return launch_early(compact_kernel<256>, grid, 256, cluster, st, p);
 }
 
 }  // extern "C"
