@@ -249,6 +249,8 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap kmap,
     static_assert(!kFp8 || D == 128, "FP8 rows are one 128-byte swizzle row");
     // Launched while the kernel before it (the selection of its block lists) may still run.
     if constexpr (kPair) asm volatile("griddepcontrol.wait;" ::: "memory");
+    // What adds the weights may be launched: it waits for this grid's end.
+    if constexpr (kScores) asm volatile("griddepcontrol.launch_dependents;");
     constexpr int kProducerWarps = producer_warps(kFp8);
     constexpr int kThreads = cta_threads(kFp8);
     constexpr uint32_t kHalves = kFp8 ? 1 : D / 64;  // 128-byte pieces of a token row
@@ -1581,6 +1583,7 @@ struct WeightsParams {
 constexpr int kAddThreads = 256;
 
 constexpr int kAddChunks = 4;   // chunks of a warp at a time
+constexpr int kAddHeads = 4;    // query heads of them at a time
 
 // weights[row][g][j] += sum over the query heads h of g of 2^(s_hj - M_h) / L_h: a warp has a
 // contiguous share of the (sequence, KV head, chunk) list, a lane a token of each of four chunks.
@@ -1588,16 +1591,20 @@ constexpr int kAddChunks = 4;   // chunks of a warp at a time
 __global__ void __launch_bounds__(kAddThreads) add_weights_kernel(const WeightsParams p) {
     asm volatile("griddepcontrol.wait;" ::: "memory");   // launched while the decode may run
     const int lane = threadIdx.x & 31;
-    if (blockIdx.x == 0)
-        for (int32_t i = threadIdx.x; i < p.B; i += kAddThreads) {
-            const int32_t row = pa::ld_behind_wait(p.rows + i);
-            if (row >= p.num_rows) pa::raise_error(p.err, PA_DEVERR_SLOT);
-            if (row >= 0 && row < p.num_rows && pa::ld_behind_wait(p.context_lens + i) > p.width)
-                pa::raise_error(p.err, PA_DEVERR_TABLE_WIDTH);
-        }
-    // the list's prefix, read once by all threads rather than again and again on the way
+    // the list's prefix, the rows (-1: takes no part) and lengths, all at once
     extern __shared__ int32_t prefix[];
-    for (int32_t i = threadIdx.x; i <= p.B; i += kAddThreads) prefix[i] = pa::ld_behind_wait(p.prefix + i);
+    int32_t *rows = prefix + p.B + 1, *lens = rows + p.B;
+    for (int32_t i = threadIdx.x; i <= p.B; i += kAddThreads) {
+        prefix[i] = pa::ld_behind_wait(p.prefix + i);
+        if (i == p.B) break;
+        const int32_t row = pa::ld_behind_wait(p.rows + i), n = pa::ld_behind_wait(p.context_lens + i);
+        if (blockIdx.x == 0) {
+            if (row >= p.num_rows) pa::raise_error(p.err, PA_DEVERR_SLOT);
+            if (row >= 0 && row < p.num_rows && n > p.width) pa::raise_error(p.err, PA_DEVERR_TABLE_WIDTH);
+        }
+        rows[i] = row < p.num_rows ? row : -1;
+        lens[i] = min(n, p.width);
+    }
     __syncthreads();
     const int32_t W = prefix[p.B];
     if (W > p.score_chunks) return;
@@ -1616,9 +1623,8 @@ __global__ void __launch_bounds__(kAddThreads) add_weights_kernel(const WeightsP
         while (prefix[i + 1] <= u * p.subs) ++i;
         const int32_t a = prefix[i], b = prefix[i + 1];
         const int32_t nc = (b - a) / (p.Hkv * p.subs), stop = min(end, b / p.subs);
-        const int32_t row = pa::ld_behind_wait(p.rows + i);
-        const int32_t n = min(pa::ld_behind_wait(p.context_lens + i), p.width);
-        if (row < 0 || row >= p.num_rows) {
+        const int32_t row = rows[i], n = lens[i];
+        if (row < 0) {
             u = stop;
             continue;
         }
@@ -1639,13 +1645,27 @@ __global__ void __launch_bounds__(kAddThreads) add_weights_kernel(const WeightsP
                     const int32_t pair = g * p.subs + x;
                     const float* s = p.scores + ((int64_t)a + (int64_t)pair * nc + c) * p.G * kChunk + lane;
                     const float* st = p.stats + ((int64_t)i * p.Hkv * p.subs + pair) * p.G * 2;
-#pragma unroll 4
-                    for (int32_t h = 0; h < p.G; ++h) {
-                        const float2 ml = pa::ld_behind_wait(reinterpret_cast<const float2*>(st) + h);
+#pragma unroll 1
+                    for (int32_t h0 = 0; h0 < p.G; h0 += kAddHeads) {
+                        // all of four heads' loads are under way together
+                        float2 ml[kAddHeads];
+                        float v[kAddHeads][kAddChunks];
 #pragma unroll
-                        for (int q = 0; q < kAddChunks; ++q)
-                            if (is[q])
-                                sum[q] += pa::fast_exp2(pa::ld_behind_wait(s + (q * p.G + h) * kChunk) - ml.x) * ml.y;
+                        for (int y = 0; y < kAddHeads; ++y) {
+                            const bool has = h0 + y < p.G;
+                            ml[y] = make_float2(0.f, 0.f);   // a head that is not there adds 0
+                            if (has) ml[y] = pa::ld_behind_wait(reinterpret_cast<const float2*>(st) + h0 + y);
+#pragma unroll
+                            for (int q = 0; q < kAddChunks; ++q) {
+                                v[y][q] = 0.f;
+                                if (has && is[q]) v[y][q] = pa::ld_behind_wait(s + (q * p.G + h0 + y) * kChunk);
+                            }
+                        }
+#pragma unroll
+                        for (int y = 0; y < kAddHeads; ++y)
+#pragma unroll
+                            for (int q = 0; q < kAddChunks; ++q)
+                                sum[q] += pa::fast_exp2(v[y][q] - ml[y].x) * ml[y].y;
                     }
                 }
 #pragma unroll
@@ -1740,7 +1760,9 @@ PA_API pa_status pa_decode_weights(const void* q, const void* k_cache, const voi
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)(8 * pa::device_sm_count()));
     cfg.blockDim = dim3(kAddThreads);
-    cfg.dynamicSmemBytes = (size_t)(B + 1) * 4;
+    cfg.dynamicSmemBytes = (size_t)(3 * B + 1) * 4;
+    static pa::DeviceOnce once;
+    if (!pa::allow_smem(once, add_weights_kernel, (3 * kMaxBatch + 1) * 4)) return PA_ERR_CUDA;
     cfg.stream = st;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;

@@ -31,17 +31,24 @@ __device__ __forceinline__ uint32_t ordered(float x) {
     const uint32_t u = __float_as_uint(x + 0.f);
     return isnan(x) ? 0u : u ^ (u >> 31 ? 0xffffffffu : 0x80000000u);
 }
+// And back (0 and NaN as the numbers that ordered() takes them for).
+__device__ __forceinline__ float weight_of(uint32_t key) {
+    return __uint_as_float(key >> 31 ? key ^ 0x80000000u : ~key);
+}
 
 constexpr int kBinBits = 10, kBins = 1 << kBinBits;
+constexpr int kMaxKeys = 48 * 1024;   // weights that shared memory holds
 
 // A warp has a contiguous stretch of the weights, 32 neighbours an instruction, so that ranks
-// inside it are counts of ballots: up to kPer instructions' in registers, or (0) any number, read
-// again from L2 by each pass.  Bound by latency: the length and row, the weights, two or three
-// passes of three barriers each, two scans.
+// inside it are counts of ballots: up to kPer instructions' in registers, or (0) up to kMaxKeys in
+// shared memory, or (kBeyond) any number, read again from L2 by each pass.  Bound by
+// latency: the length and row, the weights, two or three passes of three barriers each, two scans.
+constexpr int kBeyond = -1;
 template <int kThreads, int kPer>
 __global__ void __launch_bounds__(kThreads) select_tokens_kernel(const ChooseParams p) {
     constexpr int kWarps = kThreads / 32, kOwn = kBins / kThreads;   // bins of a thread
     __shared__ __align__(16) uint32_t hist[kBins];
+    extern __shared__ uint32_t held[];   // kPer == 0: the keys between
     __shared__ uint32_t s_top[kWarps], s_low[kWarps], wsum[kWarps], wsum2[kWarps];
     __shared__ uint32_t s_bin, s_rank, s_count;
     // What moves the rows may be launched: it waits for this grid's end.
@@ -66,19 +73,24 @@ __global__ void __launch_bounds__(kThreads) select_tokens_kernel(const ChoosePar
     float* to = p.new_weights ? p.new_weights + ((int64_t)row * p.Hkv + g) * p.width : nullptr;
     const int32_t k = p.keep - p.first - p.last, m = n - p.first - p.last;   // k < m where tokens go
     const bool choose = n > p.keep && k > 0;
-    const int32_t per = kPer ? kPer : (m + kThreads - 1) / kThreads;
+    const int32_t per = kPer > 0 ? kPer : (m + kThreads - 1) / kThreads;
     const int32_t beg = warp * per * 32 + lane;
-    float own[kPer ? kPer : 1];
+    uint32_t own[kPer > 0 ? kPer : 1];
+    auto key_at = [&](int32_t j) { return ordered(pa::ld_behind_wait(w + p.first + j)); };
     if constexpr (kPer > 0)
 #pragma unroll
         for (int q = 0; q < kPer; ++q)
-            own[q] = choose && beg + q * 32 < m ? pa::ld_behind_wait(w + p.first + beg + q * 32) : 0.f;
+            own[q] = choose && beg + q * 32 < m ? key_at(beg + q * 32) : 0u;
+    if constexpr (kPer == 0)
+        if (choose)
+#pragma unroll 8
+            for (int32_t j = tid; j < m; j += kThreads) held[j] = key_at(j);
     const int32_t head = n <= p.keep ? n : p.first;
     for (int32_t j = tid; j < head; j += kThreads) kept[j] = j;
     if (n > p.keep)
         for (int32_t j = tid; j < p.last; j += kThreads) kept[p.keep - p.last + j] = n - p.last + j;
     if (choose) {
-        // f(weight, place, whether there is one), for whole warps
+        // f(key, place, whether there is one), for whole warps
         auto each = [&](auto f) {
             if constexpr (kPer > 0) {
 #pragma unroll
@@ -87,16 +99,16 @@ __global__ void __launch_bounds__(kThreads) select_tokens_kernel(const ChoosePar
 #pragma unroll 4
                 for (int32_t q = 0; q < per; ++q) {
                     const int32_t j = beg + q * 32;
-                    f(j < m ? pa::ld_behind_wait(w + p.first + j) : 0.f, j, j < m);
+                    f(j >= m ? 0u : kPer == 0 ? held[j] : key_at(j), j, j < m);
                 }
             }
         };
         uint32_t top = 0, low = 0;    // the largest key, and the smallest's complement
         for (int b = tid; b < kBins; b += kThreads) hist[b] = 0;
-        each([&](float x, int32_t, bool is) {
-            if (!is) return;
-            top = max(top, ordered(x));
-            low = max(low, ~ordered(x));
+        if constexpr (kPer == 0) __syncthreads();
+        each([&](uint32_t x, int32_t, bool is) {
+            top = max(top, x);        // 0 where there is none
+            if (is) low = max(low, ~x);
         });
         top = __reduce_max_sync(0xffffffffu, top);
         low = __reduce_max_sync(0xffffffffu, low);
@@ -111,9 +123,9 @@ __global__ void __launch_bounds__(kThreads) select_tokens_kernel(const ChoosePar
         int shift = max(0, width - kBinBits);
         uint32_t rank = (uint32_t)k, limit, ties;      // chosen: keys above limit, and `ties` equal ones
         for (;;) {
-            each([&](float x, int32_t, bool is) {
-                const uint32_t y = ordered(x) - base;  // keys below base wrap to large numbers
-                if (is && (width == 32 || (y >> width) == 0)) atomicAdd(&hist[y >> shift], 1u);
+            each([&](uint32_t x, int32_t, bool is) {
+                x -= base;                             // keys below base wrap to large numbers
+                if (is && (width == 32 || (x >> width) == 0)) atomicAdd(&hist[x >> shift], 1u);
             });
             __syncthreads();
             // Counts from the top: thread t owns kOwn bins, those of thread 0 the highest.
@@ -150,14 +162,14 @@ __global__ void __launch_bounds__(kThreads) select_tokens_kernel(const ChoosePar
             __syncthreads();
             base += s_bin << shift;
             rank = s_rank;
-            if (shift == 0) {
-                limit = base;
-                ties = rank;
-                break;
-            }
             if (rank == s_count && base > 0) {   // the whole bin is wanted
                 limit = base - 1;
                 ties = 0;
+                break;
+            }
+            if (shift == 0) {
+                limit = base;
+                ties = rank;
                 break;
             }
             width = shift;
@@ -165,33 +177,48 @@ __global__ void __launch_bounds__(kThreads) select_tokens_kernel(const ChoosePar
         }
         // ---- positions in order
         uint32_t above = 0, equal = 0;
-        each([&](float x, int32_t, bool is) {
-            above += __popc(__ballot_sync(0xffffffffu, is && ordered(x) > limit));
-            equal += __popc(__ballot_sync(0xffffffffu, is && ordered(x) == limit));
+        each([&](uint32_t x, int32_t, bool is) {
+            above += is && x > limit;
+            if (ties) equal += is && x == limit;
         });
+        above = __reduce_add_sync(0xffffffffu, above);
+        equal = __reduce_add_sync(0xffffffffu, equal);
         if (lane == 0) {
             wsum[warp] = above;
             wsum2[warp] = equal;
         }
         __syncthreads();
-        uint32_t a = __reduce_add_sync(0xffffffffu, lane < warp ? wsum[lane % kWarps] : 0u);
-        uint32_t e = __reduce_add_sync(0xffffffffu, lane < warp ? wsum2[lane % kWarps] : 0u);
-        each([&](float x, int32_t j, bool is) {
-            const uint32_t up = __ballot_sync(0xffffffffu, is && ordered(x) > limit);
-            const uint32_t eq = __ballot_sync(0xffffffffu, is && ordered(x) == limit);
-            const uint32_t my_e = e + __popc(eq & below);
-            if (up >> lane & 1 || (eq >> lane & 1 && my_e < ties)) {
-                const uint32_t at = p.first + a + __popc(up & below) + min(my_e, ties);
-                kept[at] = p.first + j;
-                if (kPer > 0 && to) to[at] = x;    // every weight between is in registers by now
-            }
-            a += __popc(up);
-            e += __popc(eq);
-        });
+        uint32_t a = p.first + __reduce_add_sync(0xffffffffu, lane < warp ? wsum[lane % kWarps] : 0u);
+        if (!ties) {
+            each([&](uint32_t x, int32_t j, bool is) {
+                const bool take = is && x > limit;
+                const uint32_t up = __ballot_sync(0xffffffffu, take);
+                if (take) {
+                    const uint32_t at = a + __popc(up & below);
+                    kept[at] = p.first + j;
+                    if (kPer >= 0 && to) to[at] = weight_of(x);   // every weight between has been read by now
+                }
+                a += __popc(up);
+            });
+        } else {
+            uint32_t e = __reduce_add_sync(0xffffffffu, lane < warp ? wsum2[lane % kWarps] : 0u);
+            each([&](uint32_t x, int32_t j, bool is) {
+                const uint32_t up = __ballot_sync(0xffffffffu, is && x > limit);
+                const uint32_t eq = __ballot_sync(0xffffffffu, is && x == limit);
+                const uint32_t my_e = e + __popc(eq & below);
+                if (up >> lane & 1 || (eq >> lane & 1 && my_e < ties)) {
+                    const uint32_t at = a + __popc(up & below) + min(my_e, ties);
+                    kept[at] = p.first + j;
+                    if (kPer >= 0 && to) to[at] = weight_of(x);
+                }
+                a += __popc(up);
+                e += __popc(eq);
+            });
+        }
     }
     if (!to) return;
     // The other kept weights move down, kept[r] >= r: a stretch is read before any of it is written.
-    const bool rest = !(kPer > 0 && choose);
+    const bool rest = !(kPer >= 0 && choose);
     for (int32_t r = tid; r - tid < count; r += kThreads) {
         if (!rest && r - tid >= p.first && r - tid + kThreads <= p.keep - p.last) continue;
         const bool mine = r < count && (rest || r < p.first || r >= p.keep - p.last);
@@ -282,7 +309,8 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) compact_kernel(cons
 }
 
 template <typename K, typename P>
-pa_status launch_early(K kern, dim3 grid, int threads, int cluster, cudaStream_t stream, const P& p) {
+pa_status launch_early(K kern, dim3 grid, int threads, int cluster, size_t smem, cudaStream_t stream,
+                       const P& p) {
     cudaLaunchAttribute attr[2] = {};
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -292,6 +320,7 @@ pa_status launch_early(K kern, dim3 grid, int threads, int cluster, cudaStream_t
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = grid;
     cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = cluster > 0 ? 2 : 1;
@@ -324,10 +353,13 @@ PA_API pa_status pa_select_tokens(const float* weights, int32_t num_rows, int32_
     const dim3 grid((unsigned)Hkv, (unsigned)B);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const int64_t most = (int64_t)width - first - last;   // weights to choose from, at most
-    if (most <= 4 * 256) return launch_early(select_tokens_kernel<256, 4>, grid, 256, 0, st, p);
-    if (most <= 8 * 1024) return launch_early(select_tokens_kernel<1024, 8>, grid, 1024, 0, st, p);
-    if (most <= 24 * 1024) return launch_early(select_tokens_kernel<1024, 24>, grid, 1024, 0, st, p);
-    return launch_early(select_tokens_kernel<1024, 0>, grid, 1024, 0, st, p);
+    if (most <= 4 * 256) return launch_early(select_tokens_kernel<256, 4>, grid, 256, 0, 0, st, p);
+    if (most <= 8 * 1024) return launch_early(select_tokens_kernel<1024, 8>, grid, 1024, 0, 0, st, p);
+    if (most > kMaxKeys) return launch_early(select_tokens_kernel<1024, kBeyond>, grid, 1024, 0, 0, st, p);
+    auto kern = select_tokens_kernel<1024, 0>;
+    static pa::DeviceOnce once;
+    if (!pa::allow_smem(once, kern, kMaxKeys * 4)) return PA_ERR_CUDA;
+    return launch_early(kern, grid, 1024, 0, (size_t)most * 4, st, p);
 }
 
 PA_API pa_status pa_compact_tokens(void* k_cache, void* v_cache, const int32_t* kept,
@@ -356,15 +388,16 @@ PA_API pa_status pa_compact_tokens(void* k_cache, void* v_cache, const int32_t* 
     if (!sms) return PA_ERR_CUDA;
     const int64_t pairs = (int64_t)B * Hkv;
     if (pairs > INT32_MAX / 8) return PA_ERR_UNSUPPORTED;
-    // Up to eight CTAs a pair, as many as its rows fill; of 1024 threads where even so there is
-    // less than one for every SM.
+    // Up to eight CTAs a pair, as many as its rows fill; of more threads where there are too few
+    // of them to fill the SMs with 1024 each.
     int cluster = 1;
     const int small = 256 / p.vecs * kMove;
     while (cluster < 8 && (int64_t)cluster * small < keep) cluster *= 2;
     const dim3 grid((unsigned)(pairs * cluster));
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (pairs * cluster <= sms) return launch_early(compact_kernel<1024>, grid, 1024, cluster, st, p);
-    return launch_early(compact_kernel<256>, grid, 256, cluster, st, p);
+    if (pairs * cluster <= sms) return launch_early(compact_kernel<1024>, grid, 1024, cluster, 0, st, p);
+    if (pairs * cluster <= 3 * sms) return launch_early(compact_kernel<512>, grid, 512, cluster, 0, st, p);
+    return launch_early(compact_kernel<256>, grid, 256, cluster, 0, st, p);
 }
 
 }  // extern "C"
