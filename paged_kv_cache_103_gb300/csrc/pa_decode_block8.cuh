@@ -66,8 +66,13 @@ struct Block8Params {
 // The forms of the kernel by query heads of a KV head: one; up to 4; up to 8; up to 16.
 enum Form { kG1, kG4, kG8, kG16 };
 constexpr Form form_of(int G) { return G == 1 ? kG1 : G <= 4 ? kG4 : G <= 8 ? kG8 : kG16; }
+// One CTA per SM, of as many warps as the registers of a chunk leave: at d = 128 twelve of
+// 168, at d = 64 sixteen of 128; where 9 .. 16 heads need two 8-wide MMA tiles and twice the
+// accumulators eight of 255 at d = 128, and at d = 64 twelve, which spill (16 x 32768 tokens of 8 KV
+// heads, G = 16: INT8 120 us, E4M3 108; with eight, which do not, 126 and 116; ten leave the four
+// schedulers uneven: 137 and 126).
 __host__ __device__ constexpr int max_warps(int D, int form) {
-    return form == kG16 ? 8 : D == 128 ? 12 : 16;
+    return form == kG16 ? (D == 128 ? 8 : 12) : D == 128 ? 12 : 16;
 }
 constexpr uint32_t kSmemBudget = 227 * 1024;
 
