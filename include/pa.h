@@ -849,7 +849,7 @@ PA_API pa_status pa_decode_noalloc(const void* q, const void* k_cache, const voi
  * last block is copied before it is written), one host->device copy of the
  * step's inputs and tables, pa_copy_blocks when copy-on-write arises,
  * pa_reshape_and_cache, pa_decode and one device->host copy of the output
- * (their _fp8 / _int8 / _int4 forms over a quantised cache).
+ * (their _fp8 / _int8 / _int4 / _fp8_block / _int8_block forms over a quantised cache).
  * The two kernels are captured once per slot, at creation, into a CUDA graph
  * owned by the executor and replayed every step on the caller's stream; the
  * input copy runs on the executor's own copy-in stream and the output copy on
@@ -881,7 +881,10 @@ typedef struct pa_step_desc {
     float scale;              /* attention scale, 1/sqrt(d) for the pages' formula */
     int32_t q8;               /* 8-bit cache with per-(token, KV head) scales (d = 128):
                                  0 none, 1 E4M3 (pa_decode_fp8), 2 INT8 (pa_decode_int8);
-                                 4: a 4-bit cache (pa_decode_int4, d = 64 or 128) */
+                                 4: a 4-bit cache (pa_decode_int4, d = 64 or 128);
+                                 17, 18: a block-scaled cache of E4M3 or INT8 codes
+                                 (pa_decode_fp8_block, pa_decode_int8_block, d = 64 or 128,
+                                 Hkv a multiple of 4) */
     int32_t depth;            /* staging slots (and graphs): 1 or 2 */
 } pa_step_desc;
 
@@ -898,8 +901,8 @@ PA_API pa_status pa_step_layout_get(const pa_step_desc* desc, pa_step_layout* ou
 /* Creates an executor for one layer's caches k_cache / v_cache (device,
  * [num_blocks][block_size][Hkv][d], dtype or, with q8, uint8 codes plus
  * k_scale / v_scale [num_blocks][Hkv][block_size] fp32 or, with q8 == 4, codes
- * and f16 scales as pa_reshape_and_cache_int4 lays them out; the scales are NULL
- * otherwise) and the allocator alloc (all must outlive it).  workspace (device, >= pa_decode_workspace_size(B, H, d) bytes, zeroed
+ * and f16 scales as pa_reshape_and_cache_int4 lays them out or, with q8 17 or 18, codes and
+ * fp32 scales as pa_reshape_and_cache_fp8_block does; the scales are NULL otherwise) and the allocator alloc (all must outlive it).  workspace (device, >= pa_decode_workspace_size(B, H, d) bytes, zeroed
  * once) is the decode's.  Captures the graph on a private stream; nothing
  * runs.  PA_ERR_INVALID for bad arguments, misaligned staging, or an allocator
  * whose pool size or block size differs from desc's. */

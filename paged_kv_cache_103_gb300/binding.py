@@ -1037,21 +1037,28 @@ class Step:
     or :meth:`submit` / :meth:`wait` to overlap the next step's host work with
     this one's device work.  With ``kv_format`` "fp8" or "int8" the caches
     are 8-bit codes (uint8) with ``k_scale``/``v_scale``, with "int4" the 4-bit
-    codes and scales of ``pa_reshape_and_cache_int4``, and ``dtype`` gives
-    the 16-bit type of the inputs."""
+    codes and scales of ``pa_reshape_and_cache_int4``, with "fp8_block" or "int8_block"
+    those of ``pa_reshape_and_cache_fp8_block`` / ``_int8_block`` (``Hkv`` a multiple of
+    4), and ``dtype`` gives the 16-bit type of the inputs."""
 
     def __init__(self, alloc: Allocator, B: int, H: int, Hkv: int, d: int, max_blocks: int,
                  max_context_len: int, k_cache, v_cache, scale: float, k_scale=None,
                  v_scale=None, dtype=None, depth: int = 1, kv_format: str = "native"):
         import torch
         self._lib = load()
-        q8 = {"native": 0, "fp8": 1, "int8": 2, "int4": 4}[kv_format]
-        int4 = kv_format == "int4"
-        N, bs = int(k_cache.shape[0]), int(k_cache.shape[2 if int4 else 1])
+        q8 = {"native": 0, "fp8": 1, "int8": 2, "int4": 4, "fp8_block": 17,
+              "int8_block": 18}[kv_format]
+        int4, block8 = kv_format == "int4", q8 >= 17
+        N, bs = int(k_cache.shape[0]), int(k_cache.shape[2 if int4 or block8 else 1])
         if int4:
             if (tuple(k_cache.shape) != (N, Hkv, bs, d // 2) or v_cache.shape != k_cache.shape
                     or d % 64):
                 raise ValueError("4-bit caches must be [num_blocks, Hkv, block_size, d / 2]")
+        elif block8:
+            if (tuple(k_cache.shape) != (N, Hkv, bs, d) or v_cache.shape != k_cache.shape
+                    or Hkv % 4):
+                raise ValueError("block-scaled caches must be [num_blocks, Hkv, block_size, d], "
+                                 "Hkv a multiple of 4")
         elif tuple(k_cache.shape) != (N, bs, Hkv, d) or v_cache.shape != k_cache.shape:
             raise ValueError("caches must be [num_blocks, block_size, Hkv, d]")
         if q8 and (k_scale is None or v_scale is None or
@@ -1066,7 +1073,7 @@ class Step:
         if not q8 and (k_scale is not None or v_scale is not None):
             raise ValueError("scales given for a 16-bit cache: pass kv_format")
         scale_dt = torch.float16 if int4 else torch.float32
-        scale_shape = (N, Hkv, bs, d // 64, 2) if int4 else (N, Hkv, bs)
+        scale_shape = (N, Hkv, bs, d // 64, 2) if int4 else (N, Hkv) if block8 else (N, Hkv, bs)
         if q8 and (tuple(k_scale.shape) != scale_shape or tuple(v_scale.shape) != scale_shape
                    or k_scale.dtype != scale_dt or v_scale.dtype != scale_dt):
             raise ValueError("scales must be %s %s" % (scale_dt, scale_shape))

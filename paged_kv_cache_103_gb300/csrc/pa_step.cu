@@ -22,7 +22,9 @@
 namespace {
 
 constexpr int kMaxDepth = 2;
-constexpr int kInt4 = 4;   // pa_step_desc.q8 of a 4-bit cache
+// pa_step_desc.q8 of a 4-bit cache and of the block-scaled 8-bit ones
+constexpr int kInt4 = 4, kFp8Block = 17, kInt8Block = 18;
+bool block_scaled(int q8) { return q8 == kFp8Block || q8 == kInt8Block; }
 
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
@@ -33,7 +35,9 @@ bool desc_ok(const pa_step_desc* d) {
            d->num_blocks > 0 && d->max_blocks > 0 && d->max_context_len > 0 &&
            (int64_t)d->max_context_len <= (int64_t)d->max_blocks * d->block_size &&
            (d->dtype == PA_F16 || d->dtype == PA_BF16) && d->q8 >= 0 &&
-           (d->q8 <= 2 || d->q8 == kInt4) && (d->q8 == 0 || d->q8 == kInt4 || d->d == 128) &&
+           (d->q8 <= 2 || d->q8 == kInt4 || block_scaled(d->q8)) &&
+           (d->q8 == 0 || d->q8 == kInt4 || block_scaled(d->q8) || d->d == 128) &&
+           (!block_scaled(d->q8) || d->Hkv % 4 == 0) &&   // a block's scales are copied 16 bytes at a time
            d->depth >= 1 && d->depth <= kMaxDepth;
 }
 
@@ -102,7 +106,10 @@ pa_status capture(pa_step* s, int i, void* workspace, size_t ws_bytes, cudaStrea
                                        s->k_scale, s->v_scale, d->num_blocks, d->block_size, d->Hkv,
                                        d->d, d->dtype, cap);
     else if (d->q8)
-        st = (d->q8 == 1 ? pa_reshape_and_cache_fp8 : pa_reshape_and_cache_int8)(
+        st = (d->q8 == 1            ? pa_reshape_and_cache_fp8
+              : d->q8 == kFp8Block  ? pa_reshape_and_cache_fp8_block
+              : d->q8 == kInt8Block ? pa_reshape_and_cache_int8_block
+                                    : pa_reshape_and_cache_int8)(
             g + L.k_new, g + L.v_new, slots, d->B, s->k_cache, s->v_cache, ks, vs, d->num_blocks,
             d->block_size, d->Hkv, d->d, d->dtype, cap);
     else
@@ -114,7 +121,10 @@ pa_status capture(pa_step* s, int i, void* workspace, size_t ws_bytes, cudaStrea
                             d->block_size, d->num_blocks, d->scale, d->dtype, g + L.out, workspace,
                             ws_bytes, cap);
     else if (st == PA_OK && d->q8)
-        st = (d->q8 == 1 ? pa_decode_fp8 : pa_decode_int8)(
+        st = (d->q8 == 1            ? pa_decode_fp8
+              : d->q8 == kFp8Block  ? pa_decode_fp8_block
+              : d->q8 == kInt8Block ? pa_decode_int8_block
+                                    : pa_decode_int8)(
             g + L.q, s->k_cache, s->v_cache, ks, vs, tables, d->max_blocks, lens, d->max_context_len,
             d->B, d->H, d->Hkv, d->d, d->block_size, d->num_blocks, d->scale, d->dtype, g + L.out,
             workspace, ws_bytes, cap);
@@ -190,7 +200,10 @@ PA_API pa_status pa_step_create(const pa_step_desc* d, pa_allocator* alloc, void
     s->dev = static_cast<unsigned char*>(dev_stage);
     const int64_t rows = (int64_t)d->block_size * d->Hkv;
     s->block_bytes = d->q8 == kInt4 ? rows * d->d / 2 : rows * d->d * (d->q8 ? 1 : 2);
-    s->scale_bytes = d->q8 == kInt4 ? rows * (d->d / 64) * 4 : d->q8 ? rows * 4 : 0;
+    s->scale_bytes = d->q8 == kInt4         ? rows * (d->d / 64) * 4
+                     : block_scaled(d->q8) ? (int64_t)d->Hkv * 4
+                     : d->q8               ? rows * 4
+                                           : 0;
     s->submitted = 0;
     s->in_stream = s->out_stream = nullptr;
     for (int i = 0; i < kMaxDepth; ++i) {
