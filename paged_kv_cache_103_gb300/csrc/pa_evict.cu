@@ -85,6 +85,8 @@ __global__ void __launch_bounds__(kThreads) select_tokens_kernel(const ChoosePar
         if (choose)
 #pragma unroll 8
             for (int32_t j = tid; j < m; j += kThreads) held[j] = key_at(j);
+    // Of the last ones, a thread's first weight.
+    const float tail = to && n > p.keep && tid < p.last ? pa::ld_behind_wait(w + n - p.last + tid) : 0.f;
     const int32_t head = n <= p.keep ? n : p.first;
     for (int32_t j = tid; j < head; j += kThreads) kept[j] = j;
     if (n > p.keep)
@@ -217,17 +219,24 @@ __global__ void __launch_bounds__(kThreads) select_tokens_kernel(const ChoosePar
         }
     }
     if (!to) return;
-    // The other kept weights move down, kept[r] >= r: a stretch is read before any of it is written.
-    const bool rest = !(kPer >= 0 && choose);
-    for (int32_t r = tid; r - tid < count; r += kThreads) {
-        if (!rest && r - tid >= p.first && r - tid + kThreads <= p.keep - p.last) continue;
-        const bool mine = r < count && (rest || r < p.first || r >= p.keep - p.last);
-        __syncthreads();
-        const float x = mine ? pa::ld_behind_wait(w + kept[r]) : 0.f;
-        __syncthreads();
-        if (mine) to[r] = x;
-    }
+    // The weights move down, to r from kept[r] >= r: what a place held has been read, or is the
+    // place's own.
     __syncthreads();
+    if (to != w)
+        for (int32_t r = tid; r < head; r += kThreads) to[r] = pa::ld_behind_wait(w + r);
+    if (n > p.keep) {
+        auto move = [&](int32_t r0, int32_t r1, auto from) {   // a stretch is read before any of it is written
+            for (int32_t r = r0 + tid; r - tid < r1; r += kThreads) {
+                const float x = r < r1 ? pa::ld_behind_wait(w + from(r)) : 0.f;
+                __syncthreads();
+                if (r < r1) to[r] = x;
+                __syncthreads();
+            }
+        };
+        if (kPer == kBeyond && choose) move(p.first, p.keep - p.last, [&](int32_t r) { return kept[r]; });
+        if (tid < p.last) to[p.keep - p.last + tid] = tail;
+        if (p.last > kThreads) move(p.keep - p.last + kThreads, p.keep, [&](int32_t r) { return n - p.keep + r; });
+    }
     for (int32_t r = count + tid; r < p.width; r += kThreads) to[r] = 0.f;
 }
 
@@ -262,23 +271,20 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) compact_kernel(cons
     const int rows = kThreads / p.vecs, r0 = threadIdx.x / p.vecs, c = threadIdx.x % p.vecs;
     const int32_t stretch = rows * kMove * (int32_t)ctas;   // of the cluster
     auto piece = [&](int32_t slot) { return ((int64_t)slot * p.Hkv + g) * p.vecs + c; };
-#pragma unroll 1
-    for (int32_t base = 0; base < n; base += min(stretch, n - base)) {
-        uint4 k[kMove], v[kMove];
-        int32_t to[kMove], from[kMove];   // slots; -1: not this row
-        const int32_t at = base + (int32_t)rank * rows * kMove + r0;   // < 2^31 + 2^13: as an unsigned number
+    int32_t from[kMove], to[kMove];   // slots of this thread's rows of a stretch; to -1: not moved
+    auto places = [&](int32_t base) {
+        const uint32_t at = (uint32_t)base + rank * rows * kMove + r0;   // < 2^31 + 2^14
 #pragma unroll
         for (int u = 0; u < kMove; ++u) {
-            const uint32_t r = (uint32_t)at + u * rows;
-            from[u] = to[u] = -1;
-            if (r < (uint32_t)n) from[u] = pa::ld_behind_wait(kept + r);
+            const uint32_t r = at + u * rows;
+            from[u] = r < (uint32_t)n ? pa::ld_behind_wait(kept + r) : -1;
         }
 #pragma unroll
         for (int u = 0; u < kMove; ++u) {
-            const uint32_t r = (uint32_t)at + u * rows;
+            const uint32_t r = at + u * rows;
+            to[u] = -1;
             if (r >= (uint32_t)n) continue;
             const int32_t pos = from[u], sb = pos >> p.bs_shift, db = (int32_t)(r >> p.bs_shift);
-            from[u] = -1;
             if (pos < 0 || sb >= p.max_blocks || db >= p.new_max_blocks) {
                 pa::raise_error(p.err, PA_DEVERR_TABLE_WIDTH);
                 continue;
@@ -288,22 +294,41 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) compact_kernel(cons
                 pa::raise_error(p.err, PA_DEVERR_BLOCK_ID);
                 continue;
             }
-            to[u] = (dst << p.bs_shift) + (int32_t)(r & mask);
             from[u] = (src << p.bs_shift) + (pos & mask);
+            to[u] = (dst << p.bs_shift) + (int32_t)(r & mask);
             if (from[u] == to[u]) to[u] = -1;   // stays
         }
+    };
+    if (n > 0) places(0);
+#pragma unroll 1
+    for (int32_t base = 0; base < n;) {
+        uint4 k[kMove], v[kMove];
+        int32_t now[kMove];
 #pragma unroll
         for (int u = 0; u < kMove; ++u)
             if (to[u] >= 0) k[u] = pa::ld_behind_wait(p.k_cache + piece(from[u]));
 #pragma unroll
-        for (int u = 0; u < kMove; ++u)
+        for (int u = 0; u < kMove; ++u) {
             if (to[u] >= 0) v[u] = pa::ld_behind_wait(p.v_cache + piece(from[u]));
-        asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+            now[u] = to[u];
+        }
+        // The next stretch's places, three loads one behind the other, while these rows travel.
+        base += min(stretch, n - base);
+        if (base < n) places(base);
+        // What is read must have arrived before the others may write over it, which a use of it
+        // sees to; the writes before need not be anywhere (a release waits for them: 186 us for
+        // 171, 256 pairs of 4096 rows).
+        uint32_t use = 0;
 #pragma unroll
         for (int u = 0; u < kMove; ++u)
-            if (to[u] >= 0) {
-                p.k_cache[piece(to[u])] = k[u];
-                p.v_cache[piece(to[u])] = v[u];
+            if (now[u] >= 0) use |= k[u].x | v[u].x;
+        asm volatile("" ::"r"(use) : "memory");
+        asm volatile("barrier.cluster.arrive.relaxed.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+#pragma unroll
+        for (int u = 0; u < kMove; ++u)
+            if (now[u] >= 0) {
+                p.k_cache[piece(now[u])] = k[u];
+                p.v_cache[piece(now[u])] = v[u];
             }
     }
 }
@@ -388,11 +413,13 @@ PA_API pa_status pa_compact_tokens(void* k_cache, void* v_cache, const int32_t* 
     if (!sms) return PA_ERR_CUDA;
     const int64_t pairs = (int64_t)B * Hkv;
     if (pairs > INT32_MAX / 8) return PA_ERR_UNSUPPORTED;
-    // Up to eight CTAs a pair, as many as its rows fill; of more threads where there are too few
+    // CTAs of a pair: as many as its rows fill, until there are four of 256 threads for every SM,
+    // eight at most (2560 pairs of 512 rows: one 202 us, two 201, four 224, eight 261; 512 of 1024:
+    // 94, 87, 88, 97; 256 of 4096: 172, 184, 169, 171); of more threads where there are too few
     // of them to fill the SMs with 1024 each.
-    int cluster = 1;
     const int small = 256 / p.vecs * kMove;
-    while (cluster < 8 && (int64_t)cluster * small < keep) cluster *= 2;
+    int cluster = 1;
+    while (cluster < 8 && (int64_t)cluster * small < keep && pairs * cluster < 4 * sms) cluster *= 2;
     const dim3 grid((unsigned)(pairs * cluster));
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (pairs * cluster <= sms) return launch_early(compact_kernel<1024>, grid, 1024, cluster, 0, st, p);
