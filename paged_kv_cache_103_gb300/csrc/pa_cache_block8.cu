@@ -129,6 +129,23 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendParams p) 
         const int64_t s = t >= 0 && t < T ? __ldg(p.slots + t) : -1;
         return s < p.num_slots ? s : -1;
     };
+    // The nearest written token before `t` (step -1: t - 1, t - 2, ..) or from t on (step 1), as a
+    // slot; -1: none.  512 entries at a time: a padded batch has thousands between two sequences.
+    auto nearest = [&](int32_t t, int step) {
+        constexpr int kWide = 16;
+        for (int32_t at = step < 0 ? t - 1 - lane : t + lane; step < 0 ? at + lane >= 0 : at - lane < T;
+             at += step * 32 * kWide) {
+            int64_t s[kWide];
+#pragma unroll
+            for (int q = 0; q < kWide; ++q) s[q] = slot_at(at + step * 32 * q);
+#pragma unroll
+            for (int q = 0; q < kWide; ++q) {
+                const uint32_t some = __ballot_sync(0xffffffffu, s[q] >= 0);
+                if (some) return __shfl_sync(0xffffffffu, s[q], __ffs(some) - 1);
+            }
+        }
+        return (int64_t)-1;
+    };
     // ---- leaders: the nearest written token before has another block
     const int64_t mine = lane < kWindow ? slot_at(t0 + lane) : -1;
     const int64_t before = slot_at(t0 - 32 + lane);
@@ -136,13 +153,8 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendParams p) 
         pa::raise_error(p.err, PA_DEVERR_SLOT);
     const uint32_t live = __ballot_sync(0xffffffffu, mine >= 0);
     if (!live) return;
-    uint32_t some = __ballot_sync(0xffffffffu, before >= 0);
-    int64_t last = some ? __shfl_sync(0xffffffffu, before, 31 - __clz(some)) : -1;
-    for (int32_t first = t0 - 64; !some && first > -32; first -= 32) {   // padding: further back
-        const int64_t s = slot_at(first + lane);
-        some = __ballot_sync(0xffffffffu, s >= 0);
-        if (some) last = __shfl_sync(0xffffffffu, s, 31 - __clz(some));
-    }
+    const uint32_t some = __ballot_sync(0xffffffffu, before >= 0);
+    const int64_t last = some ? __shfl_sync(0xffffffffu, before, 31 - __clz(some)) : nearest(t0 - 32, -1);
     const uint32_t lower = live & ((1u << lane) - 1);
     const int64_t prev = __shfl_sync(0xffffffffu, mine, lower ? 31 - __clz(lower) : 0);
     const int64_t prev_block = (lower ? prev : last) >> kShift;   // -1: none
@@ -168,7 +180,7 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendParams p) 
         const uint32_t other = any & ~same;
         uint32_t run = other ? same & ((other & -other) - 1) : same;
         const int32_t r_lane = (int32_t)(s & (kRows - 1));
-        if (other || t + 32 >= T || __popc(run) >= kRows) {
+        if (other || t + 32 >= T || __popc(run) >= kRows || nearest(t + 32, 1) >> kShift != block) {
             // These are all of them.  (A slot named twice would make more: those are left out.)
             uint2 w[kSteps];
             uint32_t written = __reduce_or_sync(0xffffffffu, run >> lane & 1 ? 1u << r_lane : 0u);

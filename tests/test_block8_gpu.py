@@ -142,6 +142,33 @@ def test_padding_and_bad_slots_between_the_tokens_of_a_block(fmt):
 
 
 @pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("d,dtype", [(64, F16), (128, BF16)])
+def test_padded_batches(fmt, d, dtype):
+    """Sequences padded to a common length, thousands of entries between the tokens of two of them and,
+    twice, between two tokens of one block."""
+    Hkv, bs, wide, lens = 3, 16, 2500, [40, 1, 0, 2500, 17, 16]
+    starts = [5, 0, 0, 9, 15, 0]
+    N = sum((s + n + bs - 1) // bs for s, n in zip(starts, lens)) + 1
+    flat, at = runs(lens, starts, bs, N, 4), 0
+    slots = np.full((len(lens), wide), -1, np.int64)
+    for i, n in enumerate(lens):
+        slots[i, :n] = flat[at: at + n]
+        at += n
+    slots[0, 2400] = slots[0, 39]                       # the last token far behind the one before
+    slots[0, 39] = -1
+    slots[4, [600, 1200, 1800]] = slots[4, [3, 4, 5]]   # tokens 3, 4, 5 of the second block, and no other
+    slots[4, 3: 17] = -1
+    slots = slots.reshape(-1)
+    host = empty(N, Hkv, bs, d)
+    on = dev(*host)
+    T = len(slots)
+    kn, vn = rows(T, Hkv, d, dtype, 1), rows(T, Hkv, d, dtype, 2)
+    both(fmt, kn, vn, slots, on, host)
+    same(on, host)
+    assert binding.pa_check_device_errors() == 0
+
+
+@pytest.mark.parametrize("fmt", FMTS)
 @pytest.mark.parametrize("T,bs,Hkv,d", [(1, 8, 1, 64), (77, 16, 3, 128), (1001, 32, 4, 64), (6000, 16, 8, 128)])
 def test_read_back_bit_exact(fmt, T, bs, Hkv, d):
     N = T // bs + 5
