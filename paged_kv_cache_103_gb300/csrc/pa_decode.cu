@@ -1580,7 +1580,9 @@ struct WeightsParams {
     int32_t B, Hkv, G, subs, num_rows, width;   // Hkv: the cache's
 };
 
-constexpr int kAddThreads = 256;
+// Three CTAs per SM, all of them resident at once: a second wave pays the start again (the 40-head
+// batch below takes 255 us in all with six, 240 with three, 242 with four, 241 with two).
+constexpr int kAddThreads = 256, kAddCtas = 3;
 
 constexpr int kAddChunks = 4;   // chunks of a warp at a time
 constexpr int kAddHeads = 4;    // query heads of them at a time
@@ -1588,7 +1590,7 @@ constexpr int kAddHeads = 4;    // query heads of them at a time
 // weights[row][g][j] += sum over the query heads h of g of 2^(s_hj - M_h) / L_h: a warp has a
 // contiguous share of the (sequence, KV head, chunk) list, a lane a token of each of four chunks.
 // The heads are added in order, no two warps touch the same weight.
-__global__ void __launch_bounds__(kAddThreads) add_weights_kernel(const WeightsParams p) {
+__global__ void __launch_bounds__(kAddThreads, kAddCtas) add_weights_kernel(const WeightsParams p) {
     asm volatile("griddepcontrol.wait;" ::: "memory");   // launched while the decode may run
     const int lane = threadIdx.x & 31;
     // the list's prefix, the rows (-1: takes no part) and lengths, all at once
@@ -1758,7 +1760,7 @@ PA_API pa_status pa_decode_weights(const void* q, const void* k_cache, const voi
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)(8 * pa::device_sm_count()));
+    cfg.gridDim = dim3((unsigned)(kAddCtas * pa::device_sm_count()));
     cfg.blockDim = dim3(kAddThreads);
     cfg.dynamicSmemBytes = (size_t)(3 * B + 1) * 4;
     static pa::DeviceOnce once;
