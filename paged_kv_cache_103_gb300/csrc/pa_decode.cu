@@ -239,7 +239,10 @@ __device__ __forceinline__ void q8x4_to_f16(uint32_t x, uint32_t& lo, uint32_t& 
 // kScores (pa_decode_weights): the base-2 logits go to memory as well, and with each query head's
 // maximum and sum add_weights_kernel makes them weights: a probability is known only when its
 // row's sum is.  Written once and read once, mostly in L2, they are 4 G bytes a (token, KV head)
-// beside the 4 d of K and V, where another pass over K would be 2 d.
+// beside the 4 d of K and V, where another pass over K would be 2 d.  Measured (device time, with
+// pa_decode's for the same batch): 64 x U[128, 2048] tokens, 40 heads, d = 128 244 us (221); 16 x
+// 16384 tokens, 8 KV heads of G = 4 187 (161; 67 MB of logits out and in again); 32 long-tailed
+// contexts, 4 KV heads of G = 7 47 (40).  Some 9 us of each are the weights' kernel.
 template <int D, bool kBF16, int NT, bool kAsync, bool kFp8, bool kInt8, bool kPair, bool kScores>
 __global__ void __launch_bounds__(cta_threads(kFp8), kCtasPerSm)
 paged_decode_kernel(const __grid_constant__ CUtensorMap kmap,

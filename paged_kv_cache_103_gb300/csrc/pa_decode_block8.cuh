@@ -12,12 +12,11 @@
 //    K's 128 leaves as the sums' first value, -128 sum q; V's as a product of its own, P times
 //    a tile of 128s, subtracted every four chunks, so that what the tensor cores cut off
 //    their sums they cut off both, and the sums stay small between two subtractions.
-//  * an E4M3 code goes to f16 by conversion for K, two an instruction.  For V its seven lower
-//    bits are put under a bf16's exponent, its sign above: the number times 2^-120, exactly,
-//    subnormals as subnormals, in 3.5 instructions for two codes.  The conversions alone would hold
-//    their pipe 8 of the 12 cycles that a token and KV head take at the memory's rate, half of
-//    them and this hold two pipes 4 each.
-// So P is bf16 in either case: P times the block's V scale goes in two parts, its upper half
+//  * an E4M3 code goes to f16 by conversion for K, two an instruction.  V has to be bf16, as P is
+//    and both operands of a product have one type, and there is no conversion to it: the code's
+//    seven lower bits are put under a bf16's exponent, its sign above, which is the number
+//    times 2^-120, exactly, subnormals as subnormals, in 3.5 instructions for two codes.
+// P is bf16 in either case: P times the block's V scale goes in two parts, its upper half
 // and what that leaves, rounded: 16 bits at every size that fp32 holds, however far blocks' scales
 // lie apart.  A power of two, from a run's first V scale, keeps the products clear of both ends
 // of fp32's range; only a scale 2^40 times that one changes it on the way.
@@ -26,6 +25,14 @@
 // 32-token chunks through a ring of its own in shared memory (pa_runs.cuh), by asynchronous
 // 16-byte copies that put each row's 16-byte columns where neither product's reads meet in a
 // bank, and by 4-byte copies of the blocks' scales.
+//
+// Measured (device time): 16 x 32768 tokens of 8 KV heads at d = 128, E4M3: G = 1 169 us, G = 4
+// 171 (6.3 TB/s, 94 % of the measured copy; DRAM traffic 1.003 times the bytes, 45 % of the
+// ALU's and 15 % of the tensor pipe's cycles, 40 % of the issue slots), G = 8 176, G = 16 185;
+// INT8: 172, 173, 174, 195; at d = 64 88 to 95 us up to G = 8; 64 sequences of 128 .. 2048 tokens,
+// 40 heads, G = 1: INT8 118 us, E4M3 116; 4 sequences of up to 64 tokens 6.8 us, all latency.
+// The caches with a scale per token take 159 us (E4M3) and 175 (INT8) for a 40-head batch of
+// nearly this size: a conversion and a factor per key, and loading warps to wait for.
 #pragma once
 
 #include <cuda_bf16.h>
