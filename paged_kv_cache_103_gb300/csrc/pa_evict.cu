@@ -40,18 +40,19 @@ constexpr int kBinBits = 10, kBins = 1 << kBinBits;
 constexpr int kMaxKeys = 48 * 1024;   // weights that shared memory holds
 
 // A warp has a contiguous stretch of the weights, 32 neighbours an instruction, so that ranks
-// inside it are counts of ballots: up to kPer instructions' in registers, or (0) up to kMaxKeys in
-// shared memory, or (kBeyond) any number, read again from L2 by each pass.  Bound by
+// inside it are counts of ballots: up to kPer instructions' in registers, more (an accumulator's width
+// says what there may be, its context's length what there is) in shared memory, up to kMaxKeys,
+// or read again from L2 by each pass.  Bound by
 // latency: the length and row, the weights, two or three passes of three barriers each, two
 // scans: 3.5 us for 20 pairs of up to 1000 weights, 12.3 for 256 of 8192, 21 for 32 of 30000.
 // (Eight counts a bin, one for every eighth lane, took 20 us for the 256 pairs, 13.4 then: the
 // counts' clearing and adding up costs more than lanes that meet in one.)
-constexpr int kBeyond = -1;
-template <int kThreads, int kPer>
+enum More { kNone, kShared, kAgain };
+template <int kThreads, int kPer, More kMore>
 __global__ void __launch_bounds__(kThreads) select_tokens_kernel(const ChooseParams p) {
     constexpr int kWarps = kThreads / 32, kOwn = kBins / kThreads;   // bins of a thread
     __shared__ __align__(16) uint32_t hist[kBins];
-    extern __shared__ uint32_t held[];   // kPer == 0: the keys between
+    extern __shared__ uint32_t held[];   // kShared: the keys between, where registers do not hold them
     __shared__ uint32_t s_top[kWarps], s_low[kWarps], wsum[kWarps], wsum2[kWarps];
     __shared__ uint32_t s_bin, s_rank, s_count;
     // What moves the rows may be launched: it waits for this grid's end.
@@ -76,16 +77,16 @@ __global__ void __launch_bounds__(kThreads) select_tokens_kernel(const ChoosePar
     float* to = p.new_weights ? p.new_weights + ((int64_t)row * p.Hkv + g) * p.width : nullptr;
     const int32_t k = p.keep - p.first - p.last, m = n - p.first - p.last;   // k < m where tokens go
     const bool choose = n > p.keep && k > 0;
-    const int32_t per = kPer > 0 ? kPer : (m + kThreads - 1) / kThreads;
+    const bool regs = kMore == kNone || m <= kPer * kThreads;
+    const int32_t per = regs ? kPer : (m + kThreads - 1) / kThreads;
     const int32_t beg = warp * per * 32 + lane;
-    uint32_t own[kPer > 0 ? kPer : 1];
+    uint32_t own[kPer];
     auto key_at = [&](int32_t j) { return ordered(pa::ld_behind_wait(w + p.first + j)); };
-    if constexpr (kPer > 0)
 #pragma unroll
-        for (int q = 0; q < kPer; ++q)
-            own[q] = choose && beg + q * 32 < m ? key_at(beg + q * 32) : 0u;
-    if constexpr (kPer == 0)
-        if (choose)
+    for (int q = 0; q < kPer; ++q)
+        own[q] = choose && regs && beg + q * 32 < m ? key_at(beg + q * 32) : 0u;
+    if constexpr (kMore == kShared)
+        if (choose && !regs)
 #pragma unroll 8
             for (int32_t j = tid; j < m; j += kThreads) held[j] = key_at(j);
     // Of the last ones, a thread's first weight.
@@ -97,20 +98,20 @@ __global__ void __launch_bounds__(kThreads) select_tokens_kernel(const ChoosePar
     if (choose) {
         // f(key, place, whether there is one), for whole warps
         auto each = [&](auto f) {
-            if constexpr (kPer > 0) {
+            if (regs) {
 #pragma unroll
                 for (int q = 0; q < kPer; ++q) f(own[q], beg + q * 32, beg + q * 32 < m);
-            } else {
+            } else if constexpr (kMore != kNone) {
 #pragma unroll 4
                 for (int32_t q = 0; q < per; ++q) {
                     const int32_t j = beg + q * 32;
-                    f(j >= m ? 0u : kPer == 0 ? held[j] : key_at(j), j, j < m);
+                    f(j >= m ? 0u : kMore == kShared ? held[j] : key_at(j), j, j < m);
                 }
             }
         };
         uint32_t top = 0, low = 0;    // the largest key, and the smallest's complement
         for (int b = tid; b < kBins; b += kThreads) hist[b] = 0;
-        if constexpr (kPer == 0) __syncthreads();
+        if constexpr (kMore == kShared) __syncthreads();
         each([&](uint32_t x, int32_t, bool is) {
             top = max(top, x);        // 0 where there is none
             if (is) low = max(low, ~x);
@@ -180,7 +181,8 @@ __global__ void __launch_bounds__(kThreads) select_tokens_kernel(const ChoosePar
             width = shift;
             shift = max(0, shift - kBinBits);
         }
-        // ---- positions in order
+        // ---- positions in order; the weights with them where every weight between has been read
+        const bool now = regs || kMore == kShared;
         uint32_t above = 0, equal = 0;
         each([&](uint32_t x, int32_t, bool is) {
             above += is && x > limit;
@@ -201,7 +203,7 @@ __global__ void __launch_bounds__(kThreads) select_tokens_kernel(const ChoosePar
                 if (take) {
                     const uint32_t at = a + __popc(up & below);
                     kept[at] = p.first + j;
-                    if (kPer >= 0 && to) to[at] = weight_of(x);   // every weight between has been read by now
+                    if (now && to) to[at] = weight_of(x);
                 }
                 a += __popc(up);
             });
@@ -214,7 +216,7 @@ __global__ void __launch_bounds__(kThreads) select_tokens_kernel(const ChoosePar
                 if (up >> lane & 1 || (eq >> lane & 1 && my_e < ties)) {
                     const uint32_t at = a + __popc(up & below) + min(my_e, ties);
                     kept[at] = p.first + j;
-                    if (kPer >= 0 && to) to[at] = weight_of(x);
+                    if (now && to) to[at] = weight_of(x);
                 }
                 a += __popc(up);
                 e += __popc(eq);
@@ -236,7 +238,7 @@ __global__ void __launch_bounds__(kThreads) select_tokens_kernel(const ChoosePar
                 __syncthreads();
             }
         };
-        if (kPer == kBeyond && choose) move(p.first, p.keep - p.last, [&](int32_t r) { return kept[r]; });
+        if (kMore == kAgain && choose && !regs) move(p.first, p.keep - p.last, [&](int32_t r) { return kept[r]; });
         if (tid < p.last) to[p.keep - p.last + tid] = tail;
         if (p.last > kThreads) move(p.keep - p.last + kThreads, p.keep, [&](int32_t r) { return n - p.keep + r; });
     }
@@ -383,10 +385,14 @@ PA_API pa_status pa_select_tokens(const float* weights, int32_t num_rows, int32_
     const dim3 grid((unsigned)Hkv, (unsigned)B);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const int64_t most = (int64_t)width - first - last;   // weights to choose from, at most
-    if (most <= 4 * 256) return launch_early(select_tokens_kernel<256, 4>, grid, 256, 0, 0, st, p);
-    if (most <= 8 * 1024) return launch_early(select_tokens_kernel<1024, 8>, grid, 1024, 0, 0, st, p);
-    if (most > kMaxKeys) return launch_early(select_tokens_kernel<1024, kBeyond>, grid, 1024, 0, 0, st, p);
-    auto kern = select_tokens_kernel<1024, 0>;
+    if (most <= 4 * 256) return launch_early(select_tokens_kernel<256, 4, kNone>, grid, 256, 0, 0, st, p);
+    if (most <= 8 * 1024) return launch_early(select_tokens_kernel<1024, 8, kNone>, grid, 1024, 0, 0, st, p);
+    // Wider rows: shared memory for all of them where each CTA has an SM to itself anyway.
+    const int sms = pa::device_sm_count();
+    if (!sms) return PA_ERR_CUDA;
+    if (most > kMaxKeys || (int64_t)B * Hkv > sms)
+        return launch_early(select_tokens_kernel<1024, 8, kAgain>, grid, 1024, 0, 0, st, p);
+    auto kern = select_tokens_kernel<1024, 8, kShared>;
     static pa::DeviceOnce once;
     if (!pa::allow_smem(once, kern, kMaxKeys * 4)) return PA_ERR_CUDA;
     return launch_early(kern, grid, 1024, 0, (size_t)most * 4, st, p);

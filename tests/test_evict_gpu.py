@@ -200,7 +200,8 @@ def check_select(weights, rows, lens, keep, first, last, in_place=False, flag=0)
 @pytest.mark.parametrize("Hkv,W,keep,first,last", [
     (1, 1, 1, 0, 0), (2, 40, 1, 0, 0), (2, 40, 1, 1, 0), (3, 100, 37, 4, 9), (1, 100, 20, 20, 0), (2, 100, 20, 0, 20),
     (2, 1000, 999, 1, 1), (2, 1000, 256, 0, 0), (8, 5000, 1234, 4, 100), (1, 9000, 33, 1, 1), (2, 40000, 20000, 4, 512),
-    (1, 70000, 4096, 4, 64)])
+    (1, 70000, 4096, 4, 64), (1, 800, 700, 5, 400), (1, 9000, 5000, 4, 3000), (1, 5000, 2048, 0, 2048),
+    (1, 30000, 9000, 2000, 3000), (1, 60000, 9000, 2000, 3000), (40, 12000, 5000, 10, 2000)])
 def test_select(in_place, Hkv, W, keep, first, last):
     rng = np.random.default_rng(W + keep)
     lens = sorted({W, max(1, W - 1), keep, min(W, keep + 1), max(keep - 1, 0), 0, W // 2})
@@ -235,6 +236,18 @@ def test_select_reports_and_leaves_out():
     check_select(w, [2, 4, 0], [50, 50, 30], 20, 2, 3, flag=E["SLOT"])
     check_select(w, [2, 3, 0], [50, -4, 30], 20, 2, 3, flag=E["CONTEXT"])
     check_select(w, [2, 3, 0], [50, 51, 2 ** 31 - 1], 20, 2, 3, flag=E["TABLE_WIDTH"])
+
+
+@pytest.mark.parametrize("pairs_each", [2, 100])
+@pytest.mark.parametrize("W", [20000, 100000])
+def test_select_short_contexts_of_wide_rows(W, pairs_each):
+    """What one launch's rows may hold is far more than its contexts do; one of them does hold it."""
+    rng = np.random.default_rng(W)
+    lens = [700, 8200, 8300, 30, W]
+    w = rng.standard_normal((5, pairs_each, W)).astype(np.float32)
+    w[1] = rng.integers(0, 4, (pairs_each, W))
+    for in_place in (False, True):
+        check_select(w, [3, 1, 0, 4, 2], lens, 600, 3, 50, in_place)
 
 
 def test_select_without_new_weights():
