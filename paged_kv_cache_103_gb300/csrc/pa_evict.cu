@@ -385,11 +385,17 @@ PA_API pa_status pa_select_tokens(const float* weights, int32_t num_rows, int32_
     const dim3 grid((unsigned)Hkv, (unsigned)B);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const int64_t most = (int64_t)width - first - last;   // weights to choose from, at most
-    if (most <= 4 * 256) return launch_early(select_tokens_kernel<256, 4, kNone>, grid, 256, 0, 0, st, p);
-    if (most <= 8 * 1024) return launch_early(select_tokens_kernel<1024, 8, kNone>, grid, 1024, 0, 0, st, p);
-    // Wider rows: shared memory for all of them where each CTA has an SM to itself anyway.
     const int sms = pa::device_sm_count();
     if (!sms) return PA_ERR_CUDA;
+    if (most <= 4 * 256) return launch_early(select_tokens_kernel<256, 4, kNone>, grid, 256, 0, 0, st, p);
+    if (most <= 8 * 256) return launch_early(select_tokens_kernel<256, 8, kNone>, grid, 256, 0, 0, st, p);
+    // Many pairs of which few tokens are wanted have contexts to match, whatever the rows' width:
+    // small CTAs (2560 pairs, 2048 weights in rows of 4096: 26 us, with 1024 threads each 84; 640 in rows
+    // of 40000: 30 and 41; but of 8192 weights 2560 pairs 135 and 108, 640 67 and 28).
+    if ((int64_t)B * Hkv > 4 * sms && keep <= 8 * 256)
+        return launch_early(select_tokens_kernel<256, 8, kAgain>, grid, 256, 0, 0, st, p);
+    if (most <= 8 * 1024) return launch_early(select_tokens_kernel<1024, 8, kNone>, grid, 1024, 0, 0, st, p);
+    // Wider rows: shared memory for all of them where each CTA has an SM to itself anyway.
     if (most > kMaxKeys || (int64_t)B * Hkv > sms)
         return launch_early(select_tokens_kernel<1024, 8, kAgain>, grid, 1024, 0, 0, st, p);
     auto kern = select_tokens_kernel<1024, 8, kShared>;

@@ -238,16 +238,16 @@ def test_select_reports_and_leaves_out():
     check_select(w, [2, 3, 0], [50, 51, 2 ** 31 - 1], 20, 2, 3, flag=E["TABLE_WIDTH"])
 
 
-@pytest.mark.parametrize("pairs_each", [2, 100])
+@pytest.mark.parametrize("pairs_each", [2, 100, 130])
 @pytest.mark.parametrize("W", [20000, 100000])
 def test_select_short_contexts_of_wide_rows(W, pairs_each):
     """What one launch's rows may hold is far more than its contexts do; one of them does hold it."""
     rng = np.random.default_rng(W)
-    lens = [700, 8200, 8300, 30, W]
-    w = rng.standard_normal((5, pairs_each, W)).astype(np.float32)
+    lens = [700, 8200, 2100, 30, W, 8300]
+    w = rng.standard_normal((6, pairs_each, W)).astype(np.float32)
     w[1] = rng.integers(0, 4, (pairs_each, W))
     for in_place in (False, True):
-        check_select(w, [3, 1, 0, 4, 2], lens, 600, 3, 50, in_place)
+        check_select(w, [3, 1, 0, 4, 2, 5], lens, 600, 3, 50, in_place)
 
 
 def test_select_without_new_weights():
