@@ -20,8 +20,11 @@
 // What bounds it: in a prompt HBM (3 bytes a value) and issue slots (some seven instructions
 // a value, 68 % of them taken) in a launch that is over before either is full; in a decode step
 // a chain of dependent loads (slots, rows and scale, earlier codes where the scale grows).
-// Measured at d = 128, with the read back of the blocks: 8192 x 8 rows, bf16, E4M3 24.2 us on the
-// device (100 MB: 4.1 TB/s), 64 x 40 rows, f16, INT8 10.2 us.
+// Measured at d = 128 (device time): 8192 x 8 rows, bf16, E4M3 15.1 us (50 MB: 3.3 TB/s), 32768 x 8
+// rows INT8 44.5 (201 MB: 4.5 TB/s), 64 x 40 rows of as many blocks, f16, INT8 5.3, one token 2.6.
+// Rows that are neighbours in the call and in the block, as they nearly always are, have places
+// by addition, and the divisions that an odd scale needs are out of the way of the others: with each
+// row's place from its bit and both ways to a code in every step it was 16.2, 53.0, 6.5 and 3.1.
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
@@ -93,15 +96,10 @@ struct Divider {
     }
 };
 
-// Quotients of a row's values and their codes.  |x| <= TOP s (1 + 2^-24): INT8 codes need
-// no clamp where the quotient is not that of a scale below the smallest normal float.
+// Four values' codes by a Divider that is fast.  |x| <= TOP s (1 + 2^-24): INT8 codes need no clamp.
 template <bool kBF16, bool kInt8>
-__device__ __forceinline__ uint32_t row_codes(uint2 w, const Divider& by) {
+__device__ __forceinline__ uint32_t codes_fast(uint2 w, const Divider& by) {
     const float2 p = widen2<kBF16>(w.x), q = widen2<kBF16>(w.y);
-    if (!by.fast) {
-        if (!(by.s > 0.f)) return 0u;
-        return code4<kInt8>(__fdiv_rn(p.x, by.s), __fdiv_rn(p.y, by.s), __fdiv_rn(q.x, by.s), __fdiv_rn(q.y, by.s));
-    }
     if constexpr (kInt8) {
         // 1.5 2^23 more, an fp32 number's low byte is the nearest integer's (ties to even)
         constexpr float kRound = 12582912.f;
@@ -111,6 +109,14 @@ __device__ __forceinline__ uint32_t row_codes(uint2 w, const Divider& by) {
     } else {
         return code4<false>(by(p.x), by(p.y), by(q.x), by(q.y));
     }
+}
+
+// The same by divisions, for any s >= 0; zeros for 0.
+template <bool kBF16, bool kInt8>
+__device__ __forceinline__ uint32_t codes_divided(uint2 w, float s) {
+    const float2 p = widen2<kBF16>(w.x), q = widen2<kBF16>(w.y);
+    if (!(s > 0.f)) return 0u;
+    return code4<kInt8>(__fdiv_rn(p.x, s), __fdiv_rn(p.y, s), __fdiv_rn(q.x, s), __fdiv_rn(q.y, s));
 }
 
 struct AppendParams {
@@ -192,22 +198,41 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendParams p) 
         const int32_t r_lane = (int32_t)(s & (kRows - 1));
         if (other || t + 32 >= T || __popc(run) >= kRows || nearest(t + 32, 1) >> kShift != block) {
             // These are all of them.  (A slot named twice would make more: those are left out.)
-            uint2 w[kSteps];
-            uint32_t written = __reduce_or_sync(0xffffffffu, run >> lane & 1 ? 1u << r_lane : 0u);
-            uint32_t todo = run, top2 = 0;
+            const int count = min(__popc(run), kRows), r0 = __shfl_sync(0xffffffffu, r_lane, 0);
+            const bool in_run = run >> lane & 1;
+            const uint32_t written = __reduce_or_sync(0xffffffffu, in_run ? 1u << r_lane : 0u);
+            // As a rule they are neighbours in the call and in the block.
+            const bool plain = !(run & (run + 1)) && __all_sync(0xffffffffu, !in_run || r_lane == r0 + lane);
+            // f(step, token from t on, row) for this lane's row of each step that has one
+            auto rows_of = [&](auto f) {
+                if (plain) {
 #pragma unroll
-            for (int q = 0; q < kSteps; ++q) {
-                const int a = __ffs(todo) - 1;
-                todo &= todo - 1;
-                int from = a;
-                if constexpr (kPer == 2) {
-                    const int b = __ffs(todo) - 1;
-                    todo &= todo - 1;
-                    from = sub ? b : a;
+                    for (int q = 0; q < kSteps; ++q)
+                        if (q * kPer + sub < count) f(q, q * kPer + sub, r0 + q * kPer + sub);
+                } else {
+                    uint32_t todo = run;
+#pragma unroll
+                    for (int q = 0; q < kSteps; ++q) {
+                        const int a = __ffs(todo) - 1;
+                        todo &= todo - 1;
+                        int from = a;
+                        if constexpr (kPer == 2) {
+                            const int b = __ffs(todo) - 1;
+                            todo &= todo - 1;
+                            from = sub ? b : a;
+                        }
+                        const int r = __shfl_sync(0xffffffffu, r_lane, from & 31);
+                        if (from >= 0) f(q, from, r);
+                    }
                 }
-                w[q] = make_uint2(0, 0);
-                if (from >= 0) w[q] = __ldg(x + ((int64_t)(t + from) * p.Hkv + h) * kLanes);
-            }
+            };
+            const uint2* mine_x = x + ((int64_t)t * p.Hkv + h) * kLanes;
+            const int64_t stride = (int64_t)p.Hkv * kLanes;
+            uint2 w[kSteps];
+#pragma unroll
+            for (int q = 0; q < kSteps; ++q) w[q] = make_uint2(0, 0);
+            rows_of([&](int q, int from, int) { w[q] = __ldg(mine_x + from * stride); });
+            uint32_t top2 = 0;
 #pragma unroll
             for (int q = 0; q < kSteps; ++q) {
                 top2 = pa::max_x2<kBF16>(top2, w[q].x & 0x7FFF7FFFu);
@@ -227,19 +252,14 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendParams p) 
                 }
             }
             const Divider by(now);
-            todo = run;
-#pragma unroll
-            for (int q = 0; q < kSteps; ++q) {
-                const int a2 = __ffs(todo) - 1;
-                todo &= todo - 1;
-                int from = a2;
-                if constexpr (kPer == 2) {
-                    const int b = __ffs(todo) - 1;
-                    todo &= todo - 1;
-                    from = sub ? b : a2;
+            if (by.fast) {
+                rows_of([&](int q, int, int r) { cache[r * kLanes] = codes_fast<kBF16, kInt8>(w[q], by); });
+            } else {
+#pragma unroll 1
+                for (uint32_t todo = run; todo; todo &= todo - 1) {
+                    const int from = __ffs(todo) - 1, r = __shfl_sync(0xffffffffu, r_lane, from);
+                    if (sub == 0) cache[r * kLanes] = codes_divided<kBF16, kInt8>(__ldg(mine_x + from * stride), now);
                 }
-                const int r = __shfl_sync(0xffffffffu, r_lane, from & 31);
-                if (from >= 0) cache[r * kLanes] = row_codes<kBF16, kInt8>(w[q], by);
             }
             if (lane == 0) *scale = now;
             continue;
@@ -279,9 +299,8 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendParams p) 
                                                  __fmul_rn(c.z, ratio), __fmul_rn(c.w, ratio));
             }
         }
-        const Divider by(now);
         each([&](int32_t r, int32_t j) {
-            if (sub == 0) cache[r * kLanes] = row_codes<kBF16, kInt8>(row(j), by);
+            if (sub == 0) cache[r * kLanes] = codes_divided<kBF16, kInt8>(row(j), now);
         });
         if (lane == 0) *scale = now;
     }
@@ -314,11 +333,12 @@ pa_status append(const void* k_new, const void* v_new, const int64_t* slots, int
         return PA_ERR_INVALID;
     AppendParams p{static_cast<const uint2*>(k_new), static_cast<const uint2*>(v_new), slots,
                    static_cast<uint32_t*>(k_cache), static_cast<uint32_t*>(v_cache), k_scale, v_scale,
-                   pa::device_error_word(), (int64_t)num_blocks * block_size, T, Hkv, 0, 8};
+                   pa::device_error_word(), (int64_t)num_blocks * block_size, T, Hkv, 0, 16};
     const int sms = pa::device_sm_count();
     if (!p.err || !sms) return PA_ERR_CUDA;
-    // A prompt's window has a leader or none, a decode step's eight: as many tiles as warps
-    // for the former where that leaves four CTAs an SM, fewer where it does not.
+    // A prompt's window has a leader or none, a decode step's eight: two tiles a warp for the former
+    // where that leaves four CTAs an SM (32768 x 8 rows 44.5 us, one tile 51.8), fewer where it does
+    // not.
     const int64_t windows = ((int64_t)T + kWindow - 1) / kWindow;
     for (; p.per > 1 && windows * ((2 * Hkv + p.per - 1) / p.per) < 4 * sms; p.per /= 2) {}
     p.groups = (2 * Hkv + p.per - 1) / p.per;
