@@ -626,8 +626,8 @@ PA_API pa_status pa_decode_int4(const void* q, const void* k_cache, const void* 
  * _fp8_block: computes what pa_decode computes with K_j = k_scale[b][h / G] * code,
  * V_j likewise, for d = 64 or 128.  Both products take fp32 sums; a bf16 q is scaled by
  * a power of two into f16 range first (exact for elements down to 2^-25 of the KV head's
- * largest), and a probability times its block's V scale is held to 16 bits.  V scales of
- * 2^-80 and more keep that precision.  A table entry outside the pool reads rows of
+ * largest), and a probability times its block's V scale is held to 16 bits where the scale is
+ * 2^-64 of the context's largest or more (with fewer bits below that).  A table entry outside the pool reads rows of
  * zeros and sets PA_DEVERR_BLOCK_ID.  max_context_len must not be negative and is not
  * used beyond that.  Other arguments, the workspace (pa_decode_workspace_size, here
  * 16-byte aligned) and the errors are those of pa_decode.

@@ -17,9 +17,9 @@
 //    seven lower bits are put under a bf16's exponent, its sign above, which is the number
 //    times 2^-120, exactly, subnormals as subnormals, in 3.5 instructions for two codes.
 // P is bf16 in either case: P times the block's V scale goes in two parts, its upper half
-// and what that leaves, rounded: 16 bits at every size that fp32 holds, however far blocks' scales
-// lie apart.  A power of two, from a run's first V scale, keeps the products clear of both ends
-// of fp32's range; only a scale 2^40 times that one changes it on the way.
+// and what that leaves, rounded: 16 bits, whatever the other blocks' scales are.  A power of two,
+// from a run's first V scale, keeps the products clear of both ends of fp32's range: a scale 2^40
+// times that one moves it, one 2^-64 of it still has all its bits.
 //
 // What bounds it is HBM: 256 bytes a token and KV head at d = 128.  Every warp streams a run of
 // 32-token chunks through a ring of its own in shared memory (pa_runs.cuh), by asynchronous

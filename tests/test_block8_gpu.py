@@ -269,6 +269,36 @@ def test_decode_v_scales_from_tiny_to_huge(fmt, G, order):
 
 
 @pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("G", [1, 4, 8, 16])
+@pytest.mark.parametrize("e", [-60, -20, 30])
+def test_decode_small_v_scale_with_all_the_weight(fmt, G, e):
+    """One block of each context has all the weight (the others' logits are 512 lower: their weights are
+    0 in fp32) and a V scale 2^e times theirs: the result is as exact as if it stood alone."""
+    B, Hkv, bs, d, n = 150, 2, 16, 64, 272
+    nb = n // bs
+    rng = np.random.default_rng(G)
+    c = cache(B * nb, Hkv, bs, d, fmt, 5)
+    one = o.encode(np.float32(1), fmt)
+    c[0][:] = o.encode(np.float32(-1), fmt)
+    c[2][:] = 4.0
+    c[3][:] = 2.0 ** -5
+    tbl = rng.permutation(B * nb).reshape(B, nb).astype(np.int32)
+    heavy = rng.integers(0, nb, B)
+    at = tbl[np.arange(B), heavy]
+    c[0][at] = one
+    c[3][at] = np.float32(2.0 ** (e - 5))
+    q = torch.ones(B, G * Hkv, d, dtype=BF16)
+    out = torch.empty(B, G * Hkv, d, dtype=BF16, device="cuda")
+    DECODE[fmt](q.cuda(), *dev(*c), *dev(tbl, np.full(B, n, np.int32)), n, 1.0, out, workspace(B, G * Hkv, d))
+    assert binding.pa_check_device_errors() == 0
+    v = o.values(c[1], c[3], fmt)[at]                    # [B, Hkv, bs, d], equal weights
+    ref, mag = (np.repeat(x, G, 1) for x in (v.mean(2), np.abs(v).mean(2)))
+    # the output's rounding, P's two parts (2^-16), sums of a few dozen steps (2^-22 each) of codes from 128 on
+    bound = 2.0 ** -8 * np.abs(ref) + 2.0 ** -16 * mag + 64 * 2.0 ** -22 * (mag + 128 * 2.0 ** (e - 5) * (fmt == "int8"))
+    assert (np.abs(out.double().cpu().numpy() - ref) <= bound).all()
+
+
+@pytest.mark.parametrize("fmt", FMTS)
 def test_decode_zero_scales_and_all_codes(fmt):
     c = cache(12, 2, 16, 64, fmt, 3)
     c[3][::2] = 0.0
