@@ -30,7 +30,7 @@
 // 171 (6.3 TB/s, 94 % of the measured copy; DRAM traffic 1.003 times the bytes, 45 % of the
 // ALU's and 15 % of the tensor pipe's cycles, 40 % of the issue slots), G = 8 176, G = 16 185;
 // INT8: 172, 173, 174, 195; at d = 64 88 to 95 us up to G = 8; 64 sequences of 128 .. 2048 tokens,
-// 40 heads, G = 1: INT8 118 us, E4M3 116; 4 sequences of up to 64 tokens 6.8 us, all latency.
+// 40 heads, G = 1: INT8 118 us, E4M3 116; 4 sequences of up to 64 tokens 6.4 us, all latency (6.6 with the next call launched at its end).
 // The caches with a scale per token take 159 us (E4M3) and 175 (INT8) for a 40-head batch of
 // nearly this size: a conversion and a factor per key, and loading warps to wait for.
 #pragma once
@@ -163,6 +163,7 @@ __global__ void __launch_bounds__(max_warps(D, kForm) * 32, 1) decode_block8_ker
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int32_t max_len = p.max_blocks << bs_shift;
 
+    asm volatile("griddepcontrol.launch_dependents;");   // a next call may be launched: it waits
     asm volatile("griddepcontrol.wait;" ::: "memory");   // launched while the kernel before may run
 
     // The tables and queries are read a dependent load or two from now: into L2 with
@@ -678,7 +679,6 @@ __global__ void __launch_bounds__(max_warps(D, kForm) * 32, 1) decode_block8_ker
             if (pos < hi) s = next_pair(prefix, Hkv, s);
         }
     }
-    asm volatile("griddepcontrol.launch_dependents;");   // a next call may be launched: it waits
     __syncthreads();
     join_runs<D, kBF16>(p.out, cut, cta_lo, nw, smem, S * kStage, L.slots, runs, is_last, scan);
 }
