@@ -328,7 +328,8 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) compact_kernel(cons
         uint32_t use = 0;
 #pragma unroll
         for (int u = 0; u < kMove; ++u)
-            if (now[u] >= 0) use |= k[u].x | v[u].x;
+            if (now[u] >= 0)
+                use |= k[u].x | k[u].y | k[u].z | k[u].w | v[u].x | v[u].y | v[u].z | v[u].w;
         asm volatile("" ::"r"(use) : "memory");
         asm volatile("barrier.cluster.arrive.relaxed.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
 #pragma unroll
