@@ -258,9 +258,9 @@ constexpr int kMove = 4;   // rows of a thread at a time, K and V each
 // A cluster of CTAs per (sequence, KV head).  Row r comes from kept[r] >= r, and both ascend:
 // once a stretch of rows has been read, nothing that is still to be read lies in the
 // stretch.  So the cluster reads a stretch into its registers, meets, writes it, and reads the
-// next one, without meeting again.  Bound by HBM: 256 pairs of 4096 rows at d = 128 take 169 us
-// (1.07 GB, 6.3 TB/s, 95 % of the measured copy), 2560 of 512 rows 202 (6.6 TB/s); few pairs by
-// the latency of a stretch: 8 of 8000 rows 21 us, of which the bytes are 10.
+// next one, without meeting again.  Bound by HBM: 256 pairs of 4096 rows at d = 128 take 185 us
+// (1.07 GB, 5.8 TB/s, 87 % of the measured copy), 2560 of 512 rows 205 (6.6 TB/s); few pairs by
+// the latency of a stretch: 8 of 8000 rows 20 us, of which the bytes are 10.
 template <int kThreads>
 __global__ void __launch_bounds__(kThreads, 1024 / kThreads) compact_kernel(const CompactParams p) {
     asm volatile("griddepcontrol.wait;" ::: "memory");   // launched while the choice may be made
@@ -322,16 +322,14 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) compact_kernel(cons
         // The next stretch's places, three loads one behind the other, while these rows travel.
         base += min(stretch, n - base);
         if (base < n) places(base);
-        // What is read must have arrived before the others may write over it, which a use of it
-        // sees to; the writes before need not be anywhere (a release waits for them: 186 us for
-        // 171, 256 pairs of 4096 rows).
-        uint32_t use = 0;
-#pragma unroll
-        for (int u = 0; u < kMove; ++u)
-            if (now[u] >= 0)
-                use |= k[u].x | k[u].y | k[u].z | k[u].w | v[u].x | v[u].y | v[u].z | v[u].w;
-        asm volatile("" ::"r"(use) : "memory");
-        asm volatile("barrier.cluster.arrive.relaxed.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+        // Every row of the stretch has been read before any CTA writes over it: only a release and an
+        // acquire say so.  (A relaxed meeting orders nothing, and what the compiler is told about the
+        // rows' registers reaches no instruction.)  The release waits for the writes of the stretch
+        // before as well.
+        if (ctas == 1)
+            __syncthreads();
+        else
+            asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 #pragma unroll
         for (int u = 0; u < kMove; ++u)
             if (now[u] >= 0) {
@@ -432,8 +430,8 @@ PA_API pa_status pa_compact_tokens(void* k_cache, void* v_cache, const int32_t* 
     const int64_t pairs = (int64_t)B * Hkv;
     if (pairs > INT32_MAX / 8) return PA_ERR_UNSUPPORTED;
     // CTAs of a pair: as many as its rows fill, until there are four of 256 threads for every SM,
-    // eight at most (2560 pairs of 512 rows: one 202 us, two 201, four 224, eight 261; 512 of 1024:
-    // 94, 87, 88, 97; 256 of 4096: 172, 184, 169, 171); of more threads where there are too few
+    // eight at most (2560 pairs of 512 rows: one 204 us, two 214, four 217, eight 232; 512 of 1024:
+    // 95, 94, 94, 94; 256 of 4096: 178, 186, 185, 189); of more threads where there are too few
     // of them to fill the SMs with 1024 each.
     const int small = 256 / p.vecs * kMove;
     int cluster = 1;
