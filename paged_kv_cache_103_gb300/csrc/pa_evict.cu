@@ -258,8 +258,8 @@ constexpr int kMove = 4;   // rows of a thread at a time, K and V each
 // A cluster of CTAs per (sequence, KV head).  Row r comes from kept[r] >= r, and both ascend:
 // once a stretch of rows has been read, nothing that is still to be read lies in the
 // stretch.  So the cluster reads a stretch into its registers, meets, writes it, and reads the
-// next one, without meeting again.  Bound by HBM: 256 pairs of 4096 rows at d = 128 take 185 us
-// (1.07 GB, 5.8 TB/s, 87 % of the measured copy), 2560 of 512 rows 205 (6.6 TB/s); few pairs by
+// next one, without meeting again.  Bound by HBM: 256 pairs of 4096 rows at d = 128 take 176 us
+// (1.07 GB, 6.1 TB/s, 91 % of the measured copy), 2560 of 512 rows 204 (6.6 TB/s); few pairs by
 // the latency of a stretch: 8 of 8000 rows 20 us, of which the bytes are 10.
 template <int kThreads>
 __global__ void __launch_bounds__(kThreads, 1024 / kThreads) compact_kernel(const CompactParams p) {
@@ -429,13 +429,15 @@ PA_API pa_status pa_compact_tokens(void* k_cache, void* v_cache, const int32_t* 
     if (!sms) return PA_ERR_CUDA;
     const int64_t pairs = (int64_t)B * Hkv;
     if (pairs > INT32_MAX / 8) return PA_ERR_UNSUPPORTED;
-    // CTAs of a pair: as many as its rows fill, until there are four of 256 threads for every SM,
-    // eight at most (2560 pairs of 512 rows: one 204 us, two 214, four 217, eight 232; 512 of 1024:
-    // 95, 94, 94, 94; 256 of 4096: 178, 186, 185, 189); of more threads where there are too few
-    // of them to fill the SMs with 1024 each.
+    // CTAs of a pair: one where there are more pairs than SMs (256 pairs of 4096 rows at d = 128: one
+    // 176 us, two 186, four 186, eight 188; 160 of 4000: 130, 156, 149, 130; 512 of 1024: 96, 94, 94,
+    // 95; 2560 of 512: 204, 214, 217, 232); else as many as its rows fill, until there are four of 256
+    // threads for every SM, eight at most (128 pairs of 4000: 102, 96, 95, 96; 32 of 8000: 142, 92, 60,
+    // 52); of more threads where there are too few of them to fill the SMs with 1024 each.
     const int small = 256 / p.vecs * kMove;
     int cluster = 1;
-    while (cluster < 8 && (int64_t)cluster * small < keep && pairs * cluster < 4 * sms) cluster *= 2;
+    if (pairs <= sms)
+        while (cluster < 8 && (int64_t)cluster * small < keep && pairs * cluster < 4 * sms) cluster *= 2;
     const dim3 grid((unsigned)(pairs * cluster));
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (pairs * cluster <= sms) return launch_early(compact_kernel<1024>, grid, 1024, cluster, 0, st, p);
