@@ -74,13 +74,15 @@ constexpr float kLog2e = 1.4426950408889634f;
 
 struct Int4Params {
     const uint16_t* q;
+    uint16_t* out;
     const uint8_t *k_cache, *v_cache, *k_scale, *v_scale;
     const int32_t* block_tables;
     const int32_t* context_lens;
-    Out out;
+    int32_t* counters;
+    float* partials;
     unsigned int* err;
     // A KV head with more than kMaxG query heads is `subs` pairs of kMaxG heads.
-    int32_t max_blocks, B, bs_shift, num_blocks, subs, warps;
+    int32_t max_blocks, B, H, Hkv, G, bs_shift, num_blocks, subs, warps;
     float scale_log2;
 };
 
@@ -200,7 +202,7 @@ __global__ void __launch_bounds__(max_warps(D, kForm) * 32, 1) decode_int4_kerne
     constexpr uint32_t kCodes = kChunk * kRow, kScales = kChunk * kSRow;
     constexpr uint32_t kStage = 2 * (kCodes + kScales);   // K, V codes, K, V scales
     constexpr int S = ring_stages(D);
-    const int32_t B = p.B, Hkv = p.out.Hkv, G = p.out.G;
+    const int32_t B = p.B, Hkv = p.Hkv, G = p.G;
     constexpr int bs_shift = kShift, bmask = (1 << kShift) - 1;
     const int nw = p.warps, threads = nw * 32;
     const Layout L = layout_of(D, G, B, nw);
@@ -221,7 +223,7 @@ __global__ void __launch_bounds__(max_warps(D, kForm) * 32, 1) decode_int4_kerne
         const int64_t line = ((int64_t)blockIdx.x * threads + tid) * 128;
         if (line < (int64_t)B * p.max_blocks * 4)
             prefetch_l2(reinterpret_cast<const char*>(p.block_tables) + line);
-        if (line < (int64_t)B * p.out.H * D * 2) prefetch_l2(reinterpret_cast<const char*>(p.q) + line);
+        if (line < (int64_t)B * p.H * D * 2) prefetch_l2(reinterpret_cast<const char*>(p.q) + line);
     }
 
     const int32_t W = list_prefix(p.context_lens, B, Hkv, max_len, p.err, nw, prefix, scan, is_last, runs);
@@ -230,9 +232,9 @@ __global__ void __launch_bounds__(max_warps(D, kForm) * 32, 1) decode_int4_kerne
 #pragma unroll 1
     for (int32_t i = blockIdx.x; i < B; i += gridDim.x) {
         if (prefix[i + 1] != prefix[i]) continue;
-        uint4* row = reinterpret_cast<uint4*>(p.out.out + (int64_t)i * p.out.H * D);
+        uint4* row = reinterpret_cast<uint4*>(p.out + (int64_t)i * p.H * D);
 #pragma unroll 1
-        for (int v = tid; v < p.out.H * D / 8; v += threads) row[v] = make_uint4(0, 0, 0, 0);
+        for (int v = tid; v < p.H * D / 8; v += threads) row[v] = make_uint4(0, 0, 0, 0);
     }
 
     // CTAs in use have a chunk per warp at least: smaller batches take fewer CTAs
@@ -369,7 +371,7 @@ __global__ void __launch_bounds__(max_warps(D, kForm) * 32, 1) decode_int4_kerne
             for (int nt = 0; nt < NT; ++nt) {
                 const int h = kDup ? cr & 3 : 8 * nt + cr;
                 const uint4* row = reinterpret_cast<const uint4*>(
-                    p.q + ((int64_t)s.i * p.out.H + s.g * G + h) * D + 16 * c4);
+                    p.q + ((int64_t)s.i * p.H + s.g * G + h) * D + 16 * c4);
 #pragma unroll
                 for (int g = 0; g < NG; ++g) {
                     const uint4 z = make_uint4(0, 0, 0, 0);
@@ -747,7 +749,7 @@ __global__ void __launch_bounds__(max_warps(D, kForm) * 32, 1) decode_int4_kerne
                         const int at_d = 64 * g + 8 * cr;
                         if (kDup && (h >= G || c4 >= 2)) continue;
                         if (whole) {
-                            *reinterpret_cast<uint4*>(p.out.out + ((int64_t)s.i * p.out.H + s.g * G + h) * D + at_d) =
+                            *reinterpret_cast<uint4*>(p.out + ((int64_t)s.i * p.H + s.g * G + h) * D + at_d) =
                                 make_uint4(pa::pack2<kBF16>(v[0], v[1]), pa::pack2<kBF16>(v[2], v[3]),
                                            pa::pack2<kBF16>(v[4], v[5]), pa::pack2<kBF16>(v[6], v[7]));
                         } else {
@@ -773,7 +775,10 @@ __global__ void __launch_bounds__(max_warps(D, kForm) * 32, 1) decode_int4_kerne
     asm volatile("griddepcontrol.launch_dependents;");   // a next call may be launched: it waits
     __syncthreads();
 
-    join_runs<D, kBF16>(p.out, cut, cta_lo, nw, smem, S * kStage, L.slots, runs, is_last, scan);
+    // Plain fields, not an Out among the parameters: with one, registers fall differently, and forms
+    // spill that do not as it is (G = 16 in blocks of 32 at d = 64 took 63 us for 59, 8 x 32768 tokens).
+    join_runs<D, kBF16>(Out{p.out, p.counters, p.partials, p.H, p.Hkv, p.G}, cut, cta_lo, nw, smem, S * kStage,
+                        L.slots, runs, is_last, scan);
 }
 
 // ---- host side -----------------------------------------------------------------
@@ -793,7 +798,7 @@ pa_status launch(const Int4Params& p, cudaStream_t stream) {
     int ctas = pa::device_sm_count();
     if (ctas <= 0) return PA_ERR_CUDA;
     if (ctas > kMaxCtas) ctas = kMaxCtas;
-    const Layout L = layout_of(D, p.out.G, p.B, p.warps);
+    const Layout L = layout_of(D, p.G, p.B, p.warps);
     // Started early, so that its launch hides behind the append's or another call's end.
     cudaLaunchAttribute attr{};
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -817,7 +822,7 @@ pa_status launch_b(const Int4Params& p, cudaStream_t stream) {
 
 template <int D, bool kBF16>
 pa_status launch_g(const Int4Params& p, cudaStream_t stream) {
-    switch (form_of(p.out.G)) {
+    switch (form_of(p.G)) {
         case kG1: return launch_b<D, kBF16, kG1>(p, stream);
         case kG4: return launch_b<D, kBF16, kG4>(p, stream);
         case kG8: return launch_b<D, kBF16, kG8>(p, stream);
@@ -871,20 +876,20 @@ PA_API pa_status pa_decode_int4(const void* q, const void* k_cache, const void* 
     p.err = pa::device_error_word();
     if (!p.err) return PA_ERR_CUDA;
     p.q = static_cast<const uint16_t*>(q);
-    p.out.out = static_cast<uint16_t*>(out);
+    p.out = static_cast<uint16_t*>(out);
     p.k_cache = static_cast<const uint8_t*>(k_cache);
     p.v_cache = static_cast<const uint8_t*>(v_cache);
     p.k_scale = static_cast<const uint8_t*>(k_scale);
     p.v_scale = static_cast<const uint8_t*>(v_scale);
     p.block_tables = block_tables;
     p.context_lens = context_lens;
-    p.out.counters = static_cast<int32_t*>(workspace);
-    p.out.partials = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) + ticket_bytes(B, H));
+    p.counters = static_cast<int32_t*>(workspace);
+    p.partials = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) + ticket_bytes(B, H));
     p.max_blocks = max_blocks;
     p.B = B;
-    p.out.H = H;
-    p.out.Hkv = Hkv * subs;
-    p.out.G = G;
+    p.H = H;
+    p.Hkv = Hkv * subs;
+    p.G = G;
     p.subs = subs;
     p.bs_shift = block_size == 8 ? 3 : block_size == 16 ? 4 : 5;
     p.num_blocks = num_blocks;
