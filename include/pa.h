@@ -146,15 +146,30 @@ PA_API pa_status pa_free(pa_allocator* a, int64_t seq_id);
  * that keeps as many of them (pa_select_tokens, pa_compact_tokens): the blocks behind the
  * first ceil(num_tokens / block_size) are dropped as pa_free drops them, and of those
  * that stay each that other sequences share is replaced by a block from the front of the free
- * list (taken before any block is dropped), because the kept rows will be written there.
+ * list, because the kept rows will be written there.
  * The blocks that stay lose their prefix-cache entries and the sequence stops registering:
  * their content is no longer a prefix's.  A length equal to num_tokens changes nothing.
  * Export the table before the call (to read from) and after it (to write to), and compact
  * on the device before anything else writes to the dropped blocks (the same stream will
- * do).  Where the caller keeps several layers, it compacts each layer's cache.  All or
- * nothing: PA_ERR_OOM leaves every state unchanged.  PA_ERR_INVALID for a swapped-out
+ * do).  Where the caller keeps several layers, it compacts each layer's cache.
+ *   Several sequences may be cut and then moved in one pa_compact_tokens call: a block that
+ * one of them has left is neither moved into in place by its last other holder, which gets a new
+ * block as well, nor taken from the free list by another cut, as the move still reads it.
+ * This lasts for the cuts since the last pa_alloc, pa_alloc_prompt, pa_append_* or
+ * pa_swap_in that succeeded, which hand out slots to be written: moves of earlier cuts are
+ * launched before those of later ones.  So are those of a sequence that is cut again, or was
+ * forked after its cut and is cut too.
+ *   All or nothing: PA_ERR_OOM, where too few blocks are free that nobody has left in
+ * these cuts, leaves every state unchanged.  PA_ERR_INVALID for a swapped-out
  * sequence or a num_tokens outside the range. */
 PA_API pa_status pa_alloc_evict(pa_allocator* a, int64_t seq_id, int32_t num_tokens);
+
+/* pa_alloc_evict for seq_ids[0..B) in that order, all or nothing, as the first cuts of a new
+ * move: blocks that earlier cuts have left may be taken, so their moves are launched first.
+ * B = 0 says that they are.  Duplicate ids return PA_ERR_INVALID.
+ *   num_tokens (host, B int32): min(length, keep) of each, for one `keep` */
+PA_API pa_status pa_alloc_evict_batch(pa_allocator* a, const int64_t* seq_ids, const int32_t* num_tokens,
+                                      int32_t B);
 
 /* Fills block_tables (host, [B][max_blocks] int32, unused entries -1) and
  * context_lens (host, [B] int32) for seq_ids[0..B).  A table longer than
@@ -799,10 +814,11 @@ PA_API pa_status pa_select_tokens(const float* weights, int32_t num_rows, int32_
  * r < kept_lens[i], with p = kept[i][g][r],
  *   K of (new_tables[i][r / bs], row r % bs, g) = K of (block_tables[i][p / bs], p % bs, g)
  * as the cache was before the call, and the same for V; bit-exact.  A sequence's lists
- * ascend strictly (p >= r then), as pa_select_tokens writes them.  A block of new_tables[i] is either
- * the one at the same place of block_tables[i] (moved in place) or one that no block_tables
- * row of the call holds; sequences that move in place do not share the blocks that they
- * write (pa_alloc_evict sees to all of this).  Slots behind the kept tokens are left as
+ * ascend strictly (p >= r then), as pa_select_tokens writes them.  A block of new_tables[i] that
+ * rows move to is either the one at the same place of block_tables[i] (moved in place), and then
+ * in no other block_tables row of the call, or in none of them, and no two new_tables rows hold it:
+ * the allocator sees to this for the sequences that it cut for one move (pa_alloc_evict,
+ * pa_alloc_evict_batch).  A sequence that keeps all of its tokens moves none.  Slots behind the kept tokens are left as
  * they are.  A position whose block lies beyond its table or outside the pool, on either
  * side, is not moved and sets PA_DEVERR_TABLE_WIDTH or PA_DEVERR_BLOCK_ID; a kept_lens
  * outside [0, keep] is cut to it and sets PA_DEVERR_CONTEXT.

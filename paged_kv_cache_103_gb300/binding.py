@@ -128,6 +128,7 @@ SIGNATURES = {
     "pa_decode_fp8_block": (_ST, [_P, _P, _P, _P, _P, _P, _I32, _P, _I32, _I32, _I32, _I32, _I32,
                                   _I32, _I32, _F32, _ST, _P, _P, _SZ, _P]),
     "pa_alloc_evict": (_ST, [_P, _I64, _I32]),
+    "pa_alloc_evict_batch": (_ST, [_P, _P, _P, _I32]),
     "pa_decode_weights_workspace_size": (_SZ, [_I32, _I32, _I32, _I32, _I64]),
     "pa_decode_weights": (_ST, [_P, _P, _P, _P, _I32, _P, _I32, _I32, _I32, _I32, _I32, _I32, _I32,
                                 _F32, _ST, _P, _P, _P, _I32, _I32, _P, _SZ, _P]),
@@ -979,8 +980,19 @@ class Allocator:
 
     def evict(self, seq_id: int, num_tokens: int) -> None:
         """Cuts the sequence to ``num_tokens`` tokens for an eviction: export its table before
-        (``block_tables`` of ``pa_compact_tokens``) and after (``new_tables``)."""
+        (``block_tables`` of ``pa_compact_tokens``) and after (``new_tables``).  Sequences cut one after
+        the other may be moved in one call."""
         _check(self._lib.pa_alloc_evict(self._h, seq_id, num_tokens), "pa_alloc_evict")
+
+    def evict_batch(self, seq_ids, num_tokens) -> None:
+        """``evict`` of several sequences for one move, all or nothing; the moves of earlier cuts
+        have been launched (which an empty batch says too)."""
+        ids = np.ascontiguousarray(seq_ids, dtype=np.int64)
+        n = np.ascontiguousarray(num_tokens, dtype=np.int32)
+        if ids.ndim != 1 or n.shape != ids.shape:
+            raise ValueError("one num_tokens per sequence")
+        _check(self._lib.pa_alloc_evict_batch(self._h, _np_ptr(ids) if ids.size else None,
+                                              _np_ptr(n) if ids.size else None, ids.shape[0]), "pa_alloc_evict_batch")
 
     def fork(self, parent: int, child: int) -> None:
         _check(self._lib.pa_fork(self._h, parent, child), "pa_fork")

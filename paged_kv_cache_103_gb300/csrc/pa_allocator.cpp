@@ -30,6 +30,11 @@
 // from the front of a host free list and drop their device counts; swap-in
 // takes fresh device blocks from the front of the device free list and returns
 // the host blocks to the back of the host list.
+//
+// Eviction (no page's): a cut sequence's kept rows move on the device, with all others that
+// were cut since slots were last handed out, in one launch that reads the tables as they were
+// before.  So what a sequence has left in this run of cuts, whether it is free now or one
+// other holder is left, is not written for another one: not moved into in place, not taken.
 #include <algorithm>
 #include <cstdint>
 #include <cstring>
@@ -92,6 +97,10 @@ struct pa_allocator {
     std::vector<char> in_free;
     int32_t fhead = -1, ftail = -1, nfree = 0;
     std::vector<int32_t> ref;
+    // run of evictions in which a sequence last left a block; blocks of the present run on the free list
+    std::vector<uint64_t> left;
+    uint64_t run = 1;
+    int32_t held = 0;
     std::unordered_map<int64_t, Sequence> seqs;
     std::unordered_map<Key, Entry, KeyHash> cache;
     std::vector<const Key*> block_key;  // key of the entry a block holds, or null
@@ -110,6 +119,7 @@ struct pa_allocator {
         ftail = b;
         in_free[b] = 1;
         ++nfree;
+        held += left[b] == run;
     }
 
     void free_remove(int32_t b) {
@@ -117,6 +127,7 @@ struct pa_allocator {
         if (fnext[b] >= 0) fprev[fnext[b]] = fprev[b]; else ftail = fprev[b];
         in_free[b] = 0;
         --nfree;
+        held -= left[b] == run;
     }
 
     void evict(int32_t b) {
@@ -126,12 +137,56 @@ struct pa_allocator {
         pstats.evicted += 1;
     }
 
-    int32_t take_front() {
-        const int32_t b = fhead;
+    int32_t take(int32_t b) {
         free_remove(b);
         evict(b);
         ref[b] = 1;
         return b;
+    }
+
+    int32_t take_front() { return take(fhead); }
+
+    // Slots are handed out (or the caller says so): the cuts so far have been moved.
+    void end_run() {
+        ++run;
+        held = 0;
+    }
+
+    size_t blocks_of(int32_t tokens) const { return (size_t)(((int64_t)tokens + block_size - 1) / block_size); }
+
+    // Blocks that a cut of `s` to num_tokens takes in the present run.
+    int32_t cut_need(const Sequence& s, int32_t num_tokens) const {
+        int32_t need = 0;
+        if (num_tokens == s.length) return 0;
+        for (size_t j = 0; j < blocks_of(num_tokens); ++j) need += ref[s.table[j]] > 1 || left[s.table[j]] == run;
+        return need;
+    }
+
+    void leave(int32_t b) {
+        left[b] = run;
+        if (--ref[b] == 0) free_push_back(b);
+    }
+
+    // Cuts `s`; enough blocks that nobody has left in this run are free.
+    void cut(Sequence& s, int32_t num_tokens) {
+        if (num_tokens == s.length) return;
+        const size_t stay = blocks_of(num_tokens);
+        for (size_t j = 0; j < stay; ++j) {
+            int32_t& b = s.table[j];
+            if (ref[b] > 1 || left[b] == run) {
+                int32_t fresh = fhead;
+                while (left[fresh] == run) fresh = fnext[fresh];
+                take(fresh);
+                leave(b);
+                b = fresh;
+            } else {
+                evict(b);   // its content will no longer be the prefix's
+            }
+        }
+        for (size_t j = stay; j < s.table.size(); ++j) leave(s.table[j]);
+        s.table.resize(stay);
+        s.length = num_tokens;
+        untrack(s);
     }
 
     // Registers `block` under (chain, tokens) unless that key is cached;
@@ -204,6 +259,7 @@ PA_API pa_status pa_alloc_create(int32_t num_blocks, int32_t block_size,
     a->num_blocks = num_blocks;
     a->block_size = block_size;
     a->ref.assign((size_t)num_blocks, 0);
+    a->left.assign((size_t)num_blocks, 0);
     a->fprev.assign((size_t)num_blocks, -1);
     a->fnext.assign((size_t)num_blocks, -1);
     a->in_free.assign((size_t)num_blocks, 0);
@@ -243,6 +299,7 @@ PA_API pa_status pa_alloc(pa_allocator* a, int64_t seq_id, int32_t num_tokens) {
     if (held < num_tokens) need = (num_tokens - held + a->block_size - 1) / a->block_size;
     if (need > (int64_t)a->nfree) return PA_ERR_OOM;
     Sequence& s = a->seqs[seq_id];
+    a->end_run();
     for (int64_t k = 0; k < need; ++k) s.table.push_back(a->take_front());
     if (fresh || num_tokens > s.length) pa_allocator::untrack(s);  // token ids unknown
     s.length = std::max(s.length, num_tokens);
@@ -258,6 +315,7 @@ PA_API pa_status pa_append_slot(pa_allocator* a, int64_t seq_id, int64_t* slot_o
     if (a->append_need(it->second, [&](int32_t b) { return a->ref[b]; }) > a->nfree)
         return PA_ERR_OOM;
     pa_allocator::untrack(it->second);  // token id unknown
+    a->end_run();
     int32_t src, dst;
     *slot_out = a->append_checked(it->second, &src, &dst);
     if (cow_src) *cow_src = src;
@@ -297,6 +355,7 @@ pa_status append_batch(pa_allocator* a, const int64_t* seq_ids, const int32_t* t
         need += n;
     }
     if (need > (int64_t)a->nfree) return PA_ERR_OOM;
+    a->end_run();
     int32_t ncow = 0;
     for (int32_t i = 0; i < B; ++i) {
         int32_t src, dst;
@@ -352,6 +411,7 @@ PA_API pa_status pa_alloc_prompt(pa_allocator* a, int64_t seq_id, const int32_t*
     int32_t revive = 0;
     for (int32_t b : hits) revive += a->ref[b] == 0;
     if (blocks - (int32_t)hits.size() > a->nfree - revive) return PA_ERR_OOM;
+    a->end_run();
     a->pstats.lookups += looked;
     a->pstats.hits += (int64_t)hits.size();
     Sequence s;
@@ -382,6 +442,7 @@ PA_API pa_status pa_append_token(pa_allocator* a, int64_t seq_id, int32_t token,
     if (it->second.length == INT32_MAX || it->second.swapped) return PA_ERR_INVALID;
     if (a->append_need(it->second, [&](int32_t b) { return a->ref[b]; }) > a->nfree)
         return PA_ERR_OOM;
+    a->end_run();
     int32_t src, dst;
     *slot_out = a->append_checked(it->second, &src, &dst);
     a->note_token(it->second, token);
@@ -406,25 +467,33 @@ PA_API pa_status pa_alloc_evict(pa_allocator* a, int64_t seq_id, int32_t num_tok
     if (it == a->seqs.end()) return PA_ERR_NOT_FOUND;
     Sequence& s = it->second;
     if (s.swapped || num_tokens > s.length) return PA_ERR_INVALID;
-    if (num_tokens == s.length) return PA_OK;
-    const size_t stay = (size_t)(((int64_t)num_tokens + a->block_size - 1) / a->block_size);
-    int32_t need = 0;
-    for (size_t j = 0; j < stay; ++j) need += a->ref[s.table[j]] > 1;
-    if (need > a->nfree) return PA_ERR_OOM;
-    for (size_t j = 0; j < stay; ++j) {
-        int32_t& b = s.table[j];
-        if (a->ref[b] > 1) {
-            a->ref[b] -= 1;
-            b = a->take_front();
-        } else {
-            a->evict(b);   // its content will no longer be the prefix's
-        }
+    if (a->cut_need(s, num_tokens) > a->nfree - a->held) return PA_ERR_OOM;
+    a->cut(s, num_tokens);
+    return PA_OK;
+}
+
+PA_API pa_status pa_alloc_evict_batch(pa_allocator* a, const int64_t* seq_ids, const int32_t* num_tokens,
+                                      int32_t B) {
+    if (!a || B < 0 || (B > 0 && (!seq_ids || !num_tokens))) return PA_ERR_INVALID;
+    std::vector<Sequence*> batch((size_t)B);
+    std::unordered_set<int64_t> seen;
+    seen.reserve((size_t)B * 2);
+    for (int32_t i = 0; i < B; ++i) {
+        if (!seen.insert(seq_ids[i]).second) return PA_ERR_INVALID;
+        auto it = a->seqs.find(seq_ids[i]);
+        if (it == a->seqs.end()) return PA_ERR_NOT_FOUND;
+        if (it->second.swapped || num_tokens[i] < 0 || num_tokens[i] > it->second.length) return PA_ERR_INVALID;
+        batch[(size_t)i] = &it->second;
     }
-    for (size_t j = stay; j < s.table.size(); ++j)
-        if (--a->ref[s.table[j]] == 0) a->free_push_back(s.table[j]);
-    s.table.resize(stay);
-    s.length = num_tokens;
-    pa_allocator::untrack(s);
+    // In a run of their own nothing has been left yet; what the first of them leave, the last
+    // holder of it counts here as one of several.
+    int64_t need = 0;
+    for (int32_t i = 0; i < B; ++i)
+        if (num_tokens[i] != batch[(size_t)i]->length)
+            for (size_t j = 0; j < a->blocks_of(num_tokens[i]); ++j) need += a->ref[batch[(size_t)i]->table[j]] > 1;
+    if (need > (int64_t)a->nfree) return PA_ERR_OOM;
+    a->end_run();
+    for (int32_t i = 0; i < B; ++i) a->cut(*batch[(size_t)i], num_tokens[i]);
     return PA_OK;
 }
 
@@ -554,6 +623,7 @@ PA_API pa_status pa_swap_in(pa_allocator* a, int64_t seq_id, int32_t* pairs, int
     const int32_t nb = (int32_t)s.host.size();
     if (!s.swapped || cap < nb || (nb > 0 && !pairs)) return PA_ERR_INVALID;
     if (nb > a->nfree) return PA_ERR_OOM;
+    a->end_run();
     for (int32_t j = 0; j < nb; ++j) {
         const int32_t b = a->take_front();
         pairs[2 * j] = s.host[(size_t)j];

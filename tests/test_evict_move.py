@@ -1,10 +1,11 @@
-"""The meeting of pa_compact_tokens: no row is written over before every CTA of the cluster has read its
+"""pa_compact_tokens: no row is written over before every CTA of the cluster has read its
 own.  On the CPU: what the kernel's source asks of the barrier.  On the GPU: moves in place by a few
 places, several stretches of every cluster size, while another stream keeps the memory busy."""
 import numpy as np
 import pytest
 import torch
 
+from oracle import evict as oe
 from paged_kv_cache_103_gb300 import binding
 from paged_kv_cache_103_gb300 import build as pa_build
 from paged_kv_cache_103_gb300 import workloads as wl
@@ -72,3 +73,45 @@ def test_moves_in_place_by_a_few_places(B, Hkv, keep, d, bs, dtype):
         assert binding.pa_check_device_errors() == 0
         for got, w in zip(kv, want):
             assert torch.equal(got.view(torch.int16), w.view(torch.int16)), turn
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("batch", [False, True])
+@pytest.mark.parametrize("B,Hkv,n,keep,d,bs,dtype", [
+    (32, 8, 701, 300, 128, 16, BF16), (90, 8, 500, 333, 128, 8, F16), (7, 2, 3000, 2900, 64, 32, F16)])
+def test_forks_cut_for_one_move(B, Hkv, n, keep, d, bs, dtype, batch):
+    """Forks of one sequence, some of them grown on, all cut and moved in one call: what one moves
+    is what was there before the call, whatever the others write."""
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    pa_build.build()
+    rng = np.random.default_rng(B)
+    need = -(-n // bs)
+    a = binding.Allocator(need + B * (-(-keep // bs) + 3), bs)
+    a.alloc(0, n)
+    ids = list(range(B))
+    for i in ids[1:]:
+        a.fork(0, i)
+    for _ in range(bs + 1):
+        a.append_batch(ids[::2])
+    old, lens = a.export(ids, need + 3)
+    if batch:
+        a.evict_batch(ids, [keep] * B)
+    else:
+        for i in ids:
+            a.evict(i, keep)
+    new, _ = a.export(ids, need + 3)
+    for i in ids:
+        others = np.delete(old, i, 0)
+        assert not np.isin(new[i][new[i] >= 0], others).any()
+    kept = np.empty((B, Hkv, keep), np.int32)
+    for i in ids:
+        for g in range(Hkv):
+            kept[i, g] = np.sort(rng.choice(lens[i], keep, replace=False))
+    host = [rng.integers(-2 ** 15, 2 ** 15, (a.stats()["num_blocks"], bs, Hkv, d)).astype(np.int16) for _ in "kv"]
+    kv = [x.view(dtype) for x in dev(*host)]
+    binding.pa_compact_tokens(*kv, *dev(kept, np.full(B, keep, np.int32), old, new))
+    assert binding.pa_check_device_errors() == 0
+    for got, want in zip(kv, host):
+        oe.compact_tokens(want, kept, [keep] * B, old, new)
+        assert np.array_equal(got.view(torch.int16).cpu().numpy(), want)
