@@ -1,5 +1,7 @@
 """Evictions of several sequences for one move: no block that the move writes for one of them is in
 another's old table, whatever they share and however few blocks are free."""
+import os
+
 import numpy as np
 import pytest
 
@@ -286,3 +288,18 @@ def test_random_forks_and_cuts(seed):
             a.free(s)
         assert sorted(a.free_list()) == list(range(N))
     assert cuts > 60 and (N > 24 or refused > 0)
+
+
+def test_the_readme_cuts_a_batch_with_a_sequence_within_its_budget():
+    """README.md's lines between the choice and the move, run as they stand."""
+    text = open(os.path.join(os.path.dirname(pa_build.PKG), "README.md"), encoding="utf-8").read()
+    lines = text[text.index("old_tables, "): text.index("pa.pa_compact_tokens(")]
+    a = binding.Allocator(40, 8)
+    for s, n in ((5, 100), (3, 20), (8, 64)):
+        a.alloc(s, n)
+    a.fork(5, 6)
+    scope = dict(alloc=a, seq_ids=[5, 3, 6, 8], max_blocks=16, keep=64, np=np)
+    exec(lines, scope)
+    assert list(scope["new_lens"]) == [64, 20, 64, 64]
+    old, new = ([[int(x) for x in row if x >= 0] for row in scope[t]] for t in ("old_tables", "new_tables"))
+    check_move(old, new, (True, False, True, False))
