@@ -800,7 +800,7 @@ PA_API pa_status pa_decode_weights(const void* q, const void* k_cache, const voi
  * A sequence that takes no part (see rows) gets kept_lens[i] = 0 and -1s.  A negative
  * context counts as 0 and sets PA_DEVERR_CONTEXT, one longer than width is cut to it and
  * sets PA_DEVERR_TABLE_WIDTH.
- *   keep         >= first + last and >= 1; first, last >= 0
+ *   keep         >= first + last and >= 1; first, last >= 0; keep and width at most 2^31 - 1025
  *   kept         (device) [B][Hkv][keep] int32;  kept_lens (device) [B] int32
  *   new_weights  (device, nullable: not written) [num_rows][Hkv][width] fp32; may be
  *                weights itself */

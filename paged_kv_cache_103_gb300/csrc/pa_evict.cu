@@ -372,7 +372,8 @@ PA_API pa_status pa_select_tokens(const float* weights, int32_t num_rows, int32_
     if (B < 0 || Hkv <= 0 || num_rows <= 0 || width <= 0 || keep < 1 || first < 0 || last < 0 ||
         (int64_t)first + last > keep)
         return PA_ERR_INVALID;
-    if (B > 4096) return PA_ERR_UNSUPPORTED;
+    // The threads walk a row up to 1024 places at a time, in 32 bits.
+    if (B > 4096 || width > INT32_MAX - 1024 || keep > INT32_MAX - 1024) return PA_ERR_UNSUPPORTED;
     if (B == 0) return PA_OK;
     if (!weights || !rows || !context_lens || !kept || !kept_lens) return PA_ERR_INVALID;
     if (!aligned(weights, 4) || !aligned(rows, 4) || !aligned(context_lens, 4) || !aligned(kept, 4) ||
