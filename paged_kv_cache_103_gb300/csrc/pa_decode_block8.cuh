@@ -753,6 +753,8 @@ pa_status decode(const void* q, const void* k_cache, const void* v_cache, const 
     if ((int64_t)num_blocks * Hkv > INT32_MAX || B > kMaxBatch ||
         (int64_t)num_blocks * block_size > INT32_MAX || (int64_t)max_blocks * block_size > INT32_MAX)
         return PA_ERR_UNSUPPORTED;
+    // A block's codes over all KV heads are counted in 32 bits.
+    if ((int64_t)Hkv * d * block_size > UINT32_MAX) return PA_ERR_UNSUPPORTED;
     // Positions in the list are int32.
     const int64_t max_chunks = ((int64_t)max_blocks * block_size + kChunk - 1) / kChunk;
     if ((int64_t)B * Hkv * subs * (max_chunks + kPairCost) >= ((int64_t)1 << 30)) return PA_ERR_UNSUPPORTED;

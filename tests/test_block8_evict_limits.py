@@ -21,3 +21,10 @@ def lib():
 def test_select_tokens_rows_that_a_step_of_its_loops_takes_past_32_bits(lib, W, keep):
     """A CTA's threads walk a row 1024 places at a time, in 32 bits."""
     assert lib.pa_select_tokens(P, 1, W, P, P, 1, 1, keep, 0, 0, P, P, P, None) == UNSUPPORTED
+
+
+@pytest.mark.parametrize("fmt,Hkv", [("int8_block", 1 << 20), ("fp8_block", 1 << 22), ("int4", 1 << 21)])
+def test_decode_blocks_of_4_gib(lib, fmt, Hkv):
+    """A block's bytes over all KV heads, by which a block is found, are counted in 32 bits."""
+    assert getattr(lib, "pa_decode_" + fmt)(P, P, P, P, P, P, 1, P, 8, 1, Hkv, Hkv, 128, 32, 2, 0.1, 0, P, P, 1 << 40,
+                                            None) == UNSUPPORTED
