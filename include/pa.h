@@ -628,7 +628,8 @@ PA_API pa_status pa_decode_int8(const void* q, const void* k_cache, const void* 
  *   q, out           (device) 16-byte aligned
  *   k_cache, v_cache (device) [num_blocks][Hkv][block_size][d / 2] uint8, 16-byte aligned
  *   k_scale, v_scale (device) [num_blocks][Hkv][block_size][d / 64][2] f16,
- *                    16-byte aligned */
+ *                    16-byte aligned
+ *   Hkv * block_size * d / 2 must be below 2^32 (PA_ERR_UNSUPPORTED) */
 PA_API pa_status pa_decode_int4(const void* q, const void* k_cache, const void* v_cache,
                                 const void* k_scale, const void* v_scale,
                                 const int32_t* block_tables, int32_t max_blocks,
@@ -648,7 +649,8 @@ PA_API pa_status pa_decode_int4(const void* q, const void* k_cache, const void* 
  * 16-byte aligned) and the errors are those of pa_decode.
  *   q, out           (device) 16-byte aligned
  *   k_cache, v_cache (device) [num_blocks][Hkv][block_size][d] uint8, 16-byte aligned
- *   k_scale, v_scale (device) [num_blocks][Hkv] fp32 */
+ *   k_scale, v_scale (device) [num_blocks][Hkv] fp32
+ *   Hkv * block_size * d must be below 2^32 (PA_ERR_UNSUPPORTED) */
 PA_API pa_status pa_decode_int8_block(const void* q, const void* k_cache, const void* v_cache,
                                       const float* k_scale, const float* v_scale,
                                       const int32_t* block_tables, int32_t max_blocks,

@@ -21,7 +21,8 @@
 // a value, 68 % of them taken) in a launch that is over before either is full; in a decode step
 // a chain of dependent loads (slots, rows and scale, earlier codes where the scale grows).
 // Measured at d = 128 (device time): 8192 x 8 rows, bf16, E4M3 15.1 us (50 MB: 3.3 TB/s), 32768 x 8
-// rows INT8 44.5 (201 MB: 4.5 TB/s), 64 x 40 rows of as many blocks, f16, INT8 5.3, one token 2.6.
+// rows INT8 44.5 (201 MB: 4.5 TB/s), 64 x 40 rows of as many blocks, f16, INT8 5.3 (15.3 where every scale
+// grows and the blocks' other 15 rows are coded again), one token 2.6.
 // Rows that are neighbours in the call and in the block, as they nearly always are, have places
 // by addition, and the divisions that an odd scale needs are out of the way of the others: with each
 // row's place from its bit and both ways to a code in every step it was 16.2, 53.0, 6.5 and 3.1.

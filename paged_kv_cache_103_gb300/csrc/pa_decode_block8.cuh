@@ -30,7 +30,7 @@
 // 171 (6.3 TB/s, 94 % of the measured copy; DRAM traffic 1.003 times the bytes, 45 % of the
 // ALU's and 15 % of the tensor pipe's cycles, 40 % of the issue slots), G = 8 176, G = 16 185;
 // INT8: 172, 173, 174, 195; at d = 64 88 to 95 us up to G = 8; 64 sequences of 128 .. 2048 tokens,
-// 40 heads, G = 1: INT8 118 us, E4M3 116; 4 sequences of up to 64 tokens 6.4 us, all latency (6.6 with the next call launched at its end).
+// 40 heads, G = 1: INT8 118 us, E4M3 116; 4 sequences of up to 64 tokens 6.4 us, all latency.
 // The caches with a scale per token take 159 us (E4M3) and 175 (INT8) for a 40-head batch of
 // nearly this size: a conversion and a factor per key, and loading warps to wait for.
 #pragma once
