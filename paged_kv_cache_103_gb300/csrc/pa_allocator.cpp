@@ -475,15 +475,18 @@ PA_API pa_status pa_alloc_evict(pa_allocator* a, int64_t seq_id, int32_t num_tok
 PA_API pa_status pa_alloc_evict_batch(pa_allocator* a, const int64_t* seq_ids, const int32_t* num_tokens,
                                       int32_t B) {
     if (!a || B < 0 || (B > 0 && (!seq_ids || !num_tokens))) return PA_ERR_INVALID;
-    std::vector<Sequence*> batch((size_t)B);
-    std::unordered_set<int64_t> seen;
-    seen.reserve((size_t)B * 2);
-    for (int32_t i = 0; i < B; ++i) {
-        if (!seen.insert(seq_ids[i]).second) return PA_ERR_INVALID;
-        auto it = a->seqs.find(seq_ids[i]);
-        if (it == a->seqs.end()) return PA_ERR_NOT_FOUND;
-        if (it->second.swapped || num_tokens[i] < 0 || num_tokens[i] > it->second.length) return PA_ERR_INVALID;
-        batch[(size_t)i] = &it->second;
+    std::vector<Sequence*> batch;
+    try {
+        std::unordered_set<int64_t> seen;
+        for (int32_t i = 0; i < B; ++i) {
+            if (!seen.insert(seq_ids[i]).second) return PA_ERR_INVALID;
+            auto it = a->seqs.find(seq_ids[i]);
+            if (it == a->seqs.end()) return PA_ERR_NOT_FOUND;
+            if (it->second.swapped || num_tokens[i] < 0 || num_tokens[i] > it->second.length) return PA_ERR_INVALID;
+            batch.push_back(&it->second);
+        }
+    } catch (const std::bad_alloc&) {
+        return PA_ERR_OOM;
     }
     // In a run of their own nothing has been left yet; what the first of them leave, the last
     // holder of it counts here as one of several.
